@@ -27,7 +27,7 @@ _lib = ctypes.CDLL(_LIB_PATH)
 MAX_PTRS = 64
 MAX_DIMS = 3
 
-F32, F16, BF16 = 0, 1, 2
+F32, F16, BF16, F8E4M3 = 0, 1, 2, 3
 LOCAL, SLICED, REPLICATED = 0, 1, 2
 SCHED_RING, SCHED_UNROLL2, SCHED_BIDIRECTIONAL = 0, 1, 2
 
@@ -37,7 +37,7 @@ STATUS = {
     9: "COCO_ERR_TIMEOUT", 10: "COCO_ERR_VALUE",
 }
 
-_DTYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+_DTYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16, torch.float8_e4m3fn: F8E4M3}
 
 
 class CocoTensor(ctypes.Structure):
@@ -70,6 +70,7 @@ class CocoError(RuntimeError):
 
 _P = ctypes.POINTER(CocoTensor)
 _S = ctypes.c_void_p
+_A = ctypes.POINTER(ctypes.c_void_p)  # one device pointer per rank
 for _name, _args in {
     "coco_fused_allreduce": [_P, ctypes.c_void_p, _P, ctypes.c_float, ctypes.c_uint64, _P, _S],
     "coco_fused_allreduce_at": [_P, ctypes.c_void_p, _P, ctypes.c_float, ctypes.c_uint64, ctypes.c_uint64, _P, _S],
@@ -87,6 +88,12 @@ for _name, _args in {
     "coco_looped_ag_einsum_sched": [ctypes.c_char_p, _P, _P, _P, ctypes.c_int, _S],
     "coco_looped_einsum_rs_sched": [ctypes.c_char_p, _P, _P, _P, ctypes.c_int, _S],
     "coco_dropout_keep_mask": [ctypes.c_uint64, ctypes.c_float, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_void_p, _S],
+    "coco_allreduce_rmsnorm": [_P, _P, ctypes.c_void_p, ctypes.c_float, _P, _P, _A, ctypes.c_void_p, _S],
+    "coco_allreduce_rmsnorm_backward": [_P, _P, _P, ctypes.c_void_p, ctypes.c_void_p, _P, ctypes.c_void_p,
+                                        ctypes.c_void_p, ctypes.c_size_t, _S],
+    "coco_quantize_fp8": [_P, ctypes.c_int32, _P, _A, _S],
+    "coco_einsum_fp8": [ctypes.c_char_p, _P, _A, _P, _A, _P, _S],
+    "coco_grouped_einsum": [ctypes.c_char_p, _P, _A, _P, _A, ctypes.c_void_p, _P, _S],
     "coco_device_status": [_S],
     "coco_wait_selftest": [ctypes.c_uint64, _S],
 }.items():
@@ -101,6 +108,8 @@ _lib.coco_scattered_table_build.argtypes = [ctypes.c_int32, ctypes.POINTER(ctype
 _lib.coco_scattered_table_build.restype = ctypes.c_int
 _lib.coco_scattered_allreduce.argtypes = [ctypes.POINTER(CocoScatteredPlan), ctypes.c_float, _S]
 _lib.coco_scattered_allreduce.restype = ctypes.c_int
+_lib.coco_allreduce_rmsnorm_backward_bytes.argtypes = [ctypes.c_int64, ctypes.c_int64]
+_lib.coco_allreduce_rmsnorm_backward_bytes.restype = ctypes.c_size_t
 _lib.coco_status_string.argtypes = [ctypes.c_int]
 _lib.coco_status_string.restype = ctypes.c_char_p
 _lib.coco_last_cuda_error.restype = ctypes.c_int
@@ -125,6 +134,8 @@ EXPORTED = [
     "coco_scattered_table_bytes", "coco_scattered_table_build", "coco_scattered_allreduce",
     "coco_device_status", "coco_wait_selftest", "coco_kernel_launches", "coco_last_cuda_error", "coco_status_string", "coco_version",
     "coco_shard_order", "coco_loop_profitable", "coco_plan_cache_stats", "coco_plan_cache_clear",
+    "coco_allreduce_rmsnorm", "coco_allreduce_rmsnorm_backward", "coco_allreduce_rmsnorm_backward_bytes",
+    "coco_quantize_fp8", "coco_einsum_fp8", "coco_grouped_einsum",
 ]
 
 
@@ -275,6 +286,127 @@ def coco_looped_ag_einsum_sched(spec, lhs, rhs, out, schedule, stream=None):
 def coco_looped_einsum_rs_sched(spec, lhs, rhs, out, schedule, stream=None):
     _check(_lib.coco_looped_einsum_rs_sched(spec.encode(), _ref(lhs), _ref(rhs), _ref(out), int(schedule),
                                             _stream(stream)), "coco_looped_einsum_rs_sched")
+
+
+# -------------------------------------------- 8-bit and expert-grouped operators
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _scales(tensors, what):
+    """Per-rank scale tensors as an array of device pointers; their type and layout are checked here (the
+    library sees addresses only)."""
+    if tensors is None:
+        return None
+    for t in tensors:
+        if t.dtype != torch.float32 or not t.is_contiguous():
+            raise CocoError(3, what)
+    return (ctypes.c_void_p * len(tensors))(*[t.data_ptr() for t in tensors])
+
+
+def _need(ok, status, what):
+    if not ok:
+        raise CocoError(status, what)
+
+
+def _blocks(n):
+    return (n + 127) // 128
+
+
+def _check_scales(tensors, d, blocks, what):
+    """One scale tensor per pointer of ``d``, each of ``blocks`` values."""
+    if tensors is not None:
+        _need(len(tensors) == len(d.tensors), 2, what)
+        for t in tensors:
+            _need(t.numel() == blocks, 2, what)
+
+
+def coco_allreduce_rmsnorm(partials, residual, weight, eps, hidden, normed, scales, rstd, stream=None):
+    """h = sum of the ranks' partials + residual; normed = h / sqrt(mean(h^2) + eps) * weight over the last
+    dimension. ``hidden`` (the stored h), ``residual`` and ``rstd`` ([groups, rows] fp32) may be None;
+    ``normed`` holds the partials' type (``scales`` None) or float8_e4m3fn, with one fp32 scale tensor
+    [rows, ceil(cols / 128)] per normed pointer in ``scales``."""
+    what = "coco_allreduce_rmsnorm"
+    cols = partials.shape[-1]
+    rows = partials.tensors[0].numel() // cols if cols else 0
+    _need(weight.dtype == partials.tensors[0].dtype, 3, what)
+    _need(weight.numel() == cols and weight.is_contiguous(), 2, what)
+    _check_scales(scales, normed, rows * _blocks(cols), what)
+    if rstd is not None:
+        _need(rstd.dtype == torch.float32, 3, what)
+        _need(rstd.numel() == rows * partials.ngroups and rstd.is_contiguous(), 2, what)
+    _check(_lib.coco_allreduce_rmsnorm(_ref(partials), _ref(residual), _ptr(weight), float(eps), _ref(hidden),
+                                       _ref(normed), _scales(scales, what), _ptr(rstd), _stream(stream)), what)
+
+
+def coco_allreduce_rmsnorm_backward_bytes(rows, cols):
+    """Workspace bytes of coco_allreduce_rmsnorm_backward for ``rows`` rows (all groups together)."""
+    return int(_lib.coco_allreduce_rmsnorm_backward_bytes(int(rows), int(cols)))
+
+
+def coco_allreduce_rmsnorm_backward(dnormed, dhidden, hidden, weight, rstd, dx, dweight, workspace, stream=None):
+    """The gradient of coco_allreduce_rmsnorm: ``dnormed`` LOCAL (summed over the ranks here), ``dhidden`` the
+    residual stream's gradient or None; writes ``dx`` (of each partial and of the residual) and ``dweight``
+    (fp32). ``workspace``: a device tensor of coco_allreduce_rmsnorm_backward_bytes() bytes."""
+    what = "coco_allreduce_rmsnorm_backward"
+    cols = dnormed.shape[-1]
+    rows = dnormed.tensors[0].numel() // cols if cols else 0
+    _need(weight.dtype == dnormed.tensors[0].dtype and rstd.dtype == dweight.dtype == torch.float32, 3, what)
+    _need(weight.numel() == dweight.numel() == cols and rstd.numel() == rows * dnormed.ngroups and
+          weight.is_contiguous() and dweight.is_contiguous() and rstd.is_contiguous() and workspace.is_contiguous(),
+          2, what)
+    _check(_lib.coco_allreduce_rmsnorm_backward(
+        _ref(dnormed), _ref(dhidden), _ref(hidden), _ptr(weight), _ptr(rstd), _ref(dx), _ptr(dweight),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)), what)
+
+
+def coco_quantize_fp8(x, block_rows, q, scales, stream=None):
+    """Every rank's x as float8_e4m3fn values ``q`` and fp32 ``scales`` (one tensor per rank): one scale per row
+    and 128 columns (``block_rows`` 1) or per 128 x 128 tile of each matrix (128)."""
+    what = "coco_quantize_fp8"
+    shape = x.tensors[0].shape
+    if int(block_rows) in (1, 128) and len(shape) >= 1:
+        cols = shape[-1]
+        rows = x.tensors[0].numel() // cols if cols else 0
+        if block_rows == 128:
+            mats = shape[0] if len(shape) == 3 else 1
+            _check_scales(scales, q, mats * _blocks(rows // mats if mats else 0) * _blocks(cols), what)
+        else:
+            _check_scales(scales, q, rows * _blocks(cols), what)
+    _check(_lib.coco_quantize_fp8(_ref(x), int(block_rows), _ref(q), _scales(scales, what), _stream(stream)), what)
+
+
+def coco_einsum_fp8(spec, lhs, lhs_scales, rhs, rhs_scales, out, stream=None):
+    """out_r = lhs_r @ rhs_r on float8_e4m3fn operands with fp32 scales per 1 x 128 (lhs) and 128 x 128 (rhs)
+    block; ``spec`` "mk,kn->mn" or "mk,nk->mn". Scale tensors: one per pointer of the operand."""
+    what = "coco_einsum_fp8"
+    if len(lhs.tensors[0].shape) == 2 and len(rhs.tensors[0].shape) == 2:
+        m, k = lhs.tensors[0].shape
+        r, c = rhs.tensors[0].shape
+        _check_scales(lhs_scales, lhs, m * _blocks(k), what)
+        _check_scales(rhs_scales, rhs, _blocks(r) * _blocks(c), what)
+    _check(_lib.coco_einsum_fp8(spec.encode(), _ref(lhs), _scales(lhs_scales, what), _ref(rhs),
+                                _scales(rhs_scales, what), _ref(out), _stream(stream)), what)
+
+
+def coco_grouped_einsum(spec, lhs, lhs_scales, rhs, rhs_scales, offsets, out, stream=None):
+    """Products grouped by expert: rows [offsets[e], offsets[e + 1]) of lhs belong to expert e. ``spec``
+    "tk,ekn->tn", "tk,enk->tn" or the weight gradient "tk,tn->ekn"; ``offsets`` an int32 device tensor
+    [ranks, experts + 1]; scale lists for float8_e4m3fn operands, else None."""
+    what = "coco_grouped_einsum"
+    if len(lhs.tensors[0].shape) == 2 and len(rhs.tensors[0].shape) == 3:
+        t, k = lhs.tensors[0].shape
+        e, r, c = rhs.tensors[0].shape
+        _check_scales(lhs_scales, lhs, t * _blocks(k), what)
+        _check_scales(rhs_scales, rhs, e * _blocks(r) * _blocks(c), what)
+    if offsets is not None:
+        experts = (out if spec.replace(" ", "") == "tk,tn->ekn" else rhs).shape[0]
+        _need(offsets.dtype == torch.int32, 3, what)
+        _need(offsets.numel() == len(lhs.tensors) * (experts + 1) and offsets.is_contiguous(), 2, what)
+    _check(_lib.coco_grouped_einsum(spec.encode(), _ref(lhs), _scales(lhs_scales, what), _ref(rhs),
+                                    _scales(rhs_scales, what), _ptr(offsets), _ref(out), _stream(stream)), what)
 
 
 def coco_dropout_keep_mask(seed, dropout_p, first_index, count, mask, stream=None):

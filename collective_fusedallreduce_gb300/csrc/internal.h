@@ -11,7 +11,7 @@
 
 namespace coco {
 
-inline int dtype_size(int dt) { return dt == COCO_F32 ? 4 : 2; }
+inline int dtype_size(int dt) { return dt == COCO_F32 ? 4 : dt == COCO_F8E4M3 ? 1 : 2; }
 
 // ----------------------------------------------------------------- reductions
 
@@ -61,6 +61,66 @@ cudaError_t launch_scattered_allreduce(const void* table, int64_t nbuckets, int 
 
 cudaError_t launch_keep_mask(uint64_t seed, uint32_t threshold, uint64_t first, uint64_t count,
                              uint8_t* mask, cudaStream_t s);
+
+// ------------------------------------------------ norm, its gradient, quantiser
+
+// Pointer tables of one norm launch, group-major like ReduceTables: group g's distinct hidden outputs are
+// hidden[g*nranks + j], j < nhidden[g], its (normed, scales) pairs normed/scales[g*nranks + j], j < nnormed[g].
+struct NormTables {
+  const void* in[COCO_MAX_PTRS];
+  void* hidden[COCO_MAX_PTRS];
+  void* normed[COCO_MAX_PTRS];
+  float* scales[COCO_MAX_PTRS];
+  const void* residual[COCO_MAX_PTRS];  // per group, or nullptr
+  int32_t nhidden[COCO_MAX_PTRS], nnormed[COCO_MAX_PTRS];
+};
+
+constexpr int kNormMaxCols = 65536;  // a row stays in its block's registers
+
+struct NormLaunch {
+  NormTables t;
+  int dtype;
+  bool fp8;  // normed is e4m3 with scales
+  int nranks, ngroups;
+  int64_t rows;
+  int32_t cols;
+  float eps;
+  const void* weight;
+  float* rstd;  // [ngroups][rows], or nullptr
+};
+cudaError_t launch_allreduce_rmsnorm(const NormLaunch& L, cudaStream_t s);
+
+constexpr int64_t kNormMaxParts = 608;  // workspace rows of the weight's gradient, at least COCO_MAX_PTRS
+
+struct NormBwdLaunch {
+  const void* in[COCO_MAX_PTRS];
+  const void* dhidden[COCO_MAX_PTRS];  // per group, or nullptr
+  const void* hidden[COCO_MAX_PTRS];   // per group
+  void* dx[COCO_MAX_PTRS];             // group g's distinct outputs: dx[g*nranks + j], j < ndx[g]
+  int32_t ndx[COCO_MAX_PTRS];
+  int dtype;
+  int nranks, ngroups;
+  int64_t rows;
+  int32_t cols;
+  const void* weight;
+  const float* rstd;  // [ngroups][rows]
+  float* dweight;
+  float* partial;  // norm_backward_parts(ngroups * rows) rows of cols
+};
+int64_t norm_backward_parts(int64_t total_rows);
+cudaError_t launch_rmsnorm_backward(const NormBwdLaunch& L, cudaStream_t s);
+
+struct QuantLaunch {
+  const void* x[COCO_MAX_PTRS];
+  void* q[COCO_MAX_PTRS];
+  float* scales[COCO_MAX_PTRS];
+  int ntensors;
+  int dtype;
+  int block_rows;  // 1 or 128
+  int64_t rows;
+  int32_t cols;
+};
+cudaError_t launch_quantize_fp8(const QuantLaunch& L, cudaStream_t s);
 
 // ---------------------------------------------------------------- GEMM plans
 
@@ -145,6 +205,30 @@ cudaError_t tc_launch(TcPrepared* prep, cudaStream_t s, unsigned int* err_word);
 void tc_free(TcPrepared* prep);
 // fp32 path (FMA units).
 cudaError_t launch_gemm_simt(const GemmPlan& plan, cudaStream_t s);
+
+// ------------------------------------------- block-scaled and expert-grouped products
+
+// GRP_KN: rows of expert e times rhs[e] stored [k][n]; GRP_NK: rhs[e] stored [n][k]; GRP_GRAD: the weight
+// gradient, lhs^T rhs over the rows of expert e, stored out[e][k][n].
+enum GroupedForm { GRP_KN = 0, GRP_NK = 1, GRP_GRAD = 2 };
+
+// `nprob` independent problems (one per rank and group) of one shape. Problem p's expert e owns the rows
+// [offsets[p*(experts+1) + e], offsets[p*(experts+1) + e + 1]) of lhs and out (of lhs and rhs for GRP_GRAD);
+// without offsets there is one expert that owns all rows.
+struct GroupedLaunch {
+  const void* lhs[COCO_MAX_PTRS];
+  const void* rhs[COCO_MAX_PTRS];
+  const float* lhs_scales[COCO_MAX_PTRS];  // e4m3 operands only: [rows][ceil(k/128)]
+  const float* rhs_scales[COCO_MAX_PTRS];  // [experts][ceil(k/128)][ceil(n/128)] (GRP_NK: n and k exchanged)
+  void* out[COCO_MAX_PTRS];
+  const int32_t* offsets;  // device memory, or nullptr
+  int nprob, experts;
+  int form;
+  int in_dtype, out_dtype;
+  int32_t rows, k, n;
+};
+constexpr int kGroupedMaxExperts = 65536;
+cudaError_t launch_grouped(const GroupedLaunch& L, cudaStream_t s, unsigned int* err_word);
 
 // Device error word of the GEMM kernels (bounded waits record here).
 unsigned int* gemm_error_word();

@@ -88,7 +88,10 @@ typedef enum {
   COCO_ERR_VALUE = 10       /* a scalar argument is out of range (e.g. dropout p) */
 } coco_status;
 
-typedef enum { COCO_F32 = 0, COCO_F16 = 1, COCO_BF16 = 2 } coco_dtype;
+/* COCO_F8E4M3 (4 exponent bits, 3 fraction bits, largest value 448, no infinity) is taken by the entry points
+ * of the section on 8-bit and expert-grouped operators only; its innermost per-rank dimension is a multiple
+ * of 16 elements. Elsewhere it is COCO_ERR_DTYPE. */
+typedef enum { COCO_F32 = 0, COCO_F16 = 1, COCO_BF16 = 2, COCO_F8E4M3 = 3 } coco_dtype;
 
 typedef enum { COCO_LOCAL = 0, COCO_SLICED = 1, COCO_REPLICATED = 2 } coco_layout;
 
@@ -414,6 +417,124 @@ coco_status coco_shard_order(int32_t kind, int32_t schedule, int32_t rank, int32
  */
 coco_status coco_loop_profitable(double orig_comp, double orig_comm, double ring_comm, double epilogue_cost,
                                  int32_t* profitable);
+
+/* ------------------------------- 8-bit and expert-grouped operators */
+
+/*
+ * The operators around a tensor-parallel layer of a large language model whose
+ * products run in 8 bits: the norm that follows the layer's AllReduce, the
+ * quantiser, the block-scaled product, and the products of a mixture of
+ * experts. None has a counterpart on the pages; they take their tensors,
+ * layouts and error codes from the conventions above.
+ *
+ * e4m3 values and scales. A value x of an 8-bit tensor is stored as
+ * q = round(x / s) (to nearest even) with one fp32 scale s per block of 128
+ * columns of one row (activations) or of 128 rows (weights), the last block of
+ * a dimension being shorter where it does not divide by 128; x is q * s. A scale
+ * is max(amax, 2^-100) / 448 with amax the block's largest magnitude: a block of
+ * zeros has zeros, and a block that holds a NaN or an infinity has that in its
+ * scale, so it cannot pass for numbers. Scale arrays are dense fp32, row-major
+ * over the blocks ([rows, ceil(cols/128)] or [ceil(rows/128), ceil(cols/128)]),
+ * and passed as host arrays of device pointers, group-major like coco_tensor's.
+ * Scales, rstd, dweight and offsets need the alignment of their 4-byte elements
+ * only.
+ */
+
+/*
+ * AllReduce, the residual's addition and the root-mean-square norm (Zhang and
+ * Sennrich 2019) in one pass:
+ *
+ *   h = sum_{r=0}^{N-1} partials_r + residual,   y = h / sqrt(mean(h^2) + eps) * weight
+ *
+ * over the last dimension, with the sum (rank order), the statistics and the
+ * product in fp32 from the unrounded h. Each row is read once.
+ *
+ *   partials  LOCAL, dtype T in {F32, F16, BF16}; the last dimension (the row) at most 65536, else
+ *             COCO_ERR_UNSUPPORTED.
+ *   residual  REPLICATED, T, the same shape, or NULL.
+ *   weight    device pointer to one row of T.
+ *   eps       finite and >= 0, else COCO_ERR_VALUE.
+ *   hidden    REPLICATED, T: receives h (the next residual, and what the backward reads), or NULL.
+ *   normed    REPLICATED: T, or F8E4M3 with one scale per row and 128 columns.
+ *   scales    F8E4M3 only (else NULL): ngroups * nranks device pointers, each to the scales of the normed
+ *             replica at the same place.
+ *   rstd      device pointer to [ngroups, rows] fp32: receives 1 / sqrt(mean(h^2) + eps), or NULL.
+ *
+ * hidden, and normed of type T, may take an input's place exactly. Other overlaps are COCO_ERR_ALIAS.
+ */
+coco_status coco_allreduce_rmsnorm(const coco_tensor* partials, const coco_tensor* residual, const void* weight,
+                                   float eps, const coco_tensor* hidden, const coco_tensor* normed,
+                                   float* const* scales, float* rstd, void* stream);
+
+/*
+ * The gradient of coco_allreduce_rmsnorm. The norm's output feeds every rank's
+ * column-parallel product, so its gradient arrives as one partial per rank and
+ * is summed here (the AllReduce of the backward pass); the gradient with
+ * respect to h is that of each partial and of the residual alike:
+ *
+ *   dy = sum_r dnormed_r,  xhat = hidden * rstd,  g = dy * weight
+ *   dx = rstd * (g - xhat * mean(g * xhat)) + dhidden
+ *   dweight = sum over all rows (of all groups) of dy * xhat
+ *
+ * A norm stored in 8 bits passes its gradient through unchanged.
+ *   dnormed   LOCAL, T.            dhidden  REPLICATED, T (the residual stream's gradient), or NULL.
+ *   hidden    REPLICATED, T, as the forward wrote it.   rstd  [ngroups, rows] fp32, as the forward wrote it.
+ *   dx        REPLICATED, T; may take the place of dnormed_r, dhidden or hidden exactly.
+ *   dweight   device pointer to one row of fp32.
+ *   workspace device memory of at least coco_allreduce_rmsnorm_backward_bytes(ngroups * rows, cols) bytes
+ *             (fewer: COCO_ERR_SHAPE), 16-byte aligned; its contents before and after do not matter.
+ * All sums are fp32 in a fixed order: repeated calls on one device give the same bits.
+ */
+coco_status coco_allreduce_rmsnorm_backward(const coco_tensor* dnormed, const coco_tensor* dhidden,
+                                            const coco_tensor* hidden, const void* weight, const float* rstd,
+                                            const coco_tensor* dx, float* dweight, void* workspace,
+                                            size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace for `rows` rows in all groups together (0 for sizes out of range). Host only. */
+size_t coco_allreduce_rmsnorm_backward_bytes(int64_t rows, int64_t cols);
+
+/*
+ * Every rank's x in e4m3 with scales: block_rows = 1 takes one scale per row and 128 columns (activations;
+ * all leading dimensions are rows), block_rows = 128 one per 128 rows and 128 columns (weights; a 3-D tensor
+ * is a stack of matrices). x LOCAL in F32, F16 or BF16; q LOCAL in F8E4M3, the same shape; scales: one device
+ * pointer per rank. Other values of block_rows: COCO_ERR_VALUE. No output may overlap another array.
+ */
+coco_status coco_quantize_fp8(const coco_tensor* x, int32_t block_rows, const coco_tensor* q, float* const* scales,
+                              void* stream);
+
+/*
+ * The MatMul of every rank on 8-bit operands: out_r = lhs_r @ rhs_r with
+ *
+ *   out[m, n] = sum over blocks b of 128 k of lhs_scale[m, b] * rhs_scale[b, n / 128] * sum_{k in b} lhs[m, k] rhs[k, n]
+ *
+ * Specs: "mk,kn->mn" (rhs [k, n], scales [ceil(k/128), ceil(n/128)]) and "mk,nk->mn" (rhs [n, k], scales
+ * [ceil(n/128), ceil(k/128)]: the product with the transpose, which is the first one's input gradient with the
+ * same stored weight). lhs F8E4M3, scales [m, ceil(k/128)]; LOCAL, REPLICATED (read from rank 0's pointer) or
+ * SLICED on k. rhs F8E4M3; LOCAL, REPLICATED or SLICED on k. out LOCAL in F32, F16 or BF16, rounded once from the fp32 sum of the
+ * blocks. Scale pointers per rank as for the tensors. No output may overlap another array.
+ */
+coco_status coco_einsum_fp8(const char* spec, const coco_tensor* lhs, const float* const* lhs_scales,
+                            const coco_tensor* rhs, const float* const* rhs_scales, const coco_tensor* out,
+                            void* stream);
+
+/*
+ * Products grouped by expert with ragged sizes. The rows of lhs are sorted by expert: expert e owns rows
+ * [offsets[e], offsets[e+1]). `offsets` is in device memory ([nranks * ngroups, experts + 1] int32, one line
+ * per rank): the routing need not come back to the host. Specs:
+ *   "tk,ekn->tn"  out[t] = lhs[t] @ rhs[e(t)]                (forward)
+ *   "tk,enk->tn"  out[t] = lhs[t] @ rhs[e(t)]^T              (input gradient, or weights stored [n, k])
+ *   "tk,tn->ekn"  out[e] = sum over e's rows t of lhs[t]^T rhs[t]   (weight gradient; zeros for an expert without rows)
+ * lhs and rhs both F16, both BF16 (fp32 accumulation; scales NULL), or, for the first two, both F8E4M3 with lhs
+ * scales [t, ceil(k/128)] and rhs scales [e, ceil(k/128), ceil(n/128)] ("enk": [e, ceil(n/128), ceil(k/128)]);
+ * F32 operands, and F8E4M3 for the weight gradient, are COCO_ERR_UNSUPPORTED. lhs and rhs LOCAL or REPLICATED, out
+ * LOCAL in F32, F16 or BF16. At most 65536 experts.
+ * Rows before offsets[0] or from offsets[experts] on belong to no expert: their output is zero, and they do not
+ * enter a gradient, whatever they hold. Offsets are read as if clamped to [0, t] and never descending between
+ * neighbours; where they descend, the values are unspecified, but no access leaves the arrays.
+ */
+coco_status coco_grouped_einsum(const char* spec, const coco_tensor* lhs, const float* const* lhs_scales,
+                                const coco_tensor* rhs, const float* const* rhs_scales, const int32_t* offsets,
+                                const coco_tensor* out, void* stream);
 
 /* ------------------------------------------------------------- utilities */
 

@@ -25,7 +25,8 @@ Sources, cited by title and section throughout:
 Every function states the passage it follows. Where the pages are silent the
 docstring says which reading was taken and why.
 
-Pins: each public function is checked in ``tests/test_oracle_pins.py`` against
+Pins: each public function is checked in ``tests/test_oracle_pins.py`` (the
+8-bit and expert-grouped ones in ``tests/test_oracle_llm_pins.py``) against
 facts the pages or mathematics fix (brute force, closed forms, identities the
 pages state, published hash test vectors). No function here is unpinned.
 """
@@ -56,6 +57,18 @@ from .fused import (
     dropout_scale,
     fused_allreduce,
 )
+from .llm import (
+    e4m3_table,
+    to_e4m3,
+    block_amax,
+    scales_of,
+    spread,
+    quantize,
+    dequantize,
+    allreduce_rmsnorm,
+    allreduce_rmsnorm_backward,
+    grouped_einsum,
+)
 from .scattered import (
     buckets as scattered_buckets,
     metadata_bytes as scattered_metadata_bytes,
@@ -84,4 +97,6 @@ __all__ = [
     "megatron_attention_tail",
     "scattered_buckets", "scattered_metadata_bytes", "scattered_allreduce", "scattered_allreduce_by_buckets",
     "loop_profitable",
+    "e4m3_table", "to_e4m3", "block_amax", "scales_of", "spread", "quantize", "dequantize",
+    "allreduce_rmsnorm", "allreduce_rmsnorm_backward", "grouped_einsum",
 ]
