@@ -1,114 +1,737 @@
-// Products of e4m3 operands with block scales, and products grouped by expert.
-// One 64 x 64 output tile per block step, operands staged element by element.
+// Products of e4m3 operands with block scales, and products grouped by expert
+// with ragged sizes, on the sm_103a tensor cores (tcgen05 + TMEM + TMA).
+//
+// Block scales. With one scale per row and 128 k of lhs and per 128 k x 128 n
+// of rhs,
+//   out[m, n] = sum_b sa[m, b] sb[b, n / 128] P_b[m, n],   P_b = the plain e4m3 product over block b.
+// P_b is one k-block of tensor-core work; it is read back from TMEM and added
+// to the fp32 sum in registers with one fused multiply-add per element, while
+// the next block's product is under way in the other TMEM buffer.
+//
+// Ragged groups. Where each expert's rows begin is known on the device only.
+// Work units are numbered expert by expert, and every warp finds its unit by
+// itself: 32 lanes read 32 experts' offsets, a prefix sum over their tile counts
+// and a ballot give the expert, so neither a table nor a launch per expert is
+// needed and empty experts cost one lane of one read.
+//
+// k_grouped_pair (many rows): CTA pairs, persistent, one 256 x 256 output tile
+// per pair and step (tcgen05 cta_group::2: M = 256, N = 256; each CTA holds 128
+// rows of A, 128 columns of B and its 128 rows of the accumulator).
+//   warp 0        TMA producer: k-blocks 128 bytes deep into a ring of 6 stages of 32 KB.
+//   warp 1        issues the MMAs (CTA 0 of the pair) and owns TMEM.
+//   warp 2        in weight gradients: clears what a k-block holds of the next expert's rows.
+//   warps 4..11   two per TMEM lane quarter, 128 columns each: sum of the scaled blocks, conversion, stores.
+// Every mbarrier wait is bounded by %globaltimer as in the other tensor-core
+// kernels: on expiry COCO_ERR_TIMEOUT is recorded, the roles drain and return.
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
+
+#include <atomic>
 
 #include "internal.h"
+#include "tc_ptx.h"
 
 namespace coco {
 namespace {
 
-constexpr int TM = 64, TN = 64, TK = 16;
+constexpr int BKB = 128;  // bytes of k per k-block: 128 e4m3 or 64 16-bit values
+constexpr int TILE_M = 256, TILE_N = 256;
+constexpr int A_BYTES = 128 * BKB, B_BYTES = 128 * BKB;  // one CTA's rows of A / columns of B
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int STAGES = 6;
+constexpr int EPI_WARPS = 8, FIRST_EPI_WARP = 4;
+constexpr int THREADS = 32 * (FIRST_EPI_WARP + EPI_WARPS);
+constexpr int STRIP = 32 * 128;  // an epilogue warp's staging: 32 rows x 128 bytes
+constexpr int STRIP_OFF = STAGES * STAGE_BYTES;
+constexpr int BAR_OFF = STRIP_OFF + EPI_WARPS * STRIP;
+// full, empty and cleared per stage, accumulator full x2, empty x2, drain
+constexpr int NUM_BARS = 3 * STAGES + 5;
+constexpr int SMEM_BYTES = BAR_OFF + 8 * NUM_BARS + 16 + 1024;  // + alignment slack
+static_assert(SMEM_BYTES <= 232448, "shared memory over the per-CTA limit");
+constexpr uint32_t TMEM_COLS = 512;
+constexpr int GROUP_MT = 8;  // rasterisation: m-tiles per group, n-major inside a group
 
-__device__ float value(const void* p, int64_t i, int dtype) {
-  if (dtype == COCO_F16) return __half2float(static_cast<const __half*>(p)[i]);
-  if (dtype == COCO_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-  __nv_fp8_e4m3 v = static_cast<const __nv_fp8_e4m3*>(p)[i];
-  return static_cast<float>(v);
-}
-__device__ void put(void* p, int64_t i, int dtype, float v) {
-  if (dtype == COCO_F32) static_cast<float*>(p)[i] = v;
-  else if (dtype == COCO_F16) static_cast<__half*>(p)[i] = __float2half_rn(v);
-  else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-}
+struct GroupedParams {
+  CUtensorMap a[COCO_MAX_PTRS], b[COCO_MAX_PTRS];
+  void* out[COCO_MAX_PTRS];
+  const float* sa[COCO_MAX_PTRS];
+  const float* sb[COCO_MAX_PTRS];
+  const int32_t* offsets;
+  unsigned int* err;
+  int32_t nprob, experts, form, out_dtype;
+  int32_t rows, k, n;
+  int32_t kblocks;     // of the k dimension (weight gradients: each expert's rows give their own)
+  int32_t bk;          // elements of a k-block
+  int32_t kscales, nscales;
+  uint32_t idesc;
+  uint32_t bstep;      // B's descriptor advance per MMA, in 16-byte units
+  uint32_t blead;      // B's leading byte offset >> 4
+};
+static_assert(sizeof(GroupedParams) <= 32000, "kernel parameter block too large");
 
-// Grid: x = n tiles, y = m tiles of the largest possible expert, z = problem * experts + expert.
-__global__ void __launch_bounds__(256) k_grouped_simple(const __grid_constant__ GroupedLaunch L) {
-  __shared__ float As[TK][TM + 4], Bs[TK][TN + 4];
-  const int p = blockIdx.z / L.experts, e = blockIdx.z % L.experts;
-  int r0 = 0, r1 = L.rows;
-  if (L.offsets) {
-    const int32_t* off = L.offsets + static_cast<int64_t>(p) * (L.experts + 1) + e;
-    r0 = min(max(off[0], 0), L.rows);
-    r1 = min(max(off[1], r0), L.rows);
-  }
-  const bool grad = L.form == GRP_GRAD, fp8 = L.in_dtype == COCO_F8E4M3;
-  const int M = grad ? L.k : r1 - r0, K = grad ? r1 - r0 : L.k, N = L.n;
-  const int kb = (L.k + 127) / 128, nb = (L.n + 127) / 128;
-  const int m0 = blockIdx.y * TM, n0 = blockIdx.x * TN;
-  if (m0 >= M) return;
-  float acc[4][4] = {};
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  for (int k0 = 0; k0 < K; k0 += TK) {
-    for (int i = threadIdx.x; i < TM * TK; i += 256) {
-      const int kk = i % TK, mm = i / TK, k = k0 + kk, m = m0 + mm;
-      float v = 0.0f;
-      if (k < K && m < M) {
-        if (grad) v = value(L.lhs[p], static_cast<int64_t>(r0 + k) * L.k + m, L.in_dtype);
-        else v = value(L.lhs[p], static_cast<int64_t>(r0 + m) * L.k + k, L.in_dtype);
-        if (fp8) v *= L.lhs_scales[p][static_cast<int64_t>(r0 + m) * kb + k / 128];
-      }
-      As[kk][mm] = v;
+// ------------------------------------------------------------- work units
+
+struct Tile {
+  int p, e;    // problem and expert
+  int r0, r1;  // the expert's rows
+  int m0, n0;  // the tile's first row (of the expert; weight gradients: first row of k) and column
+};
+
+// A warp's view of 32 consecutive (problem, expert) pairs: lane l holds pair base + l.
+struct Walk {
+  int base;
+  int r0, r1, tiles;
+  int upto;  // units of all pairs up to and including this lane's
+};
+
+template <bool GRAD>
+__device__ __forceinline__ void walk_load(const GroupedParams& P, Walk& w, int base, int before, int tm, int tn) {
+  const int lane = threadIdx.x & 31;
+  w.base = base;
+  w.r0 = w.r1 = w.tiles = 0;
+  const int pe = base + lane;
+  if (pe < P.nprob * P.experts) {
+    w.r1 = P.rows;
+    if (P.offsets) {
+      const int p = pe / P.experts;
+      const int32_t* o = P.offsets + pe + p;  // (each problem has experts + 1 offsets)
+      w.r0 = min(max(__ldg(o), 0), P.rows);
+      w.r1 = min(max(__ldg(o + 1), w.r0), P.rows);
     }
-    for (int i = threadIdx.x; i < TN * TK; i += 256) {
-      const int nn = i % TN, kk = i / TN, k = k0 + kk, n = n0 + nn;
-      float v = 0.0f;
-      if (k < K && n < N) {
-        const int64_t eo = static_cast<int64_t>(e) * L.k * L.n;
-        if (grad) v = value(L.rhs[p], static_cast<int64_t>(r0 + k) * L.n + n, L.in_dtype);
-        else if (L.form == GRP_KN) v = value(L.rhs[p], eo + static_cast<int64_t>(k) * L.n + n, L.in_dtype);
-        else v = value(L.rhs[p], eo + static_cast<int64_t>(n) * L.k + k, L.in_dtype);
-        if (fp8) {
-          const int64_t so = static_cast<int64_t>(e) * kb * nb;
-          v *= L.rhs_scales[p][so + (L.form == GRP_KN ? (k / 128) * nb + n / 128 : (n / 128) * kb + k / 128)];
+    const int m = GRAD ? P.k : w.r1 - w.r0;
+    w.tiles = ((m + tm - 1) / tm) * ((P.n + tn - 1) / tn);
+  }
+  int s = w.tiles;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, s, d);
+    if (lane >= d) s += v;
+  }
+  w.upto = before + s;
+}
+
+// The tile of unit u (ascending from call to call), or false past the last one. The whole warp calls it.
+template <bool GRAD>
+__device__ __forceinline__ bool walk_find(const GroupedParams& P, Walk& w, int u, Tile& t, int tm, int tn) {
+  for (;;) {
+    const int last = __shfl_sync(0xffffffffu, w.upto, 31);
+    if (u < last) break;
+    if (w.base + 32 >= P.nprob * P.experts) return false;
+    walk_load<GRAD>(P, w, w.base + 32, last, tm, tn);
+  }
+  const int f = __ffs(__ballot_sync(0xffffffffu, u < w.upto)) - 1;
+  const int pe = w.base + f;
+  t.p = pe / P.experts;
+  t.e = pe - t.p * P.experts;
+  t.r0 = __shfl_sync(0xffffffffu, w.r0, f);
+  t.r1 = __shfl_sync(0xffffffffu, w.r1, f);
+  const int local = u - (__shfl_sync(0xffffffffu, w.upto, f) - __shfl_sync(0xffffffffu, w.tiles, f));
+  const int mts = ((GRAD ? P.k : t.r1 - t.r0) + tm - 1) / tm, nts = (P.n + tn - 1) / tn;
+  const int group = local / (GROUP_MT * nts);
+  const int gm = min(GROUP_MT, mts - group * GROUP_MT);
+  const int in_g = local - group * GROUP_MT * nts;
+  const int nt = in_g / gm;
+  t.m0 = (group * GROUP_MT + in_g - nt * gm) * tm;
+  t.n0 = nt * tn;
+  return true;
+}
+
+// ------------------------------------------------------------ PTX (this file)
+
+// D (+)= A B over the pair, e4m3 operands (kind::f8f6f4, K = 32) or 16-bit ones (kind::f16, K = 16).
+template <bool E4M3>
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (E4M3)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    umma_pair(d, a, b, idesc, accumulate);
+}
+
+// The bounded waits of tc_ptx.h without a function call: ptxas cannot split registers between warps
+// (setmaxnreg) in a kernel that makes one.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_test(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_test(bar, parity)) return true;
+    if ((it & 31) == 0 && (*abort_flag || globaltimer() - t0 > kTimeoutNs)) return false;
+  }
+}
+__device__ __forceinline__ bool wait_bar_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = wait_bar(bar, parity, abort_flag);
+  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+
+// A descriptor of operand tiles in 128-byte swizzled rows (tcgen05 matrix descriptor: start address >> 4,
+// leading byte offset >> 4 at bit 16, stride byte offset >> 4 at bit 32, version 1, 128-byte swizzle): groups
+// of 8 rows are 1024 bytes apart; `lead` is the distance of 128-byte wide boxes of operands whose rows run
+// along k (unused for operands whose rows hold 128 bytes of k).
+__device__ __forceinline__ uint64_t tile_desc(uint32_t saddr, uint32_t lead) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFF) | (static_cast<uint64_t>(lead) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// Waits for this thread's TMEM loads; the registers pass through, so no use of them can move ahead of it.
+__device__ __forceinline__ void tmem_wait_for(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_for(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// A wait that also sees what the other CTA of the pair wrote before its arrival.
+__device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
+// ---------------------------------------------------------------- epilogue
+
+// Writes 32 rows x 128 bytes held one row per lane: through shared memory, so that each store instruction
+// covers four whole 128-byte lines, and bounded by rows and bytes, so that a tile may end anywhere.
+__device__ __forceinline__ void store_strip(uint32_t strip, const uint32_t (&p)[32], char* out, int64_t pitch,
+                                            int rows, int64_t bytes) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    st_shared_v4(strip + lane * 128 + ((c ^ (lane & 7)) << 4), p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
+  __syncwarp();
+  const int ch = lane & 7;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = i * 4 + (lane >> 3);
+    const uint4 v = ld_shared_v4(strip + row * 128 + ((ch ^ (row & 7)) << 4));
+    if (row < rows && ch * 16 < bytes) *reinterpret_cast<uint4*>(out + row * pitch + ch * 16) = v;
+  }
+  __syncwarp();
+}
+
+// Rows of no expert are zero. Every thread of `nthreads` takes its share.
+__device__ __forceinline__ void clear_rest(const GroupedParams& P, int64_t thread, int64_t nthreads) {
+  const int64_t pitch = static_cast<int64_t>(P.n) * (P.out_dtype == COCO_F32 ? 4 : 2) / 16;
+  for (int p = 0; p < P.nprob; ++p) {
+    const int32_t* o = P.offsets + static_cast<int64_t>(p) * (P.experts + 1);
+    const int64_t head = min(max(__ldg(o), 0), P.rows);
+    const int64_t tail = max(min(max(__ldg(o + P.experts), 0), P.rows), static_cast<int>(head));
+    const int64_t total = (head + P.rows - tail) * pitch;
+    uint4* out = static_cast<uint4*>(P.out[p]);
+    for (int64_t i = thread; i < total; i += nthreads)
+      out[i < head * pitch ? i : i + (tail - head) * pitch] = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+// ------------------------------------------------------------ pair kernel
+
+template <bool SCALED, bool GRAD>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    k_grouped_pair(const __grid_constant__ GroupedParams P) {
+  static_assert(!(SCALED && GRAD), "weight gradients have 16-bit operands");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + BAR_OFF;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+  auto clear_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };  // weight gradients: an expert's last block
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (3 * STAGES + a); };
+  auto tempty_bar = [&](int a) { return bar0 + 8u * (3 * STAGES + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (3 * STAGES + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + BAR_OFF + 8 * NUM_BARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + BAR_OFF + 8 * NUM_BARS + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int cluster_id = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+  constexpr uint16_t kPair = 0x3;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      // CTA 0's is the pair's: its own producer's arrival, and in weight gradients one of each CTA (the producer's,
+      // or for an expert's last block that of the warp that cleared it)
+      mbar_init(full_bar(s), GRAD ? 2 : 1);
+      mbar_init(empty_bar(s), 1);
+      mbar_init(clear_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), 2 * EPI_WARPS);  // CTA 0's: the epilogue warps of both CTAs
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc<true>(smem_u32(tmem_slot), TMEM_COLS);
+  tc_fence_before();
+  cluster_sync();  // the peer's barriers exist before the pair's copies or commits reach them
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  auto fail = [&]() {
+    *abort_flag = 1;
+    atomicCAS(P.err, 0u, static_cast<unsigned int>(COCO_ERR_TIMEOUT));
+  };
+  int dummy = 0;
+  volatile int* never = &dummy;
+
+  // Registers: an epilogue thread holds 128 sums. The launch's 384 threads have 168 each; the four warps in
+  // front give up what the eight epilogue warps take (128 x 56 + 256 x 224 = 384 x 168).
+  if (warp < FIRST_EPI_WARP) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0) {
+      // ------------------------------------------------------ TMA producer
+      const bool leader = elect_one();
+      Walk w;
+      walk_load<GRAD>(P, w, 0, 0, TILE_M, TILE_N);
+      Tile t;
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t issued = 0, parity = 0, own = 0, clear_parity = 0;  // per stage; own: the copies complete clear_bar
+      bool ok = true;
+      for (int u = cluster_id; ok && walk_find<GRAD>(P, w, u, t, TILE_M, TILE_N); u += nclusters) {
+        const CUtensorMap *ma = &P.a[t.p], *mb = &P.b[t.p];
+        const int kblocks = GRAD ? (t.r1 - t.r0 + P.bk - 1) / P.bk : P.kblocks;
+        const bool ragged = GRAD && (t.r1 - t.r0) % P.bk != 0;
+        const int arow = t.r0 + t.m0 + 128 * rank, acol = t.m0 + 128 * rank, bcol = t.n0 + 128 * rank;
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if (!wait_bar_warp(empty_bar(stage), phase ^ 1u, abort_flag)) {
+            if (leader) fail();
+            ok = false;
+            break;
+          }
+          const uint32_t sa = sbase + stage * STAGE_BYTES, sb = sa + A_BYTES;
+          const bool to_clear = ragged && kb == kblocks - 1;
+          if (leader) {
+            if constexpr (GRAD) {
+              // both operands' rows run along the contraction: 64 rows x 64 columns a box
+              const int r = t.r0 + kb * P.bk;
+              if (to_clear) {
+                mbar_expect_tx(clear_bar(stage), STAGE_BYTES);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  tma_load_3d(sa + j * (A_BYTES / 2), ma, clear_bar(stage), acol + 64 * j, r, 0);
+                  tma_load_3d(sb + j * (B_BYTES / 2), mb, clear_bar(stage), bcol + 64 * j, r, 0);
+                }
+              } else {
+                const uint32_t fb = mapa_rank0(full_bar(stage));
+                if (rank == 0) mbar_expect_tx(full_bar(stage), 2 * STAGE_BYTES);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  tma_load_3d_pair(sa + j * (A_BYTES / 2), ma, fb, acol + 64 * j, r, 0);
+                  tma_load_3d_pair(sb + j * (B_BYTES / 2), mb, fb, bcol + 64 * j, r, 0);
+                }
+                if (rank != 0) mbar_arrive_cluster(fb);
+              }
+            } else {
+              const uint32_t fb = mapa_rank0(full_bar(stage));
+              if (rank == 0) mbar_expect_tx(full_bar(stage), 2 * STAGE_BYTES);
+              const int k0 = kb * P.bk;
+              tma_load_3d_pair(sa, ma, fb, k0, arow, 0);
+              if (P.form == GRP_NK) {
+                tma_load_3d_pair(sb, mb, fb, k0, bcol, t.e);
+              } else if constexpr (SCALED) {
+                tma_load_3d_pair(sb, mb, fb, bcol, k0, t.e);
+              } else {
+                tma_load_3d_pair(sb, mb, fb, bcol, k0, t.e);
+                tma_load_3d_pair(sb + B_BYTES / 2, mb, fb, bcol + 64, k0, t.e);
+              }
+            }
+          }
+          __syncwarp();
+          const uint32_t bit = 1u << stage;
+          issued |= bit;
+          parity = (parity & ~bit) | (phase << stage);
+          own = to_clear ? own | bit : own & ~bit;
+          if (to_clear) clear_parity ^= bit;  // (starts at 0: after the first use, its phase 0 is the one in flight)
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }
-      Bs[kk][nn] = v;
+      if (!ok) {  // let copies in flight land (CTA 0's barriers count both CTAs')
+        for (int s = 0; s < STAGES; ++s) {
+          if (!((issued >> s) & 1u)) continue;
+          if ((own >> s) & 1u) wait_bar_warp(clear_bar(s), ((clear_parity >> s) & 1u) ^ 1u, never);
+          else if (rank == 0) wait_bar_warp(full_bar(s), (parity >> s) & 1u, never);
+        }
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------- MMA issuer
+      if (rank == 0) {
+        const bool leader = elect_one();
+        const uint32_t idesc = P.idesc, bstep = P.bstep;
+        // A: rows of 128 bytes of k (32 bytes an MMA), or in weight gradients rows along k (16 rows an MMA)
+        constexpr uint32_t astep = GRAD ? 128 : 2;
+        const uint64_t ad0 = tile_desc(sbase, GRAD ? (A_BYTES / 2) >> 4 : 1);
+        const uint64_t bd0 = tile_desc(sbase + A_BYTES, P.blead);
+        constexpr uint32_t kStageDesc = static_cast<uint32_t>(STAGE_BYTES >> 4);
+        Walk w;
+        walk_load<GRAD>(P, w, 0, 0, TILE_M, TILE_N);
+        Tile t;
+        int stage = 0;
+        uint32_t phase = 0;
+        int acc = 0;
+        uint32_t accph = 0;
+        bool ok = true, any_mma = false;
+        auto take_acc = [&]() {
+          if (!wait_bar_warp(tempty_bar(acc), accph ^ 1u, abort_flag)) {
+            if (leader) fail();
+            return false;
+          }
+          tc_fence_after();
+          return true;
+        };
+        auto give_acc = [&]() {
+          if (leader) umma_commit_pair(tfull_bar(acc), kPair);
+          acc ^= 1;
+          if (acc == 0) accph ^= 1u;
+        };
+        for (int u = cluster_id; ok && walk_find<GRAD>(P, w, u, t, TILE_M, TILE_N); u += nclusters) {
+          const int kblocks = GRAD ? (t.r1 - t.r0 + P.bk - 1) / P.bk : P.kblocks;
+          if (GRAD && kblocks == 0) continue;  // no rows: the epilogue stores zeros
+          const bool ragged = GRAD && (t.r1 - t.r0) % P.bk != 0;
+          if (!SCALED && !take_acc()) { ok = false; break; }
+          for (int kb = 0; kb < kblocks; ++kb) {
+            if (SCALED && !take_acc()) { ok = false; break; }
+            bool in = wait_bar_warp(full_bar(stage), phase, abort_flag);
+            if (in && ragged && kb == kblocks - 1)  // what the peer's clearing warp wrote
+              in = __all_sync(0xffffffffu, mbar_test_cluster(full_bar(stage), phase));
+            if (!in) {
+              if (leader) fail();
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            if (leader) {
+              const uint64_t off = static_cast<uint64_t>(stage * kStageDesc);
+              const uint64_t ad = ad0 + off, bd = bd0 + off;
+              const uint32_t d = tmem_base + acc * TILE_N;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_pair<SCALED>(d, ad + astep * k, bd + bstep * k, idesc, SCALED ? k != 0 : (kb | k) != 0);
+              umma_commit_pair(empty_bar(stage), kPair);
+            }
+            __syncwarp();
+            any_mma = true;
+            if (SCALED) give_acc();
+            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+          }
+          if (!SCALED && ok) give_acc();
+          __syncwarp();
+        }
+        if (!ok && any_mma) {  // wait for the MMAs already issued before TMEM is freed
+          if (leader) umma_commit_pair(drain_bar, 0x1);
+          __syncwarp();
+          wait_bar_warp(drain_bar, 0, never);
+        }
+      }
+    } else if (GRAD && warp == 2) {
+      // ------------------------------------- clearing of the next expert's rows
+      // An expert's last k-block holds rows past its end. Both operands' are cleared (one alone would leave
+      // 0 * infinity), in each CTA's own shared memory, before the pair's MMA may read the stage.
+      Walk w;
+      walk_load<GRAD>(P, w, 0, 0, TILE_M, TILE_N);
+      Tile t;
+      int stage = 0;
+      uint32_t clear_phase = 0;  // per stage: parity of its next use
+      bool ok = true;
+      for (int u = cluster_id; ok && walk_find<GRAD>(P, w, u, t, TILE_M, TILE_N); u += nclusters) {
+        const int rows = t.r1 - t.r0, kblocks = (rows + P.bk - 1) / P.bk;
+        const int last = (stage + kblocks + STAGES - 1) % STAGES;
+        stage = (stage + kblocks) % STAGES;
+        const int valid = rows % P.bk;
+        if (valid == 0) continue;
+        if (!wait_bar_warp(clear_bar(last), (clear_phase >> last) & 1u, abort_flag)) {
+          if (lane == 0) fail();
+          ok = false;
+          break;
+        }
+        clear_phase ^= 1u << last;
+        const uint32_t base = sbase + last * STAGE_BYTES;
+        for (int box = 0; box < 4; ++box)  // rows of 128 bytes, 64 to a box (the swizzle stays within a row)
+          for (int b = valid * 128 + lane * 16; b < 64 * 128; b += 32 * 16)
+            st_shared_v4(base + box * (A_BYTES / 2) + b, 0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (rank == 0) mbar_arrive(full_bar(last));
+          else mbar_arrive_cluster(mapa_rank0(full_bar(last)));
+        }
+        __syncwarp();
+      }
     }
-    __syncthreads();
-    for (int kk = 0; kk < TK; ++kk)
-      for (int i = 0; i < 4; ++i)
-        for (int q = 0; q < 4; ++q) acc[i][q] = fmaf(As[kk][ty * 4 + i], Bs[kk][tx * 4 + q], acc[i][q]);
-    __syncthreads();
+  } else {
+    // --------------------------------------------------------- epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    const int quarter = warp & 3;                       // TMEM lanes 32*quarter .. +31 belong to this warp
+    const int half = (warp - FIRST_EPI_WARP) >> 2;      // columns 128*half .. +127 of the tile
+    const uint32_t strip = sbase + STRIP_OFF + (warp - FIRST_EPI_WARP) * STRIP;
+    const uint32_t tacc = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128;
+    const uint32_t tempty0 = rank == 0 ? 0 : mapa_rank0(tempty_bar(0));
+    const int esize = P.out_dtype == COCO_F32 ? 4 : 2;
+    const int64_t pitch = static_cast<int64_t>(P.n) * esize;
+    Walk w;
+    walk_load<GRAD>(P, w, 0, 0, TILE_M, TILE_N);
+    Tile t;
+    int acc = 0;
+    uint32_t accph = 0;
+    auto wait_acc = [&]() {
+      const bool ready = __all_sync(0xffffffffu, wait_bar(tfull_bar(acc), accph, abort_flag));
+      if (!ready && lane == 0) fail();
+      tc_fence_after();
+      return ready;
+    };
+    auto free_acc = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive_relaxed(tempty_bar(acc));
+        else mbar_arrive_cluster_relaxed(tempty0 + 8u * acc);
+      }
+      acc ^= 1;
+      if (acc == 0) accph ^= 1u;
+    };
+    bool ok = true;
+    for (int u = cluster_id; ok && walk_find<GRAD>(P, w, u, t, TILE_M, TILE_N); u += nclusters) {
+      const int m_end = GRAD ? P.k : t.r1 - t.r0;             // rows of the expert's output
+      const int row = t.m0 + 128 * rank + quarter * 32;       // this warp's first one
+      const int rows = min(32, m_end - row);                  // (may be negative: nothing to store)
+      const int col = t.n0 + 128 * half;
+      const int64_t out_row = (GRAD ? static_cast<int64_t>(t.e) * P.k : static_cast<int64_t>(t.r0)) + row;
+      char* out = static_cast<char*>(P.out[t.p]) + out_row * pitch + static_cast<int64_t>(col) * esize;
+      const int64_t bytes = pitch - static_cast<int64_t>(col) * esize;  // left of the row
+      if constexpr (SCALED) {
+        float sum[128];
+#pragma unroll
+        for (int j = 0; j < 128; ++j) sum[j] = 0.0f;
+        // this lane's row of lhs scales, and the scales of this warp's 128 columns; out of range: any valid one
+        const float* sa = P.sa[t.p] + static_cast<int64_t>(min(t.r0 + row + lane, P.rows - 1)) * P.kscales;
+        const int nblk = min(col / 128, P.nscales - 1);
+        const float* sb = P.sb[t.p] + static_cast<int64_t>(t.e) * P.kscales * P.nscales +
+                          (P.form == GRP_NK ? static_cast<int64_t>(nblk) * P.kscales : nblk);
+        const int sb_step = P.form == GRP_NK ? 1 : P.nscales;
+        float s = __ldg(sa) * __ldg(sb);
+        for (int kb = 0; kb < P.kblocks; ++kb) {
+          float s_next = 0.0f;
+          if (kb + 1 < P.kblocks) s_next = __ldg(sa + kb + 1) * __ldg(sb + static_cast<int64_t>(kb + 1) * sb_step);
+          if (!wait_acc()) { ok = false; break; }
+          const uint32_t ta = tacc + acc * TILE_N;
+          // 16 columns at a time, the next 16 on their way while these are added
+          uint32_t r0[16], r1[16];
+          tmem_ld16(ta, r0);
+#pragma unroll
+          for (int c = 0; c < 8; c += 2) {
+            tmem_wait_for(r0);
+            tmem_ld16(ta + 16 * c + 16, r1);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum[16 * c + j] = fmaf(__uint_as_float(r0[j]), s, sum[16 * c + j]);
+            tmem_wait_for(r1);
+            if (c < 6) tmem_ld16(ta + 16 * c + 32, r0);
+            else free_acc();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum[16 * c + 16 + j] = fmaf(__uint_as_float(r1[j]), s, sum[16 * c + 16 + j]);
+          }
+          s = s_next;
+        }
+        if (!ok) break;
+        if (rows > 0 && bytes > 0) {
+          if (esize == 4) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t p[32];
+#pragma unroll
+              for (int j = 0; j < 32; ++j) p[j] = __float_as_uint(sum[32 * c + j]);
+              store_strip(strip, p, out + 128 * c, pitch, rows, bytes - 128 * c);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              uint32_t p[32];
+#pragma unroll
+              for (int j = 0; j < 32; ++j) p[j] = cvt_pair(sum[64 * c + 2 * j], sum[64 * c + 2 * j + 1], P.out_dtype);
+              store_strip(strip, p, out + 128 * c, pitch, rows, bytes - 128 * c);
+            }
+          }
+        }
+      } else {
+        const bool none = GRAD && t.r1 == t.r0;
+        if (!none && !wait_acc()) { ok = false; break; }
+        const uint32_t ta = tacc + acc * TILE_N;
+        const int strips = esize == 4 ? 4 : 2;
+        for (int c = 0; c < strips; ++c) {
+          uint32_t p[32];
+          if (none) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) p[j] = 0u;
+          } else if (esize == 4) {
+            tmem_ld32(ta + 32 * c, p);
+            tmem_wait_for(p);
+          } else {
+            uint32_t r0[32], r1[32];
+            tmem_ld32(ta + 64 * c, r0);
+            tmem_ld32(ta + 64 * c + 32, r1);
+            tmem_wait_for(r0);
+            tmem_wait_for(r1);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              p[j] = cvt_pair(__uint_as_float(r0[2 * j]), __uint_as_float(r0[2 * j + 1]), P.out_dtype);
+              p[16 + j] = cvt_pair(__uint_as_float(r1[2 * j]), __uint_as_float(r1[2 * j + 1]), P.out_dtype);
+            }
+          }
+          if (!none && c == strips - 1) free_acc();
+          if (rows > 0 && bytes > 128 * c) store_strip(strip, p, out + 128 * c, pitch, rows, bytes - 128 * c);
+        }
+      }
+    }
+    if (!GRAD && P.offsets)
+      clear_rest(P, static_cast<int64_t>(blockIdx.x) * (32 * EPI_WARPS) + threadIdx.x - 32 * FIRST_EPI_WARP,
+                 static_cast<int64_t>(gridDim.x) * (32 * EPI_WARPS));
   }
-  for (int i = 0; i < 4; ++i)
-    for (int q = 0; q < 4; ++q) {
-      const int m = m0 + ty * 4 + i, n = n0 + tx * 4 + q;
-      if (m >= M || n >= N) continue;
-      const int64_t row = grad ? static_cast<int64_t>(e) * L.k + m : r0 + m;
-      put(L.out[p], row * L.n + n, L.out_dtype, acc[i][q]);
-    }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no CTA leaves while its peer may still signal its barriers or read its TMEM
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc<true>(tmem_base, TMEM_COLS);
+  }
 }
 
-// Rows of no expert: zeros. Grid: x = steps of elements, y = problem.
-__global__ void __launch_bounds__(256) k_grouped_rest(const __grid_constant__ GroupedLaunch L) {
-  const int p = blockIdx.y;
-  const int32_t* off = L.offsets + static_cast<int64_t>(p) * (L.experts + 1);
-  const int64_t head = min(max(off[0], 0), L.rows), tail = min(max(off[L.experts], static_cast<int>(head)), L.rows);
-  const int64_t total = (head + L.rows - tail) * L.n;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t at = i < head * L.n ? i : i - head * L.n + tail * L.n;
-    put(L.out[p], at, L.out_dtype, 0.0f);
-  }
+// ------------------------------------------------------------------- host
+
+// A dense [d2][d1][d0] array of 1- or 2-byte elements in boxes of box0 x box1, 128-byte swizzle, zeros outside.
+bool encode(CUtensorMap* map, const void* ptr, int dtype, int64_t d0, int64_t d1, int64_t d2, int box0, int box1) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const int es = dtype_size(dtype);
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d0), static_cast<cuuint64_t>(d1), static_cast<cuuint64_t>(d2)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(d0) * es, static_cast<cuuint64_t>(d0 * d1) * es};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(box0), static_cast<cuuint32_t>(box1), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapDataType dt = dtype == COCO_F8E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                 : dtype == COCO_F16  ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                      : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return enc(map, dt, 3, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+std::atomic<bool> smem_set[3][64];
+
+cudaError_t allow_smem(const void* kernel, int which, int bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && smem_set[which][dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) smem_set[which][dev].store(true, std::memory_order_release);
+  return e;
+}
+
+// Tensor-core instruction descriptor: fp32 accumulators, both operands of the input type (e4m3 and f16: format
+// 0 of their kinds, bf16: 1), "MN-major" bits for operands whose rows run along k.
+uint32_t instruction(int dtype, bool a_mn, bool b_mn, int m, int n) {
+  const uint32_t fmt = dtype == COCO_BF16 ? 1 : 0;
+  return (1u << 4) | (fmt << 7) | (fmt << 10) | (static_cast<uint32_t>(a_mn) << 15) |
+         (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(m >> 4) << 24);
 }
 
 }  // namespace
 
-cudaError_t launch_grouped(const GroupedLaunch& L, cudaStream_t s, unsigned int*) {
-  const int m = L.form == GRP_GRAD ? L.k : L.rows;
-  if (L.experts * L.nprob > 65535 || (m + TM - 1) / TM > 65535) return cudaErrorNotSupported;
-  const dim3 grid((L.n + TN - 1) / TN, (m + TM - 1) / TM, L.experts * L.nprob);
-  k_grouped_simple<<<grid, 256, 0, s>>>(L);
-  count_launch();
-  cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess && L.offsets && L.form != GRP_GRAD) {
-    k_grouped_rest<<<dim3(sm_count(), L.nprob), 256, 0, s>>>(L);
-    count_launch();
-    e = cudaGetLastError();
+cudaError_t launch_grouped(const GroupedLaunch& L, cudaStream_t s, unsigned int* err_word) {
+  // coordinates of a tile's last rows and columns stay within 32 bits
+  const int32_t most = INT32_MAX - 1024;
+  if (L.rows > most || L.k > most || L.n > most) return cudaErrorNotSupported;
+  const bool fp8 = L.in_dtype == COCO_F8E4M3, grad = L.form == GRP_GRAD;
+  GroupedParams P;
+  P.offsets = L.offsets;
+  P.err = err_word;
+  P.nprob = L.nprob;
+  P.experts = L.experts;
+  P.form = L.form;
+  P.out_dtype = L.out_dtype;
+  P.rows = L.rows;
+  P.k = L.k;
+  P.n = L.n;
+  P.bk = fp8 ? 128 : 64;
+  P.kblocks = (L.k + P.bk - 1) / P.bk;
+  P.kscales = (L.k + 127) / 128;
+  P.nscales = (L.n + 127) / 128;
+  P.idesc = instruction(L.in_dtype, grad, L.form != GRP_NK, TILE_M, TILE_N);
+  // rows along k: an MMA's k values are 32 (e4m3) or 16 rows of 128 bytes; else 32 bytes of a row
+  P.bstep = L.form == GRP_NK ? 2 : fp8 ? 256 : 128;
+  P.blead = L.form == GRP_NK ? 1 : fp8 ? B_BYTES >> 4 : (B_BYTES / 2) >> 4;
+  for (int p = 0; p < L.nprob; ++p) {
+    P.out[p] = L.out[p];
+    P.sa[p] = L.lhs_scales[p];
+    P.sb[p] = L.rhs_scales[p];
+    const int bk = P.bk;
+    bool good;
+    if (grad)
+      good = encode(&P.a[p], L.lhs[p], L.in_dtype, L.k, L.rows, 1, 64, 64) &&
+             encode(&P.b[p], L.rhs[p], L.in_dtype, L.n, L.rows, 1, 64, 64);
+    else
+      good = encode(&P.a[p], L.lhs[p], L.in_dtype, L.k, L.rows, 1, bk, 128) &&
+             (L.form == GRP_NK ? encode(&P.b[p], L.rhs[p], L.in_dtype, L.k, L.n, L.experts, bk, 128)
+                               : encode(&P.b[p], L.rhs[p], L.in_dtype, L.n, L.k, L.experts, bk, bk));
+    if (!good) return cudaErrorNotSupported;
   }
-  return e;
+  // at most one partly filled tile per expert beyond the full ones
+  const int64_t mts = grad ? static_cast<int64_t>(L.experts) * ((L.k + TILE_M - 1) / TILE_M)
+                           : static_cast<int64_t>(L.rows / TILE_M) + L.experts;
+  const int64_t units = L.nprob * mts * ((L.n + TILE_N - 1) / TILE_N);
+  const int pairs = sm_count() / 2;
+  const int grid = 2 * static_cast<int>(units < pairs ? units : pairs);
+  void (*kernel)(const GroupedParams) = fp8    ? k_grouped_pair<true, false>
+                                        : grad ? k_grouped_pair<false, true>
+                                               : k_grouped_pair<false, false>;
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), fp8 ? 0 : grad ? 1 : 2, SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, THREADS, SMEM_BYTES, s>>>(P);
+  count_launch();
+  return cudaGetLastError();
 }
 
 }  // namespace coco
