@@ -14,7 +14,9 @@ there is no fallback.
 """
 
 import ctypes
+import functools
 import os
+import struct
 
 import torch
 
@@ -70,7 +72,7 @@ class CocoError(RuntimeError):
 
 _P = ctypes.POINTER(CocoTensor)
 _S = ctypes.c_void_p
-_A = ctypes.POINTER(ctypes.c_void_p)  # one device pointer per rank
+_B = ctypes.c_void_p  # a coco_tensor or a pointer array, packed into a bytes object (see Dist.packed)
 for _name, _args in {
     "coco_fused_allreduce": [_P, ctypes.c_void_p, _P, ctypes.c_float, ctypes.c_uint64, _P, _S],
     "coco_fused_allreduce_at": [_P, ctypes.c_void_p, _P, ctypes.c_float, ctypes.c_uint64, ctypes.c_uint64, _P, _S],
@@ -88,12 +90,12 @@ for _name, _args in {
     "coco_looped_ag_einsum_sched": [ctypes.c_char_p, _P, _P, _P, ctypes.c_int, _S],
     "coco_looped_einsum_rs_sched": [ctypes.c_char_p, _P, _P, _P, ctypes.c_int, _S],
     "coco_dropout_keep_mask": [ctypes.c_uint64, ctypes.c_float, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_void_p, _S],
-    "coco_allreduce_rmsnorm": [_P, _P, ctypes.c_void_p, ctypes.c_float, _P, _P, _A, ctypes.c_void_p, _S],
-    "coco_allreduce_rmsnorm_backward": [_P, _P, _P, ctypes.c_void_p, ctypes.c_void_p, _P, ctypes.c_void_p,
+    "coco_allreduce_rmsnorm": [_B, _B, ctypes.c_void_p, ctypes.c_float, _B, _B, _B, ctypes.c_void_p, _S],
+    "coco_allreduce_rmsnorm_backward": [_B, _B, _B, ctypes.c_void_p, ctypes.c_void_p, _B, ctypes.c_void_p,
                                         ctypes.c_void_p, ctypes.c_size_t, _S],
-    "coco_quantize_fp8": [_P, ctypes.c_int32, _P, _A, _S],
-    "coco_einsum_fp8": [ctypes.c_char_p, _P, _A, _P, _A, _P, _S],
-    "coco_grouped_einsum": [ctypes.c_char_p, _P, _A, _P, _A, ctypes.c_void_p, _P, _S],
+    "coco_quantize_fp8": [_B, ctypes.c_int32, _B, _B, _S],
+    "coco_einsum_fp8": [ctypes.c_char_p, _B, _B, _B, _B, _B, _S],
+    "coco_grouped_einsum": [ctypes.c_char_p, _B, _B, _B, _B, ctypes.c_void_p, _B, _S],
     "coco_device_status": [_S],
     "coco_wait_selftest": [ctypes.c_uint64, _S],
 }.items():
@@ -160,7 +162,7 @@ class Dist:
     def __init__(self, layout, tensors, shape, slice_dim=-1, ngroups=1, dtype=None):
         self.layout = layout
         self.tensors = list(tensors)
-        self.shape = tuple(int(s) for s in shape)
+        self.shape = tuple(map(int, shape))
         self.slice_dim = slice_dim
         self.ngroups = ngroups
         self.nranks = len(self.tensors) // ngroups
@@ -179,6 +181,30 @@ class Dist:
         for i, x in enumerate(self.tensors):
             t.ptr[i] = x.data_ptr() if x is not None else None
         return t
+
+    def packed(self):
+        """The coco_tensor as bytes: one struct.pack instead of a field at a time, which is most of what a call
+        on small tensors costs."""
+        return _tensor_struct(len(self.tensors)).pack(
+            self.dtype, self.layout, len(self.shape), self.slice_dim, *(self.shape + (0, 0, 0))[:3], self.nranks,
+            self.ngroups, *_addresses(self.tensors))
+
+
+@functools.lru_cache(maxsize=None)
+def _tensor_struct(n):
+    return struct.Struct(f"=4i3q2i{n}Q{8 * max(0, MAX_PTRS - n)}x")
+
+
+@functools.lru_cache(maxsize=None)
+def _pointer_struct(n):
+    return struct.Struct(f"={n}Q")
+
+
+def _addresses(tensors):
+    try:
+        return list(map(torch.Tensor.data_ptr, tensors))
+    except TypeError:  # a None stands for a null pointer
+        return [0 if x is None else x.data_ptr() for x in tensors]
 
 
 def local(tensors, ngroups=1):
@@ -200,8 +226,8 @@ def sliced(tensors, dim, ngroups=1):
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the current stream's handle, without building a Stream object around it (3 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -295,32 +321,43 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _scales(tensors, what):
-    """Per-rank scale tensors as an array of device pointers; their type and layout are checked here (the
-    library sees addresses only)."""
-    if tensors is None:
-        return None
-    for t in tensors:
-        if t.dtype != torch.float32 or not t.is_contiguous():
-            raise CocoError(3, what)
-    return (ctypes.c_void_p * len(tensors))(*[t.data_ptr() for t in tensors])
-
-
-def _need(ok, status, what):
-    if not ok:
-        raise CocoError(status, what)
+def _packed(d):
+    return None if d is None else d.packed()
 
 
 def _blocks(n):
     return (n + 127) // 128
 
 
-def _check_scales(tensors, d, blocks, what):
-    """One scale tensor per pointer of ``d``, each of ``blocks`` values."""
-    if tensors is not None:
-        _need(len(tensors) == len(d.tensors), 2, what)
-        for t in tensors:
-            _need(t.numel() == blocks, 2, what)
+def _rows_cols(d):
+    """Rows and columns of a rank's tensor (all leading dimensions are rows)."""
+    x = d.tensors[0]
+    cols = x.shape[-1]
+    return (x.numel() // cols if cols else 0), cols
+
+
+def _vector(t, dtype, numel, what):
+    """A plain tensor argument's address; the library sees nothing else of it, so its type, size and layout are
+    checked here."""
+    if t.dtype is not dtype:
+        raise CocoError(3, what)
+    if t.numel() != numel or not t.is_contiguous():
+        raise CocoError(2, what)
+    return t.data_ptr()
+
+
+def _scales(tensors, d, blocks, what):
+    """The scale tensors of ``d`` (one per pointer, ``blocks`` values each) as an array of device pointers."""
+    if tensors is None:
+        return None
+    if len(tensors) != len(d.tensors):
+        raise CocoError(2, what)
+    ptrs, last, p = [], None, 0
+    for t in tensors:
+        if t is not last:
+            last, p = t, _vector(t, torch.float32, blocks, what)
+        ptrs.append(p)
+    return _pointer_struct(len(ptrs)).pack(*ptrs)
 
 
 def coco_allreduce_rmsnorm(partials, residual, weight, eps, hidden, normed, scales, rstd, stream=None):
@@ -329,16 +366,11 @@ def coco_allreduce_rmsnorm(partials, residual, weight, eps, hidden, normed, scal
     ``normed`` holds the partials' type (``scales`` None) or float8_e4m3fn, with one fp32 scale tensor
     [rows, ceil(cols / 128)] per normed pointer in ``scales``."""
     what = "coco_allreduce_rmsnorm"
-    cols = partials.shape[-1]
-    rows = partials.tensors[0].numel() // cols if cols else 0
-    _need(weight.dtype == partials.tensors[0].dtype, 3, what)
-    _need(weight.numel() == cols and weight.is_contiguous(), 2, what)
-    _check_scales(scales, normed, rows * _blocks(cols), what)
-    if rstd is not None:
-        _need(rstd.dtype == torch.float32, 3, what)
-        _need(rstd.numel() == rows * partials.ngroups and rstd.is_contiguous(), 2, what)
-    _check(_lib.coco_allreduce_rmsnorm(_ref(partials), _ref(residual), _ptr(weight), float(eps), _ref(hidden),
-                                       _ref(normed), _scales(scales, what), _ptr(rstd), _stream(stream)), what)
+    rows, cols = _rows_cols(partials)
+    w = _vector(weight, partials.tensors[0].dtype, cols, what)
+    r = None if rstd is None else _vector(rstd, torch.float32, rows * partials.ngroups, what)
+    _check(_lib.coco_allreduce_rmsnorm(partials.packed(), _packed(residual), w, eps, _packed(hidden), normed.packed(),
+                                       _scales(scales, normed, rows * _blocks(cols), what), r, _stream(stream)), what)
 
 
 def coco_allreduce_rmsnorm_backward_bytes(rows, cols):
@@ -351,44 +383,46 @@ def coco_allreduce_rmsnorm_backward(dnormed, dhidden, hidden, weight, rstd, dx, 
     residual stream's gradient or None; writes ``dx`` (of each partial and of the residual) and ``dweight``
     (fp32). ``workspace``: a device tensor of coco_allreduce_rmsnorm_backward_bytes() bytes."""
     what = "coco_allreduce_rmsnorm_backward"
-    cols = dnormed.shape[-1]
-    rows = dnormed.tensors[0].numel() // cols if cols else 0
-    _need(weight.dtype == dnormed.tensors[0].dtype and rstd.dtype == dweight.dtype == torch.float32, 3, what)
-    _need(weight.numel() == dweight.numel() == cols and rstd.numel() == rows * dnormed.ngroups and
-          weight.is_contiguous() and dweight.is_contiguous() and rstd.is_contiguous() and workspace.is_contiguous(),
-          2, what)
-    _check(_lib.coco_allreduce_rmsnorm_backward(
-        _ref(dnormed), _ref(dhidden), _ref(hidden), _ptr(weight), _ptr(rstd), _ref(dx), _ptr(dweight),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)), what)
+    rows, cols = _rows_cols(dnormed)
+    w = _vector(weight, dnormed.tensors[0].dtype, cols, what)
+    r = _vector(rstd, torch.float32, rows * dnormed.ngroups, what)
+    dw = _vector(dweight, torch.float32, cols, what)
+    if not workspace.is_contiguous():
+        raise CocoError(2, what)
+    _check(_lib.coco_allreduce_rmsnorm_backward(dnormed.packed(), _packed(dhidden), hidden.packed(), w, r, dx.packed(),
+                                                dw, workspace.data_ptr(), workspace.nbytes, _stream(stream)), what)
 
 
 def coco_quantize_fp8(x, block_rows, q, scales, stream=None):
     """Every rank's x as float8_e4m3fn values ``q`` and fp32 ``scales`` (one tensor per rank): one scale per row
     and 128 columns (``block_rows`` 1) or per 128 x 128 tile of each matrix (128)."""
     what = "coco_quantize_fp8"
-    shape = x.tensors[0].shape
-    if int(block_rows) in (1, 128) and len(shape) >= 1:
-        cols = shape[-1]
-        rows = x.tensors[0].numel() // cols if cols else 0
-        if block_rows == 128:
-            mats = shape[0] if len(shape) == 3 else 1
-            _check_scales(scales, q, mats * _blocks(rows // mats if mats else 0) * _blocks(cols), what)
-        else:
-            _check_scales(scales, q, rows * _blocks(cols), what)
-    _check(_lib.coco_quantize_fp8(_ref(x), int(block_rows), _ref(q), _scales(scales, what), _stream(stream)), what)
+    rows, cols = _rows_cols(x)
+    if block_rows == 128:
+        mats = x.shape[0] if len(x.shape) == 3 else 1
+        blocks = mats * _blocks(rows // mats if mats else 0) * _blocks(cols)
+    else:
+        blocks = rows * _blocks(cols)
+    _check(_lib.coco_quantize_fp8(x.packed(), block_rows, q.packed(), _scales(scales, q, blocks, what),
+                                  _stream(stream)), what)
+
+
+def _operand_scales(lhs, lhs_scales, rhs, rhs_scales, what):
+    """The scale arrays of a product's operands: per row and 128 columns, and per 128 x 128 tile of each matrix."""
+    if lhs_scales is None and rhs_scales is None:
+        return None, None
+    rows, cols = _rows_cols(lhs)
+    shape = rhs.tensors[0].shape
+    tiles = (shape[0] if len(shape) == 3 else 1) * _blocks(shape[-2] if len(shape) > 1 else 1) * _blocks(shape[-1])
+    return _scales(lhs_scales, lhs, rows * _blocks(cols), what), _scales(rhs_scales, rhs, tiles, what)
 
 
 def coco_einsum_fp8(spec, lhs, lhs_scales, rhs, rhs_scales, out, stream=None):
     """out_r = lhs_r @ rhs_r on float8_e4m3fn operands with fp32 scales per 1 x 128 (lhs) and 128 x 128 (rhs)
     block; ``spec`` "mk,kn->mn" or "mk,nk->mn". Scale tensors: one per pointer of the operand."""
     what = "coco_einsum_fp8"
-    if len(lhs.tensors[0].shape) == 2 and len(rhs.tensors[0].shape) == 2:
-        m, k = lhs.tensors[0].shape
-        r, c = rhs.tensors[0].shape
-        _check_scales(lhs_scales, lhs, m * _blocks(k), what)
-        _check_scales(rhs_scales, rhs, _blocks(r) * _blocks(c), what)
-    _check(_lib.coco_einsum_fp8(spec.encode(), _ref(lhs), _scales(lhs_scales, what), _ref(rhs),
-                                _scales(rhs_scales, what), _ref(out), _stream(stream)), what)
+    sa, sb = _operand_scales(lhs, lhs_scales, rhs, rhs_scales, what)
+    _check(_lib.coco_einsum_fp8(spec.encode(), lhs.packed(), sa, rhs.packed(), sb, out.packed(), _stream(stream)), what)
 
 
 def coco_grouped_einsum(spec, lhs, lhs_scales, rhs, rhs_scales, offsets, out, stream=None):
@@ -396,17 +430,11 @@ def coco_grouped_einsum(spec, lhs, lhs_scales, rhs, rhs_scales, offsets, out, st
     "tk,ekn->tn", "tk,enk->tn" or the weight gradient "tk,tn->ekn"; ``offsets`` an int32 device tensor
     [ranks, experts + 1]; scale lists for float8_e4m3fn operands, else None."""
     what = "coco_grouped_einsum"
-    if len(lhs.tensors[0].shape) == 2 and len(rhs.tensors[0].shape) == 3:
-        t, k = lhs.tensors[0].shape
-        e, r, c = rhs.tensors[0].shape
-        _check_scales(lhs_scales, lhs, t * _blocks(k), what)
-        _check_scales(rhs_scales, rhs, e * _blocks(r) * _blocks(c), what)
-    if offsets is not None:
-        experts = (out if spec.replace(" ", "") == "tk,tn->ekn" else rhs).shape[0]
-        _need(offsets.dtype == torch.int32, 3, what)
-        _need(offsets.numel() == len(lhs.tensors) * (experts + 1) and offsets.is_contiguous(), 2, what)
-    _check(_lib.coco_grouped_einsum(spec.encode(), _ref(lhs), _scales(lhs_scales, what), _ref(rhs),
-                                    _scales(rhs_scales, what), _ptr(offsets), _ref(out), _stream(stream)), what)
+    sa, sb = _operand_scales(lhs, lhs_scales, rhs, rhs_scales, what)
+    experts = (rhs if len(rhs.shape) == 3 else out).shape[0]
+    off = None if offsets is None else _vector(offsets, torch.int32, len(lhs.tensors) * (experts + 1), what)
+    _check(_lib.coco_grouped_einsum(spec.encode(), lhs.packed(), sa, rhs.packed(), sb, off, out.packed(),
+                                    _stream(stream)), what)
 
 
 def coco_dropout_keep_mask(seed, dropout_p, first_index, count, mask, stream=None):

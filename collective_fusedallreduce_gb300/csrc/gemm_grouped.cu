@@ -19,7 +19,7 @@
 // rows of A, 128 columns of B and its 128 rows of the accumulator).
 //   warp 0        TMA producer: k-blocks 128 bytes deep into a ring of 6 stages of 32 KB.
 //   warp 1        issues the MMAs (CTA 0 of the pair) and owns TMEM.
-//   warp 2        in weight gradients: clears what a k-block holds of the next expert's rows.
+//   warps 2, 3    in weight gradients: clear what a k-block holds of the next expert's rows.
 //   warps 4..11   two per TMEM lane quarter, 128 columns each: sum of the scaled blocks, conversion, stores.
 // Every mbarrier wait is bounded by %globaltimer as in the other tensor-core
 // kernels: on expiry COCO_ERR_TIMEOUT is recorded, the roles drain and return.
@@ -192,40 +192,29 @@ __device__ __forceinline__ void tmem_wait_for(uint32_t (&r)[32]) {
                : "memory");
 }
 
-__device__ __forceinline__ void tmem_wait_for(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :
-               : "memory");
+// Two fp32 values in a 64-bit register, and sum += value * scale on both in one instruction (each rounded
+// once, as fmaf): the additions are the epilogue's issue slots, and those bound the block-scaled products.
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
+  return v;
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
+__device__ __forceinline__ void unpack2(uint64_t v, uint32_t& lo, uint32_t& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+}
+__device__ __forceinline__ void add_scaled(uint64_t& sum, uint32_t lo, uint32_t hi, uint64_t scale) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(sum) : "l"(pack2(lo, hi)), "l"(scale));
 }
 
-// A wait that also sees what the other CTA of the pair wrote before its arrival.
-__device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
+// Arrivals that publish a warp's shared-memory writes to its own SM's tensor core: the writes are fenced to the
+// async proxy first (fence.proxy.async), and the only reader of a CTA's operands is that CTA's half of the pair's
+// MMA, which reads its own SM's shared memory. CTA scope is therefore enough for the remote arrival too; a release
+// at cluster scope costs some 2000 cycles per call (it made the ragged weight gradient 30 % slower).
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
 // ---------------------------------------------------------------- epilogue
@@ -289,9 +278,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      // CTA 0's is the pair's: its own producer's arrival, and in weight gradients one of each CTA (the producer's,
-      // or for an expert's last block that of the warp that cleared it)
-      mbar_init(full_bar(s), GRAD ? 2 : 1);
+      // CTA 0's is the pair's: its own producer's arrival, and in weight gradients two of each CTA (the producer's,
+      // or for an expert's last block those of the warps that cleared it)
+      mbar_init(full_bar(s), GRAD ? 4 : 1);
       mbar_init(empty_bar(s), 1);
       mbar_init(clear_bar(s), 1);
     }
@@ -356,13 +345,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 }
               } else {
                 const uint32_t fb = mapa_rank0(full_bar(stage));
-                if (rank == 0) mbar_expect_tx(full_bar(stage), 2 * STAGE_BYTES);
+                if (rank == 0) {
+                  mbar_expect_tx(full_bar(stage), 2 * STAGE_BYTES);
+                  mbar_arrive_relaxed(full_bar(stage));
+                }
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                   tma_load_3d_pair(sa + j * (A_BYTES / 2), ma, fb, acol + 64 * j, r, 0);
                   tma_load_3d_pair(sb + j * (B_BYTES / 2), mb, fb, bcol + 64 * j, r, 0);
                 }
-                if (rank != 0) mbar_arrive_cluster(fb);
+                if (rank != 0) {  // (relaxed: these publish nothing of this thread's)
+                  mbar_arrive_cluster_relaxed(fb);
+                  mbar_arrive_cluster_relaxed(fb);
+                }
               }
             } else {
               const uint32_t fb = mapa_rank0(full_bar(stage));
@@ -429,14 +424,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         for (int u = cluster_id; ok && walk_find<GRAD>(P, w, u, t, TILE_M, TILE_N); u += nclusters) {
           const int kblocks = GRAD ? (t.r1 - t.r0 + P.bk - 1) / P.bk : P.kblocks;
           if (GRAD && kblocks == 0) continue;  // no rows: the epilogue stores zeros
-          const bool ragged = GRAD && (t.r1 - t.r0) % P.bk != 0;
           if (!SCALED && !take_acc()) { ok = false; break; }
           for (int kb = 0; kb < kblocks; ++kb) {
             if (SCALED && !take_acc()) { ok = false; break; }
-            bool in = wait_bar_warp(full_bar(stage), phase, abort_flag);
-            if (in && ragged && kb == kblocks - 1)  // what the peer's clearing warp wrote
-              in = __all_sync(0xffffffffu, mbar_test_cluster(full_bar(stage), phase));
-            if (!in) {
+            if (!wait_bar_warp(full_bar(stage), phase, abort_flag)) {
               if (leader) fail();
               ok = false;
               break;
@@ -465,7 +456,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           wait_bar_warp(drain_bar, 0, never);
         }
       }
-    } else if (GRAD && warp == 2) {
+    } else if (GRAD && warp >= 2) {
       // ------------------------------------- clearing of the next expert's rows
       // An expert's last k-block holds rows past its end. Both operands' are cleared (one alone would leave
       // 0 * infinity), in each CTA's own shared memory, before the pair's MMA may read the stage.
@@ -488,9 +479,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         clear_phase ^= 1u << last;
         const uint32_t base = sbase + last * STAGE_BYTES;
-        for (int box = 0; box < 4; ++box)  // rows of 128 bytes, 64 to a box (the swizzle stays within a row)
+        // rows of 128 bytes, 64 to a box (the swizzle stays within a row): A's two boxes by one warp, B's by the other
+        for (int box = 0; box < 2; ++box)
           for (int b = valid * 128 + lane * 16; b < 64 * 128; b += 32 * 16)
-            st_shared_v4(base + box * (A_BYTES / 2) + b, 0u, 0u, 0u, 0u);
+            st_shared_v4(base + (warp - 2) * A_BYTES + box * (A_BYTES / 2) + b, 0u, 0u, 0u, 0u);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -541,9 +533,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       char* out = static_cast<char*>(P.out[t.p]) + out_row * pitch + static_cast<int64_t>(col) * esize;
       const int64_t bytes = pitch - static_cast<int64_t>(col) * esize;  // left of the row
       if constexpr (SCALED) {
-        float sum[128];
+        uint64_t sum[64];  // pairs of fp32 sums of neighbouring columns
 #pragma unroll
-        for (int j = 0; j < 128; ++j) sum[j] = 0.0f;
+        for (int j = 0; j < 64; ++j) sum[j] = 0ull;
         // this lane's row of lhs scales, and the scales of this warp's 128 columns; out of range: any valid one
         const float* sa = P.sa[t.p] + static_cast<int64_t>(min(t.r0 + row + lane, P.rows - 1)) * P.kscales;
         const int nblk = min(col / 128, P.nscales - 1);
@@ -556,21 +548,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           if (kb + 1 < P.kblocks) s_next = __ldg(sa + kb + 1) * __ldg(sb + static_cast<int64_t>(kb + 1) * sb_step);
           if (!wait_acc()) { ok = false; break; }
           const uint32_t ta = tacc + acc * TILE_N;
-          // 16 columns at a time, the next 16 on their way while these are added
-          uint32_t r0[16], r1[16];
-          tmem_ld16(ta, r0);
+          // 64 columns on their way at a time (two waits a block: each costs a TMEM latency)
+          uint32_t r0[32], r1[32];
+          const uint64_t ss = pack2(__float_as_uint(s), __float_as_uint(s));
+          tmem_ld32(ta, r0);
+          tmem_ld32(ta + 32, r1);
+          tmem_wait_for(r0);
+          tmem_wait_for(r1);
 #pragma unroll
-          for (int c = 0; c < 8; c += 2) {
-            tmem_wait_for(r0);
-            tmem_ld16(ta + 16 * c + 16, r1);
+          for (int j = 0; j < 16; ++j) add_scaled(sum[j], r0[2 * j], r0[2 * j + 1], ss);
+          tmem_ld32(ta + 64, r0);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) sum[16 * c + j] = fmaf(__uint_as_float(r0[j]), s, sum[16 * c + j]);
-            tmem_wait_for(r1);
-            if (c < 6) tmem_ld16(ta + 16 * c + 32, r0);
-            else free_acc();
+          for (int j = 0; j < 16; ++j) add_scaled(sum[16 + j], r1[2 * j], r1[2 * j + 1], ss);
+          tmem_ld32(ta + 96, r1);
+          tmem_wait_for(r0);
+          tmem_wait_for(r1);
+          free_acc();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) sum[16 * c + 16 + j] = fmaf(__uint_as_float(r1[j]), s, sum[16 * c + 16 + j]);
-          }
+          for (int j = 0; j < 16; ++j) add_scaled(sum[32 + j], r0[2 * j], r0[2 * j + 1], ss);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) add_scaled(sum[48 + j], r1[2 * j], r1[2 * j + 1], ss);
           s = s_next;
         }
         if (!ok) break;
@@ -580,7 +577,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             for (int c = 0; c < 4; ++c) {
               uint32_t p[32];
 #pragma unroll
-              for (int j = 0; j < 32; ++j) p[j] = __float_as_uint(sum[32 * c + j]);
+              for (int j = 0; j < 16; ++j) unpack2(sum[16 * c + j], p[2 * j], p[2 * j + 1]);
               store_strip(strip, p, out + 128 * c, pitch, rows, bytes - 128 * c);
             }
           } else {
@@ -588,7 +585,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             for (int c = 0; c < 2; ++c) {
               uint32_t p[32];
 #pragma unroll
-              for (int j = 0; j < 32; ++j) p[j] = cvt_pair(sum[64 * c + 2 * j], sum[64 * c + 2 * j + 1], P.out_dtype);
+              for (int j = 0; j < 32; ++j) {
+                uint32_t x, y;
+                unpack2(sum[32 * c + j], x, y);
+                p[j] = cvt_pair(__uint_as_float(x), __uint_as_float(y), P.out_dtype);
+              }
               store_strip(strip, p, out + 128 * c, pitch, rows, bytes - 128 * c);
             }
           }
