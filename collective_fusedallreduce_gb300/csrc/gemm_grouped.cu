@@ -46,8 +46,8 @@ constexpr int THREADS = 32 * (FIRST_EPI_WARP + EPI_WARPS);
 constexpr int STRIP = 32 * 128;  // an epilogue warp's staging: 32 rows x 128 bytes
 constexpr int STRIP_OFF = STAGES * STAGE_BYTES;
 constexpr int BAR_OFF = STRIP_OFF + EPI_WARPS * STRIP;
-// full, empty and cleared per stage, accumulator full x2, empty x2, drain
-constexpr int NUM_BARS = 3 * STAGES + 5;
+// full, empty and cleared per stage; full and empty per accumulator buffer and half; drain
+constexpr int NUM_BARS = 3 * STAGES + 9;
 constexpr int SMEM_BYTES = BAR_OFF + 8 * NUM_BARS + 16 + 1024;  // + alignment slack
 static_assert(SMEM_BYTES <= 232448, "shared memory over the per-CTA limit");
 constexpr uint32_t TMEM_COLS = 512;
@@ -65,9 +65,11 @@ struct GroupedParams {
   int32_t kblocks;     // of the k dimension (weight gradients: each expert's rows give their own)
   int32_t bk;          // elements of a k-block
   int32_t kscales, nscales;
+  int32_t sb_k, sb_n;  // steps of the rhs scales along k and n
   uint32_t idesc;
   uint32_t bstep;      // B's descriptor advance per MMA, in 16-byte units
   uint32_t blead;      // B's leading byte offset >> 4
+  uint32_t bhalf;      // block scales: from the first 64 columns of a CTA's B to the others, in 16-byte units
 };
 static_assert(sizeof(GroupedParams) <= 32000, "kernel parameter block too large");
 
@@ -138,6 +140,16 @@ __device__ __forceinline__ bool walk_find(const GroupedParams& P, Walk& w, int u
   return true;
 }
 
+// The number of all units: for a warp whose work is the same for every tile.
+template <bool GRAD>
+__device__ __forceinline__ int walk_total(const GroupedParams& P, int tm, int tn) {
+  Walk w;
+  walk_load<GRAD>(P, w, 0, 0, tm, tn);
+  while (w.base + 32 < P.nprob * P.experts)
+    walk_load<GRAD>(P, w, w.base + 32, __shfl_sync(0xffffffffu, w.upto, 31), tm, tn);
+  return __shfl_sync(0xffffffffu, w.upto, 31);
+}
+
 // ------------------------------------------------------------ PTX (this file)
 
 // D (+)= A B over the pair, e4m3 operands (kind::f8f6f4, K = 32) or 16-bit ones (kind::f16, K = 16).
@@ -180,18 +192,15 @@ __device__ __forceinline__ uint64_t tile_desc(uint32_t saddr, uint32_t lead) {
          (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-// Waits for this thread's TMEM loads; the registers pass through, so no use of them can move ahead of it.
-__device__ __forceinline__ void tmem_wait_for(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
-                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                 "+r"(r[30]), "+r"(r[31])
-               :
-               : "memory");
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
 }
-
 // Two fp32 values in a 64-bit register, and sum += value * scale on both in one instruction (each rounded
 // once, as fmaf): the additions are the epilogue's issue slots, and those bound the block-scaled products.
 __device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
@@ -203,7 +212,7 @@ __device__ __forceinline__ void unpack2(uint64_t v, uint32_t& lo, uint32_t& hi) 
   asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
 }
 __device__ __forceinline__ void add_scaled(uint64_t& sum, uint32_t lo, uint32_t hi, uint64_t scale) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(sum) : "l"(pack2(lo, hi)), "l"(scale));
+  asm volatile("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(sum) : "l"(pack2(lo, hi)), "l"(scale));
 }
 
 // Arrivals that publish a warp's shared-memory writes to its own SM's tensor core: the writes are fenced to the
@@ -219,11 +228,25 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
 
 // ---------------------------------------------------------------- epilogue
 
+// Values that a k loop does not need, kept in the warp's (then idle) staging strip across it: its 128 sums and
+// the loads in flight take nearly all of a thread's registers.
+__device__ __forceinline__ void park(uint32_t strip, int i, int v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(strip + 4 * (32 * i + (threadIdx.x & 31))), "r"(v) : "memory");
+}
+__device__ __forceinline__ int unpark(uint32_t strip, int i) {
+  int v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(strip + 4 * (32 * i + (threadIdx.x & 31))) : "memory");
+  return v;
+}
+
 // Writes 32 rows x 128 bytes held one row per lane: through shared memory, so that each store instruction
 // covers four whole 128-byte lines, and bounded by rows and bytes, so that a tile may end anywhere.
 __device__ __forceinline__ void store_strip(uint32_t strip, const uint32_t (&p)[32], char* out, int64_t pitch,
                                             int rows, int64_t bytes) {
-  const int lane = threadIdx.x & 31;
+  // The lane is read anew (volatile): the two dozen addresses below would otherwise be computed once, ahead of the
+  // tiles, and kept in the registers that the k loop's sums need.
+  int lane;
+  asm volatile("mov.u32 %0, %%laneid;" : "=r"(lane));
 #pragma unroll
   for (int c = 0; c < 8; ++c)
     st_shared_v4(strip + lane * 128 + ((c ^ (lane & 7)) << 4), p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
@@ -265,9 +288,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
   auto clear_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };  // weight gradients: an expert's last block
-  auto tfull_bar = [&](int a) { return bar0 + 8u * (3 * STAGES + a); };
-  auto tempty_bar = [&](int a) { return bar0 + 8u * (3 * STAGES + 2 + a); };
-  const uint32_t drain_bar = bar0 + 8u * (3 * STAGES + 4);
+  // accumulator buffer a; block scales: its half h (columns 128 h .. 128 h + 127) by itself
+  auto tfull_bar = [&](int a, int h) { return bar0 + 8u * (3 * STAGES + 2 * a + h); };
+  auto tempty_bar = [&](int a, int h) { return bar0 + 8u * (3 * STAGES + 4 + 2 * a + h); };
+  const uint32_t drain_bar = bar0 + 8u * (3 * STAGES + 8);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + BAR_OFF + 8 * NUM_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + BAR_OFF + 8 * NUM_BARS + 4);
 
@@ -284,10 +308,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       mbar_init(empty_bar(s), 1);
       mbar_init(clear_bar(s), 1);
     }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(tfull_bar(a), 1);
-      mbar_init(tempty_bar(a), 2 * EPI_WARPS);  // CTA 0's: the epilogue warps of both CTAs
-    }
+    for (int a = 0; a < 2; ++a)
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(tfull_bar(a, h), 1);
+        mbar_init(tempty_bar(a, h), SCALED ? EPI_WARPS : 2 * EPI_WARPS);  // CTA 0's: epilogue warps of both CTAs
+      }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -305,10 +330,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   int dummy = 0;
   volatile int* never = &dummy;
 
-  // Registers: an epilogue thread holds 128 sums. The launch's 384 threads have 168 each; the four warps in
-  // front give up what the eight epilogue warps take (128 x 56 + 256 x 224 = 384 x 168).
+  // Registers, block scales: an epilogue thread holds 128 sums. The launch's 384 threads have 168 each; the four warps in
+  // front give up what the eight epilogue warps take (128 x 72 + 256 x 216 = 384 x 168). Neither side may spill: a few
+  // reloads in the MMA warp's loop or the sums' cost the block-scaled product 20 to 60 %.
   if (warp < FIRST_EPI_WARP) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if constexpr (SCALED) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0) {
       // ------------------------------------------------------ TMA producer
       const bool leader = elect_one();
@@ -400,54 +426,77 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const uint64_t ad0 = tile_desc(sbase, GRAD ? (A_BYTES / 2) >> 4 : 1);
         const uint64_t bd0 = tile_desc(sbase + A_BYTES, P.blead);
         constexpr uint32_t kStageDesc = static_cast<uint32_t>(STAGE_BYTES >> 4);
+        // (only weight gradients' tiles differ in length: the others need no more than their number)
+        const int total = GRAD ? 0 : walk_total<GRAD>(P, TILE_M, TILE_N);
         Walk w;
-        walk_load<GRAD>(P, w, 0, 0, TILE_M, TILE_N);
+        if constexpr (GRAD) walk_load<GRAD>(P, w, 0, 0, TILE_M, TILE_N);
         Tile t;
         int stage = 0;
         uint32_t phase = 0;
         int acc = 0;
         uint32_t accph = 0;
         bool ok = true, any_mma = false;
-        auto take_acc = [&]() {
-          if (!wait_bar_warp(tempty_bar(acc), accph ^ 1u, abort_flag)) {
+        auto more = [&](int u) {
+          if constexpr (GRAD) return walk_find<GRAD>(P, w, u, t, TILE_M, TILE_N);
+          else return u < total;
+        };
+        auto take_acc = [&](int h) {
+          if (!wait_bar_warp(tempty_bar(acc, h), accph ^ 1u, abort_flag)) {
             if (leader) fail();
             return false;
           }
           tc_fence_after();
           return true;
         };
-        auto give_acc = [&]() {
-          if (leader) umma_commit_pair(tfull_bar(acc), kPair);
+        auto next_acc = [&]() {
           acc ^= 1;
           if (acc == 0) accph ^= 1u;
         };
-        for (int u = cluster_id; ok && walk_find<GRAD>(P, w, u, t, TILE_M, TILE_N); u += nclusters) {
+        for (int u = cluster_id; ok && more(u); u += nclusters) {
           const int kblocks = GRAD ? (t.r1 - t.r0 + P.bk - 1) / P.bk : P.kblocks;
           if (GRAD && kblocks == 0) continue;  // no rows: the epilogue stores zeros
-          if (!SCALED && !take_acc()) { ok = false; break; }
+          if (!SCALED && !take_acc(0)) { ok = false; break; }
           for (int kb = 0; kb < kblocks; ++kb) {
-            if (SCALED && !take_acc()) { ok = false; break; }
             if (!wait_bar_warp(full_bar(stage), phase, abort_flag)) {
               if (leader) fail();
               ok = false;
               break;
             }
             tc_fence_after();
-            if (leader) {
-              const uint64_t off = static_cast<uint64_t>(stage * kStageDesc);
-              const uint64_t ad = ad0 + off, bd = bd0 + off;
-              const uint32_t d = tmem_base + acc * TILE_N;
+            const uint64_t off = static_cast<uint64_t>(stage * kStageDesc);
+            const uint64_t ad = ad0 + off, bd = bd0 + off;
+            if constexpr (SCALED) {
+              for (int h = 0; h < 2; ++h) {
+                if (!take_acc(h)) { ok = false; break; }
+                if (leader) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_pair<SCALED>(d, ad + astep * k, bd + bstep * k, idesc, SCALED ? k != 0 : (kb | k) != 0);
-              umma_commit_pair(empty_bar(stage), kPair);
+                  for (int k = 0; k < 4; ++k)
+                    mma_pair<true>(tmem_base + acc * TILE_N + 128 * h, ad + astep * k, bd + P.bhalf * h + bstep * k,
+                                   idesc, k != 0);
+                  umma_commit_pair(tfull_bar(acc, h), kPair);
+                }
+                __syncwarp();
+                any_mma = true;
+              }
+              if (!ok) break;
+              if (leader) umma_commit_pair(empty_bar(stage), kPair);
+              next_acc();
+            } else {
+              if (leader) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  mma_pair<false>(tmem_base + acc * TILE_N, ad + astep * k, bd + bstep * k, idesc, (kb | k) != 0);
+                umma_commit_pair(empty_bar(stage), kPair);
+              }
+              any_mma = true;
             }
             __syncwarp();
-            any_mma = true;
-            if (SCALED) give_acc();
             if (++stage == STAGES) { stage = 0; phase ^= 1u; }
           }
-          if (!SCALED && ok) give_acc();
+          if (!SCALED && ok) {
+            if (leader) umma_commit_pair(tfull_bar(acc, 0), kPair);
+            next_acc();
+          }
           __syncwarp();
         }
         if (!ok && any_mma) {  // wait for the MMAs already issued before TMEM is freed
@@ -494,21 +543,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
   } else {
     // --------------------------------------------------------- epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    if constexpr (SCALED) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int quarter = warp & 3;                       // TMEM lanes 32*quarter .. +31 belong to this warp
     const int half = (warp - FIRST_EPI_WARP) >> 2;      // columns 128*half .. +127 of the tile
     const uint32_t strip = sbase + STRIP_OFF + (warp - FIRST_EPI_WARP) * STRIP;
     const uint32_t tacc = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128;
-    const uint32_t tempty0 = rank == 0 ? 0 : mapa_rank0(tempty_bar(0));
-    const int esize = P.out_dtype == COCO_F32 ? 4 : 2;
-    const int64_t pitch = static_cast<int64_t>(P.n) * esize;
+    const int hb = SCALED ? half : 0;  // the half whose barriers this warp follows
+    const uint32_t tempty0 = rank == 0 ? 0 : mapa_rank0(tempty_bar(0, hb));
     Walk w;
     walk_load<GRAD>(P, w, 0, 0, TILE_M, TILE_N);
     Tile t;
     int acc = 0;
     uint32_t accph = 0;
     auto wait_acc = [&]() {
-      const bool ready = __all_sync(0xffffffffu, wait_bar(tfull_bar(acc), accph, abort_flag));
+      const bool ready = __all_sync(0xffffffffu, wait_bar(tfull_bar(acc, hb), accph, abort_flag));
       if (!ready && lane == 0) fail();
       tc_fence_after();
       return ready;
@@ -517,68 +565,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if (rank == 0) mbar_arrive_relaxed(tempty_bar(acc));
-        else mbar_arrive_cluster_relaxed(tempty0 + 8u * acc);
+        if (rank == 0) mbar_arrive_relaxed(tempty_bar(acc, hb));
+        else mbar_arrive_cluster_relaxed(tempty0 + 16u * acc);
       }
       acc ^= 1;
       if (acc == 0) accph ^= 1u;
     };
     bool ok = true;
     for (int u = cluster_id; ok && walk_find<GRAD>(P, w, u, t, TILE_M, TILE_N); u += nclusters) {
-      const int m_end = GRAD ? P.k : t.r1 - t.r0;             // rows of the expert's output
-      const int row = t.m0 + 128 * rank + quarter * 32;       // this warp's first one
-      const int rows = min(32, m_end - row);                  // (may be negative: nothing to store)
-      const int col = t.n0 + 128 * half;
-      const int64_t out_row = (GRAD ? static_cast<int64_t>(t.e) * P.k : static_cast<int64_t>(t.r0)) + row;
-      char* out = static_cast<char*>(P.out[t.p]) + out_row * pitch + static_cast<int64_t>(col) * esize;
-      const int64_t bytes = pitch - static_cast<int64_t>(col) * esize;  // left of the row
       if constexpr (SCALED) {
         uint64_t sum[64];  // pairs of fp32 sums of neighbouring columns
 #pragma unroll
         for (int j = 0; j < 64; ++j) sum[j] = 0ull;
-        // this lane's row of lhs scales, and the scales of this warp's 128 columns; out of range: any valid one
-        const float* sa = P.sa[t.p] + static_cast<int64_t>(min(t.r0 + row + lane, P.rows - 1)) * P.kscales;
-        const int nblk = min(col / 128, P.nscales - 1);
-        const float* sb = P.sb[t.p] + static_cast<int64_t>(t.e) * P.kscales * P.nscales +
-                          (P.form == GRP_NK ? static_cast<int64_t>(nblk) * P.kscales : nblk);
-        const int sb_step = P.form == GRP_NK ? 1 : P.nscales;
-        float s = __ldg(sa) * __ldg(sb);
-        for (int kb = 0; kb < P.kblocks; ++kb) {
-          float s_next = 0.0f;
-          if (kb + 1 < P.kblocks) s_next = __ldg(sa + kb + 1) * __ldg(sb + static_cast<int64_t>(kb + 1) * sb_step);
+        // The half's 128 columns are 64 of CTA 0's columns of B and 64 of CTA 1's: tile columns 64 half .. + 63
+        // and 128 + 64 half .. + 63, in two different blocks of 128. This lane's row of lhs scales, and the two
+        // blocks' scales (out of range: any valid ones).
+        const int my_row = t.r0 + t.m0 + 128 * rank + quarter * 32 + lane;
+        const float* sa = P.sa[t.p] + static_cast<int64_t>(min(my_row, P.rows - 1)) * P.kscales;
+        const float* sb0 = P.sb[t.p] + static_cast<int64_t>(t.e) * P.kscales * P.nscales +
+                           static_cast<int64_t>(t.n0 / 128) * P.sb_n;
+        const float* sb1 = sb0 + (t.n0 / 128 + 1 < P.nscales ? P.sb_n : 0);
+        const int64_t sb_k = P.sb_k;
+        park(strip, 0, w.base); park(strip, 1, w.r0); park(strip, 2, w.r1); park(strip, 3, w.tiles);
+        park(strip, 4, w.upto); park(strip, 5, t.p); park(strip, 6, t.r0); park(strip, 7, t.r1);
+        park(strip, 8, t.m0); park(strip, 9, t.n0); park(strip, 10, u);
+        float a_s = __ldg(sa), b_s0 = __ldg(sb0), b_s1 = __ldg(sb1);
+        for (int left = P.kblocks; left > 0; --left) {
+          const float s0 = a_s * b_s0, s1 = a_s * b_s1;
+          if (left > 1) {  // the next block's scales, ahead of its sums
+            a_s = __ldg(++sa);
+            b_s0 = __ldg(sb0 += sb_k);
+            b_s1 = __ldg(sb1 += sb_k);
+          }
           if (!wait_acc()) { ok = false; break; }
           const uint32_t ta = tacc + acc * TILE_N;
-          // 64 columns on their way at a time (two waits a block: each costs a TMEM latency)
-          uint32_t r0[32], r1[32];
-          const uint64_t ss = pack2(__float_as_uint(s), __float_as_uint(s));
-          tmem_ld32(ta, r0);
-          tmem_ld32(ta + 32, r1);
-          tmem_wait_for(r0);
-          tmem_wait_for(r1);
+          const uint64_t ss0 = pack2(__float_as_uint(s0), __float_as_uint(s0));
+          const uint64_t ss1 = pack2(__float_as_uint(s1), __float_as_uint(s1));
+          // (every sum is pinned behind its load by asm volatile: moved on, the sums' operands do not fit the registers)
 #pragma unroll
-          for (int j = 0; j < 16; ++j) add_scaled(sum[j], r0[2 * j], r0[2 * j + 1], ss);
-          tmem_ld32(ta + 64, r0);
+          for (int c = 0; c < 8; ++c) {
+            uint32_t r[16];
+            tmem_ld16(ta + 16 * c, r);
+            tmem_ld_wait();
+            if (c == 7) free_acc();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) add_scaled(sum[16 + j], r1[2 * j], r1[2 * j + 1], ss);
-          tmem_ld32(ta + 96, r1);
-          tmem_wait_for(r0);
-          tmem_wait_for(r1);
-          free_acc();
-#pragma unroll
-          for (int j = 0; j < 16; ++j) add_scaled(sum[32 + j], r0[2 * j], r0[2 * j + 1], ss);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) add_scaled(sum[48 + j], r1[2 * j], r1[2 * j + 1], ss);
-          s = s_next;
+            for (int j = 0; j < 8; ++j) add_scaled(sum[8 * c + j], r[2 * j], r[2 * j + 1], c < 4 ? ss0 : ss1);
+          }
         }
         if (!ok) break;
-        if (rows > 0 && bytes > 0) {
+        w.base = unpark(strip, 0); w.r0 = unpark(strip, 1); w.r1 = unpark(strip, 2); w.tiles = unpark(strip, 3);
+        w.upto = unpark(strip, 4); t.p = unpark(strip, 5); t.r0 = unpark(strip, 6); t.r1 = unpark(strip, 7);
+        t.m0 = unpark(strip, 8); t.n0 = unpark(strip, 9); u = unpark(strip, 10);
+        __syncwarp();  // (the strip is written again below)
+        const int row = t.m0 + 128 * rank + quarter * 32;  // this warp's first one
+        const int rows = min(32, t.r1 - t.r0 - row);       // (may be negative: nothing to store)
+        const int esize = P.out_dtype == COCO_F32 ? 4 : 2;
+        const int64_t pitch = static_cast<int64_t>(P.n) * esize;
+        const int64_t first = static_cast<int64_t>(t.n0 + 64 * half) * esize;
+        char* out = static_cast<char*>(P.out[t.p]) + (static_cast<int64_t>(t.r0) + row) * pitch + first;
+        const int64_t left = pitch - first;  // bytes from the first column to the row's end
+        if (rows > 0 && left > 0) {
           if (esize == 4) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               uint32_t p[32];
 #pragma unroll
               for (int j = 0; j < 16; ++j) unpack2(sum[16 * c + j], p[2 * j], p[2 * j + 1]);
-              store_strip(strip, p, out + 128 * c, pitch, rows, bytes - 128 * c);
+              const int at = (c >> 1) * 512 + (c & 1) * 128;
+              store_strip(strip, p, out + at, pitch, rows, left - at);
             }
           } else {
 #pragma unroll
@@ -590,11 +644,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 unpack2(sum[32 * c + j], x, y);
                 p[j] = cvt_pair(__uint_as_float(x), __uint_as_float(y), P.out_dtype);
               }
-              store_strip(strip, p, out + 128 * c, pitch, rows, bytes - 128 * c);
+              store_strip(strip, p, out + 256 * c, pitch, rows, left - 256 * c);
             }
           }
         }
       } else {
+        const int esize = P.out_dtype == COCO_F32 ? 4 : 2;
+        const int64_t pitch = static_cast<int64_t>(P.n) * esize;
+        const int m_end = GRAD ? P.k : t.r1 - t.r0;             // rows of the expert's output
+        const int row = t.m0 + 128 * rank + quarter * 32;       // this warp's first one
+        const int rows = min(32, m_end - row);                  // (may be negative: nothing to store)
+        const int col = t.n0 + 128 * half;
+        const int64_t out_row = (GRAD ? static_cast<int64_t>(t.e) * P.k : static_cast<int64_t>(t.r0)) + row;
+        char* out = static_cast<char*>(P.out[t.p]) + out_row * pitch + static_cast<int64_t>(col) * esize;
+        const int64_t bytes = pitch - static_cast<int64_t>(col) * esize;  // left of the row
         const bool none = GRAD && t.r1 == t.r0;
         if (!none && !wait_acc()) { ok = false; break; }
         const uint32_t ta = tacc + acc * TILE_N;
@@ -606,13 +669,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             for (int j = 0; j < 32; ++j) p[j] = 0u;
           } else if (esize == 4) {
             tmem_ld32(ta + 32 * c, p);
-            tmem_wait_for(p);
+            tmem_ld_wait();
           } else {
             uint32_t r0[32], r1[32];
             tmem_ld32(ta + 64 * c, r0);
             tmem_ld32(ta + 64 * c + 32, r1);
-            tmem_wait_for(r0);
-            tmem_wait_for(r1);
+            tmem_ld_wait();
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               p[j] = cvt_pair(__uint_as_float(r0[2 * j]), __uint_as_float(r0[2 * j + 1]), P.out_dtype);
@@ -700,10 +762,13 @@ cudaError_t launch_grouped(const GroupedLaunch& L, cudaStream_t s, unsigned int*
   P.kblocks = (L.k + P.bk - 1) / P.bk;
   P.kscales = (L.k + 127) / 128;
   P.nscales = (L.n + 127) / 128;
-  P.idesc = instruction(L.in_dtype, grad, L.form != GRP_NK, TILE_M, TILE_N);
+  P.sb_k = L.form == GRP_NK ? 1 : P.nscales;
+  P.sb_n = L.form == GRP_NK ? P.kscales : 1;
+  P.idesc = instruction(L.in_dtype, grad, L.form != GRP_NK, TILE_M, fp8 ? 128 : TILE_N);
   // rows along k: an MMA's k values are 32 (e4m3) or 16 rows of 128 bytes; else 32 bytes of a row
   P.bstep = L.form == GRP_NK ? 2 : fp8 ? 256 : 128;
   P.blead = L.form == GRP_NK ? 1 : fp8 ? B_BYTES >> 4 : (B_BYTES / 2) >> 4;
+  P.bhalf = (L.form == GRP_NK ? 64 * BKB : 64) >> 4;  // 64 rows, or 64 bytes of every row
   for (int p = 0; p < L.nprob; ++p) {
     P.out[p] = L.out[p];
     P.sa[p] = L.lhs_scales[p];
