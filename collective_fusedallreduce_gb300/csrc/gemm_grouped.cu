@@ -70,6 +70,7 @@ struct GroupedParams {
   uint32_t bstep;      // B's descriptor advance per MMA, in 16-byte units
   uint32_t blead;      // B's leading byte offset >> 4
   uint32_t bhalf;      // block scales: from the first 64 columns of a CTA's B to the others, in 16-byte units
+  int32_t split;       // few-row kernel: CTAs of a cluster that share a tile's k range
 };
 static_assert(sizeof(GroupedParams) <= 32000, "kernel parameter block too large");
 
@@ -701,6 +702,340 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
 }
 
+// ------------------------------------------------------------ few rows
+//
+// k_grouped_few: rows of lhs by the dozen (decoding, or many experts with a few rows each). The weights are
+// what there is to read, so they are the MMA's M side (128 of their columns n a tile) and the rows its N side
+// (ROWS = 16 or 64): out^T = rhs^T lhs^T, one CTA an MMA, no weight read twice, no idle rows to speak of.
+// Where there are fewer tiles than SMs, a cluster of `split` CTAs shares a tile's k range: each sends its fp32
+// sums for another's rows straight into that CTA's shared memory (st.async, counted on an mbarrier), which
+// adds them in rank order. No atomics, no workspace: repeated calls give the same bits.
+//   warp 0        TMA producer, a ring of 128-byte deep k-blocks: 16 KB of weights, ROWS x 128 bytes of lhs.
+//   warp 1        issues the MMAs and owns TMEM.
+//   warps 2..     epilogue, one per TMEM lane quarter (ROWS = 64: two, 32 rows each): a lane holds one column n.
+
+template <bool SCALED, int ROWS>
+struct FewCfg {
+  static constexpr int W_BYTES = 128 * BKB;
+  static constexpr int STAGE = W_BYTES + ROWS * BKB;
+  static constexpr int RED_BYTES = ROWS * 128 * 4;                   // the cluster's sums for this CTA's rows
+  static constexpr int STAGES = ROWS == 16 ? 11 : 7;
+  static constexpr int EPI_WARPS = ROWS == 16 ? 4 : 8;
+  static constexpr int PER_WARP = ROWS / (EPI_WARPS / 4);            // rows of a warp
+  static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+  static constexpr int ACCS = SCALED ? 4 : 2;                        // accumulator buffers of ROWS columns
+  static constexpr uint32_t COLS = ACCS * ROWS < 32 ? 32 : ACCS * ROWS;
+  static constexpr int RED_OFF = STAGES * STAGE;
+  static constexpr int BAR_OFF = RED_OFF + RED_BYTES;
+  static constexpr int NUM_BARS = 2 * STAGES + 2 * ACCS + 2;         // full, empty; accumulators full, empty; drain; sums
+  static constexpr int SMEM_BYTES = BAR_OFF + 8 * NUM_BARS + 16 + 1024;
+  static_assert(SMEM_BYTES <= 232448, "shared memory over the per-CTA limit");
+};
+constexpr int FEW_N = 128;
+
+template <bool E4M3>
+__device__ __forceinline__ void mma_one(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (E4M3)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    umma(d, a, b, idesc, accumulate);
+}
+
+__device__ __forceinline__ uint32_t mapa(uint32_t addr, int cta) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(cta));
+  return r;
+}
+// Two fp32 values into another CTA's shared memory; their 8 bytes count on that CTA's mbarrier.
+__device__ __forceinline__ void send2(uint32_t addr, float a, float b, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(addr),
+               "r"(__float_as_uint(a)), "r"(__float_as_uint(b)), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ bool wait_bar_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  const uint64_t t0 = globaltimer();
+  for (uint32_t it = 1;; ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((it & 31) == 0 && (*abort_flag || globaltimer() - t0 > kTimeoutNs)) return false;
+  }
+}
+
+// Sends this thread's sums (column `n_lane` of 128, PER_WARP rows from row0 on) to the CTAs that own the rows: CTA d
+// of SPLIT owns OWN = ROWS / SPLIT rows from d * OWN on (OWN divides PER_WARP). Layout there: [source][pair of
+// rows][column][2].
+template <int PER_WARP, int OWN>
+__device__ __forceinline__ void send_sums(const float (&sum)[PER_WARP], uint32_t red, uint32_t bar, int rank, int row0,
+                                          int n_lane) {
+#pragma unroll
+  for (int d = 0; d < PER_WARP / OWN; ++d) {
+    const int cta = row0 / OWN + d;
+    const uint32_t to = mapa(red, cta) + static_cast<uint32_t>(rank * (OWN / 2) * 128 + n_lane) * 8;
+    const uint32_t b = mapa(bar, cta);
+#pragma unroll
+    for (int j = 0; j < OWN / 2; ++j) send2(to + j * 128 * 8, sum[d * OWN + 2 * j], sum[d * OWN + 2 * j + 1], b);
+  }
+}
+
+__device__ __forceinline__ void store_one(void* out, int64_t i, int dtype, float v) {
+  if (dtype == COCO_F32) static_cast<float*>(out)[i] = v;
+  else if (dtype == COCO_F16) static_cast<__half*>(out)[i] = __float2half_rn(v);
+  else static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
+}
+
+template <bool SCALED, int ROWS>
+__global__ void __launch_bounds__(FewCfg<SCALED, ROWS>::THREADS, 1) k_grouped_few(const __grid_constant__ GroupedParams P) {
+  using C = FewCfg<SCALED, ROWS>;
+  constexpr int STAGES_ = C::STAGES, ACCS = C::ACCS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + C::BAR_OFF;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES_ + s); };
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * STAGES_ + a); };
+  auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * STAGES_ + ACCS + a); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES_ + 2 * ACCS), red_bar = drain_bar + 8u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::BAR_OFF + 8 * C::NUM_BARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::BAR_OFF + 8 * C::NUM_BARS + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = P.split;
+  const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int cluster_id = blockIdx.x / split, nclusters = gridDim.x / split;
+  // this CTA's part of every tile's k range
+  const int kb0 = static_cast<int>(static_cast<int64_t>(P.kblocks) * rank / split);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(P.kblocks) * (rank + 1) / split);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES_; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < ACCS; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), C::EPI_WARPS);
+    }
+    mbar_init(drain_bar, 1);
+    mbar_init(red_bar, 1);
+    if (split > 1) mbar_expect_tx(red_bar, C::RED_BYTES);  // (a cluster has at most one tile then)
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc<false>(smem_u32(tmem_slot), C::COLS);
+  tc_fence_before();
+  if (split > 1) cluster_sync();  // peers' barriers exist before sums arrive on them
+  else __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  auto fail = [&]() {
+    *abort_flag = 1;
+    atomicCAS(P.err, 0u, static_cast<unsigned int>(COCO_ERR_TIMEOUT));
+  };
+  int dummy = 0;
+  volatile int* never = &dummy;
+
+  if (warp == 0) {
+    // -------------------------------------------------------- TMA producer
+    const bool leader = elect_one();
+    Walk w;
+    walk_load<false>(P, w, 0, 0, ROWS, FEW_N);
+    Tile t;
+    int stage = 0;
+    uint32_t phase = 0, issued = 0, parity = 0;
+    bool ok = true;
+    for (int u = cluster_id; ok && walk_find<false>(P, w, u, t, ROWS, FEW_N); u += nclusters) {
+      const CUtensorMap *mx = &P.a[t.p], *mw = &P.b[t.p];
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!wait_bar_warp(empty_bar(stage), phase ^ 1u, abort_flag)) {
+          if (leader) fail();
+          ok = false;
+          break;
+        }
+        if (leader) {
+          const uint32_t sw = sbase + stage * C::STAGE, sx = sw + C::W_BYTES;
+          const int k0 = kb * P.bk;
+          mbar_expect_tx(full_bar(stage), C::STAGE);
+          if (P.form == GRP_NK) {
+            tma_load_3d(sw, mw, full_bar(stage), k0, t.n0, t.e);
+          } else {
+            tma_load_3d(sw, mw, full_bar(stage), t.n0, k0, t.e);
+            if constexpr (!SCALED) tma_load_3d(sw + C::W_BYTES / 2, mw, full_bar(stage), t.n0 + 64, k0, t.e);
+          }
+          tma_load_3d(sx, mx, full_bar(stage), k0, t.r0 + t.m0, 0);
+        }
+        __syncwarp();
+        issued |= 1u << stage;
+        parity = (parity & ~(1u << stage)) | (phase << stage);
+        if (++stage == STAGES_) { stage = 0; phase ^= 1u; }
+      }
+    }
+    if (!ok)  // let copies in flight land
+      for (int s = 0; s < STAGES_; ++s)
+        if ((issued >> s) & 1u) wait_bar_warp(full_bar(s), (parity >> s) & 1u, never);
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    const bool leader = elect_one();
+    const uint32_t idesc = P.idesc, wstep = P.bstep;
+    const uint64_t wd0 = tile_desc(sbase, P.blead), xd0 = tile_desc(sbase + C::W_BYTES, 1);
+    const int total = walk_total<false>(P, ROWS, FEW_N);
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, accph = 0;
+    bool ok = true, any_mma = false;
+    auto wait = [&](uint32_t bar, uint32_t par) {
+      if (!wait_bar_warp(bar, par, abort_flag)) {
+        if (leader) fail();
+        return false;
+      }
+      tc_fence_after();
+      return true;
+    };
+    for (int u = cluster_id; ok && u < total; u += nclusters) {
+      if (!SCALED && !wait(tempty_bar(acc), accph ^ 1u)) { ok = false; break; }
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (SCALED && !wait(tempty_bar(acc), accph ^ 1u)) { ok = false; break; }
+        if (!wait(full_bar(stage), phase)) { ok = false; break; }
+        if (leader) {
+          const uint64_t off = static_cast<uint64_t>(stage * (C::STAGE >> 4));
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_one<SCALED>(tmem_base + acc * ROWS, wd0 + off + wstep * k, xd0 + off + 2 * k, idesc,
+                            SCALED ? k != 0 : (kb != kb0 || k != 0));
+          umma_commit(empty_bar(stage));
+          if (SCALED || kb + 1 == kb1) umma_commit(tfull_bar(acc));
+        }
+        __syncwarp();
+        any_mma = true;
+        if (SCALED || kb + 1 == kb1)
+          if (++acc == ACCS) { acc = 0; accph ^= 1u; }
+        if (++stage == STAGES_) { stage = 0; phase ^= 1u; }
+      }
+    }
+    if (!ok && any_mma) {  // wait for the MMAs already issued before TMEM is freed
+      if (leader) umma_commit(drain_bar);
+      __syncwarp();
+      wait_bar_warp(drain_bar, 0, never);
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int quarter = warp & 3;
+    const int n_lane = quarter * 32 + lane;  // this lane's column of the tile
+    constexpr int PW = C::PER_WARP, HALVES = C::EPI_WARPS / 4;
+    const int half = (warp - 2) >> 2, row0 = half * PW;  // this warp's rows of the tile
+    const uint32_t tacc = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + row0;
+    Walk w;
+    walk_load<false>(P, w, 0, 0, ROWS, FEW_N);
+    Tile t;
+    int acc = 0;
+    uint32_t accph = 0;
+    bool ok = true;
+    auto wait_acc = [&]() {
+      const bool ready = __all_sync(0xffffffffu, wait_bar(tfull_bar(acc), accph, abort_flag));
+      if (!ready && lane == 0) fail();
+      tc_fence_after();
+      return ready;
+    };
+    auto load_acc = [&](uint32_t (&r)[PW]) {  // and hands the accumulator back
+      if constexpr (PW == 16) tmem_ld16(tacc + acc * ROWS, r);
+      else tmem_ld32(tacc + acc * ROWS, r);
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_relaxed(tempty_bar(acc));
+      if (++acc == ACCS) { acc = 0; accph ^= 1u; }
+    };
+    for (int u = cluster_id; ok && walk_find<false>(P, w, u, t, ROWS, FEW_N); u += nclusters) {
+      float sum[PW];
+      uint32_t r[PW];
+      if constexpr (SCALED) {
+#pragma unroll
+        for (int j = 0; j < PW; ++j) sum[j] = 0.0f;
+        // lane l holds the lhs scale of the warp's row l times the tile's rhs scale (its 128 columns are one block),
+        // and it is passed around by shuffles. Rows past the end: any valid row's.
+        const float* sa = P.sa[t.p] + static_cast<int64_t>(min(t.r0 + t.m0 + row0 + lane, P.rows - 1)) * P.kscales;
+        const float* sb = P.sb[t.p] + static_cast<int64_t>(t.e) * P.kscales * P.nscales +
+                          static_cast<int64_t>(t.n0 / 128) * P.sb_n;
+        auto scale = [&](int kb) { return __ldg(sa + kb) * __ldg(sb + static_cast<int64_t>(kb) * P.sb_k); };
+        float s = scale(kb0);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          const float s_next = scale(kb + 1 < kb1 ? kb + 1 : kb);
+          if (!wait_acc()) { ok = false; break; }
+          load_acc(r);
+#pragma unroll
+          for (int j = 0; j < PW; ++j) sum[j] = fmaf(__uint_as_float(r[j]), __shfl_sync(0xffffffffu, s, j), sum[j]);
+          s = s_next;
+        }
+        if (!ok) break;
+      } else {
+        if (!wait_acc()) { ok = false; break; }
+        load_acc(r);
+#pragma unroll
+        for (int j = 0; j < PW; ++j) sum[j] = __uint_as_float(r[j]);
+      }
+      const int n = t.n0 + n_lane;
+      const int rows = t.r1 - t.r0 - t.m0;  // of this tile (at least one)
+      const int64_t at = (static_cast<int64_t>(t.r0) + t.m0) * P.n + n;
+      void* out = P.out[t.p];
+      if (split == 1) {
+#pragma unroll
+        for (int j = 0; j < PW; ++j)
+          if (row0 + j < rows && n < P.n)
+            store_one(out, at + static_cast<int64_t>(row0 + j) * P.n, P.out_dtype, sum[j]);
+      } else {
+        const uint32_t red = sbase + C::RED_OFF;
+        if (split == 2) send_sums<PW, ROWS / 2>(sum, red, red_bar, rank, row0, n_lane);
+        else if (split == 4) send_sums<PW, ROWS / 4>(sum, red, red_bar, rank, row0, n_lane);
+        else send_sums<PW, ROWS / 8>(sum, red, red_bar, rank, row0, n_lane);
+        const bool all = __all_sync(0xffffffffu, wait_bar_cluster(red_bar, 0, abort_flag));
+        if (!all) {
+          if (lane == 0) fail();
+          ok = false;
+          break;
+        }
+        const int own = ROWS / split;
+        for (int j = half; j < own / 2; j += HALVES) {
+          float x = 0.0f, y = 0.0f;
+          for (int src = 0; src < split; ++src) {
+            const uint32_t a = red + static_cast<uint32_t>((src * (own / 2) + j) * 128 + n_lane) * 8;
+            float px, py;
+            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(px), "=f"(py) : "r"(a) : "memory");
+            x += px;
+            y += py;
+          }
+          const int row = rank * own + 2 * j;
+          if (n < P.n && row < rows) store_one(out, at + static_cast<int64_t>(row) * P.n, P.out_dtype, x);
+          if (n < P.n && row + 1 < rows) store_one(out, at + static_cast<int64_t>(row + 1) * P.n, P.out_dtype, y);
+        }
+      }
+    }
+    if (P.offsets)
+      clear_rest(P, static_cast<int64_t>(blockIdx.x) * (C::THREADS - 64) + threadIdx.x - 64,
+                 static_cast<int64_t>(gridDim.x) * (C::THREADS - 64));
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (split > 1) cluster_sync();  // no CTA leaves while its peers may still write its shared memory
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc<false>(tmem_base, C::COLS);
+  }
+}
+
 // ------------------------------------------------------------------- host
 
 // A dense [d2][d1][d0] array of 1- or 2-byte elements in boxes of box0 x box1, 128-byte swizzle, zeros outside.
@@ -720,7 +1055,7 @@ bool encode(CUtensorMap* map, const void* ptr, int dtype, int64_t d0, int64_t d1
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-std::atomic<bool> smem_set[3][64];
+std::atomic<bool> smem_set[7][64];
 
 cudaError_t allow_smem(const void* kernel, int which, int bytes) {
   int dev = 0;
@@ -743,6 +1078,71 @@ uint32_t instruction(int dtype, bool a_mn, bool b_mn, int m, int n) {
 
 }  // namespace
 
+// Which kernel, and how many CTAs share a tile's k range.
+struct Choice {
+  int rows;   // 16 or 64: k_grouped_few with that many rows a tile; 0: k_grouped_pair
+  int split;
+  int64_t units;
+};
+
+// The time of each kernel is the k-blocks that its busiest SM goes through, times what one takes there, and the
+// choice is the least product. Measured on a GB300, in ns a k-block (128 bytes of k): pairs 450 to 570 in e4m3 and
+// 290 to 420 in 16 bits, by how many run; few rows 250 / 230 with 16 and 350 / 260 with 64 rows while the weights
+// come from few SMs, and the HBM's time for 16 KB from each active SM (some 350 with all of them) beyond that; 1900
+// once for a shared k range. Both sides, one call from a graph, k = n = 4096 in e4m3: 1 row 7.3 us (16 rows, four
+// CTAs a tile) and 18.3 us (pairs); 64 rows 9.7 and 19.1; 256 rows 17.5 and 19.2; 512 rows 31.1 and 19.6. 64
+// experts, k 4096, n 2048 stored [n][k]: 32 rows 29.6 and 36.8 us, 256 rows 81 and 110, 1024 rows 117 and 115,
+// 4096 rows 296 and 133.
+Choice choose(const GroupedLaunch& L, int kblocks) {
+  const bool fp8 = L.in_dtype == COCO_F8E4M3;
+  const int64_t pair_ns = fp8 ? 520 : 400, few16_ns = fp8 ? 250 : 230, few64_ns = fp8 ? 350 : 260, split_ns = 1900;
+  const int sms = sm_count();
+  auto tiles = [&](int tm, int tn) {  // at most one partly filled tile per expert beyond the full ones
+    const int64_t by_rows = static_cast<int64_t>(L.rows / tm) + (L.experts < L.rows ? L.experts : L.rows);
+    const int64_t mts = L.offsets ? by_rows : (static_cast<int64_t>(L.rows) + tm - 1) / tm;
+    return L.nprob * mts * ((L.n + tn - 1) / tn);
+  };
+  auto waves = [](int64_t n, int64_t at_once) { return (n + at_once - 1) / at_once; };
+  Choice best{0, 1, tiles(TILE_M, TILE_N)};
+  int64_t least = waves(best.units, sms / 2) * kblocks * pair_ns;
+  for (int rows : {16, 64}) {
+    const int64_t units = tiles(rows, FEW_N);
+    for (int split = 1; split <= 8 && split <= kblocks; split *= 2) {
+      if (split > 1 && units * split > sms) break;  // (a cluster that shares a tile has no second one)
+      const int64_t active = units * split < sms ? units * split : sms;
+      const int64_t hbm = active * 16384 / 7000, lat = rows == 16 ? few16_ns : few64_ns;
+      const int64_t ns = waves(units * split, sms) * ((kblocks + split - 1) / split) * (hbm > lat ? hbm : lat) +
+                         (split > 1 ? split_ns : 0);
+      if (ns < least) {
+        least = ns;
+        best = Choice{rows, split, units};
+      }
+    }
+  }
+  return best;
+}
+
+template <bool SCALED, int ROWS>
+cudaError_t launch_few(const GroupedParams& P, const Choice& c, int which, cudaStream_t s) {
+  using C = FewCfg<SCALED, ROWS>;
+  void (*kernel)(const GroupedParams) = k_grouped_few<SCALED, ROWS>;
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), which, C::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  const int64_t ctas = c.split > 1 ? c.units * c.split : c.units < sm_count() ? c.units : sm_count();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = c.split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = c.split > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, P);
+}
+
 cudaError_t launch_grouped(const GroupedLaunch& L, cudaStream_t s, unsigned int* err_word) {
   // coordinates of a tile's last rows and columns stay within 32 bits
   const int32_t most = INT32_MAX - 1024;
@@ -764,7 +1164,11 @@ cudaError_t launch_grouped(const GroupedLaunch& L, cudaStream_t s, unsigned int*
   P.nscales = (L.n + 127) / 128;
   P.sb_k = L.form == GRP_NK ? 1 : P.nscales;
   P.sb_n = L.form == GRP_NK ? P.kscales : 1;
-  P.idesc = instruction(L.in_dtype, grad, L.form != GRP_NK, TILE_M, fp8 ? 128 : TILE_N);
+  const Choice few = grad ? Choice{0, 1, 0} : choose(L, P.kblocks);
+  P.split = few.split;
+  // few rows: the rhs is the M side and the lhs the N side
+  P.idesc = few.rows ? instruction(L.in_dtype, L.form != GRP_NK, false, FEW_N, few.rows)
+                     : instruction(L.in_dtype, grad, L.form != GRP_NK, TILE_M, fp8 ? 128 : TILE_N);
   // rows along k: an MMA's k values are 32 (e4m3) or 16 rows of 128 bytes; else 32 bytes of a row
   P.bstep = L.form == GRP_NK ? 2 : fp8 ? 256 : 128;
   P.blead = L.form == GRP_NK ? 1 : fp8 ? B_BYTES >> 4 : (B_BYTES / 2) >> 4;
@@ -779,10 +1183,17 @@ cudaError_t launch_grouped(const GroupedLaunch& L, cudaStream_t s, unsigned int*
       good = encode(&P.a[p], L.lhs[p], L.in_dtype, L.k, L.rows, 1, 64, 64) &&
              encode(&P.b[p], L.rhs[p], L.in_dtype, L.n, L.rows, 1, 64, 64);
     else
-      good = encode(&P.a[p], L.lhs[p], L.in_dtype, L.k, L.rows, 1, bk, 128) &&
+      good = encode(&P.a[p], L.lhs[p], L.in_dtype, L.k, L.rows, 1, bk, few.rows ? few.rows : 128) &&
              (L.form == GRP_NK ? encode(&P.b[p], L.rhs[p], L.in_dtype, L.k, L.n, L.experts, bk, 128)
                                : encode(&P.b[p], L.rhs[p], L.in_dtype, L.n, L.k, L.experts, bk, bk));
     if (!good) return cudaErrorNotSupported;
+  }
+  if (few.rows) {
+    const cudaError_t e = few.rows == 16 ? (fp8 ? launch_few<true, 16>(P, few, 3, s) : launch_few<false, 16>(P, few, 4, s))
+                                         : (fp8 ? launch_few<true, 64>(P, few, 5, s) : launch_few<false, 64>(P, few, 6, s));
+    if (e != cudaSuccess) return e;
+    count_launch();
+    return cudaGetLastError();
   }
   // at most one partly filled tile per expert beyond the full ones
   const int64_t mts = grad ? static_cast<int64_t>(L.experts) * ((L.k + TILE_M - 1) / TILE_M)
