@@ -75,7 +75,7 @@ struct NormTables {
   int32_t nhidden[COCO_MAX_PTRS], nnormed[COCO_MAX_PTRS];
 };
 
-constexpr int kNormMaxCols = 65536;  // a row stays in its block's registers
+constexpr int kNormMaxCols = 32768;  // a row stays in its block's registers
 
 struct NormLaunch {
   NormTables t;

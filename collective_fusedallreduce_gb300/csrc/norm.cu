@@ -38,7 +38,9 @@ __device__ __forceinline__ uint4 ld_stream(const void* p) {
   return r;
 }
 
-// Eight consecutive elements as loaded, and their conversions from and to fp32.
+// Eight consecutive elements as loaded, and their conversions from and to fp32. Stores are streaming ones,
+// which keeps outputs from displacing what is still to be read (the gradient, 8192 x 4096 fp16 on eight ranks: 118 to
+// 116 us; in the quantiser the same cost 15 %, and it stores plainly).
 template <typename T>
 struct Chunk {
   uint4 v;
@@ -70,7 +72,7 @@ struct Chunk {
     }
     v = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  __device__ __forceinline__ void store(void* base, int64_t c) const { static_cast<uint4*>(base)[c] = v; }
+  __device__ __forceinline__ void store(void* base, int64_t c) const { __stcs(static_cast<uint4*>(base) + c, v); }
 };
 
 template <>
@@ -94,8 +96,8 @@ struct Chunk<float> {
     w = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
   }
   __device__ __forceinline__ void store(void* base, int64_t c) const {
-    static_cast<uint4*>(base)[2 * c] = v;
-    static_cast<uint4*>(base)[2 * c + 1] = w;
+    __stcs(static_cast<uint4*>(base) + 2 * c, v);
+    __stcs(static_cast<uint4*>(base) + 2 * c + 1, w);
   }
 };
 
@@ -116,13 +118,33 @@ __device__ __forceinline__ float chunk_amax(const float (&f)[kChunk]) {
 // The scale of a block whose largest magnitude is `amax`: the largest e4m3 value stands for that magnitude.
 __device__ __forceinline__ float scale_of(float amax) { return __fdiv_rn(max_nan(amax, kAmaxFloor), kE4m3Max); }
 
-// Eight values over a block's scale, in e4m3 (round to nearest even). The quotient is a product with the
-// scale's reciprocal: at most an ulp of fp32 from the division, against the 2^-4 steps of the format.
-__device__ __forceinline__ uint2 to_e4m3(const float (&f)[kChunk], float inv) {
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+
+// Eight values over a block's scale, in e4m3 (round to nearest even). The quotient is the value times the
+// scale's rounded reciprocal, corrected by its own residual (Markstein, "Computation of elementary functions on
+// the IBM RISC System/6000 processor", 1990), which makes it the rounded quotient: with the product alone, one
+// value in some hundred thousand falls on the other side of a rounding boundary. An infinite scale keeps the
+// uncorrected product (0, or NaN for the infinity itself).
+__device__ __forceinline__ uint2 to_e4m3(const float (&f)[kChunk], float scale) {
+  const float inv = __frcp_rn(scale);
+  const float s = inv == 0.0f ? 0.0f : -scale;
+  const uint64_t inv2 = pack2(inv, inv), s2 = pack2(s, s);  // (two values an instruction)
   uint32_t h[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    h[i] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * i] * inv, f[2 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t f2 = pack2(f[2 * i], f[2 * i + 1]);
+    uint64_t q2, r2;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q2) : "l"(f2), "l"(inv2));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r2) : "l"(q2), "l"(s2), "l"(f2));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(q2) : "l"(r2), "l"(inv2));
+    float2 q;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(q.x), "=f"(q.y) : "l"(q2));
+    h[i] = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+  }
   return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
@@ -192,9 +214,12 @@ struct NormArgs {
   float* rstd;
 };
 
-// Grid x: rows (blockDim / tpr a block), grid y: groups.
-template <typename T, int NR, int VPT, bool FP8, int MAX_THREADS>
-__global__ void __launch_bounds__(MAX_THREADS) k_allreduce_rmsnorm(const __grid_constant__ NormArgs a) {
+// Grid x: rows (blockDim / tpr a block), grid y: groups. A row's loads, its barrier and its stores do not overlap,
+// so what keeps HBM busy is other blocks on the SM: four of 512 threads (16-bit types, the compiler held to 32
+// registers) took 8192 x 4096 fp16 on eight ranks, eight copies, from 233 to 213 us (6.64 TB/s); three had not
+// been enough.
+template <typename T, int NR, int VPT, bool FP8>
+__global__ void __launch_bounds__(512, VPT == 1 && NR > 0 && sizeof(T) == 2 ? 4 : 1) k_allreduce_rmsnorm(const __grid_constant__ NormArgs a) {
   __shared__ float red[2][32];
   const int g = blockIdx.y;
   const int tpr = 1 << a.tpr_log2;
@@ -260,10 +285,10 @@ __global__ void __launch_bounds__(MAX_THREADS) k_allreduce_rmsnorm(const __grid_
         for (int x = kBlockLanes / 2; x; x >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, x));
         if (mine) {
           const float s = scale_of(m);
-          const uint2 q8 = to_e4m3(y, __frcp_rn(s));
+          const uint2 q8 = to_e4m3(y, s);
           const int64_t so = row * a.nblocks + c / kBlockLanes;
           for (int q = 0; q < nnormed; ++q) {
-            static_cast<uint2*>(a.t.normed[slot0 + q])[c0 + c] = q8;
+            __stcs(static_cast<uint2*>(a.t.normed[slot0 + q]) + c0 + c, q8);
             if (c % kBlockLanes == 0) a.t.scales[slot0 + q][so] = s;
           }
         }
@@ -299,10 +324,16 @@ struct NormBwdArgs {
   float* partial;  // [gridDim.y * gridDim.x][cols]
 };
 
-template <typename T, int NR, int VPT, int MAX_THREADS>
-__global__ void __launch_bounds__(MAX_THREADS) k_rmsnorm_backward(const __grid_constant__ NormBwdArgs a) {
+// Rows so wide that a thread has kSharedDw chunks or more keep the dw sums in shared memory (each thread its own
+// columns') and read dhidden only when it is added: their registers hold the row's g and h.
+constexpr int kSharedDw = 4;
+
+template <typename T, int NR, int VPT>
+__global__ void __launch_bounds__(512) k_rmsnorm_backward(const __grid_constant__ NormBwdArgs a) {
+  constexpr bool WIDE = VPT >= kSharedDw;
   __shared__ float red[2][32];
   __shared__ float slots[VPT == 1 ? 256 * kChunk : 1];  // several rows a block (narrow rows): their dw, to be joined
+  extern __shared__ float4 wide_dw[];                   // [2 * nchunks]
   const int g = blockIdx.y;
   const int tpr = 1 << a.tpr_log2;
   const int t = threadIdx.x & (tpr - 1), slot = threadIdx.x >> a.tpr_log2, rpb = blockDim.x >> a.tpr_log2;
@@ -310,11 +341,17 @@ __global__ void __launch_bounds__(MAX_THREADS) k_rmsnorm_backward(const __grid_c
   const void* dhidden = a.dhidden[g];
   const void* hidden = a.hidden[g];
   const float inv_cols = 1.0f / static_cast<float>(a.cols);
-  float dw[VPT][kChunk];
+  float dw[WIDE ? 1 : VPT][kChunk];
 #pragma unroll
-  for (int i = 0; i < VPT; ++i)
+  for (int i = 0; i < VPT; ++i) {
+    if constexpr (WIDE) {
+      const int c = t + i * tpr;
+      if (c < a.nchunks) wide_dw[2 * c] = wide_dw[2 * c + 1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    } else {
 #pragma unroll
-    for (int j = 0; j < kChunk; ++j) dw[i][j] = 0.0f;
+      for (int j = 0; j < kChunk; ++j) dw[i][j] = 0.0f;
+    }
+  }
   int turn = 0;
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * rpb; base < a.rows;
        base += static_cast<int64_t>(gridDim.x) * rpb, turn ^= 1) {
@@ -322,27 +359,43 @@ __global__ void __launch_bounds__(MAX_THREADS) k_rmsnorm_backward(const __grid_c
     const bool live = row < a.rows;
     const int64_t c0 = row * a.nchunks;
     const float rstd = live ? a.rstd[g * a.rows + row] : 0.0f;
-    float gr[VPT][kChunk], xh[VPT][kChunk];
-    Chunk<T> dh[VPT];
+    float gr[VPT][kChunk];
+    Chunk<T> hv[WIDE ? VPT : 1], dh[WIDE ? 1 : VPT];  // (narrow rows keep xhat itself)
+    float xk[WIDE ? 1 : VPT][kChunk];
     float along = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = t + i * tpr;
       if (live && c < a.nchunks) {
-        Chunk<T> hv, wv;
-        hv.load(hidden, c0 + c);
-        if (dhidden) dh[i].load(dhidden, c0 + c);
+        Chunk<T> wv;
+        Chunk<T>& h = hv[WIDE ? i : 0];
+        h.load(hidden, c0 + c);
+        if constexpr (!WIDE)
+          if (dhidden) dh[i].load(dhidden, c0 + c);
         wv.load_cached(a.weight, c);
         sum_ranks<T, NR>(in, a.nranks, c0 + c, gr[i]);
-        hv.get(xh[i]);
-        float w[kChunk];
+        float w[kChunk], xh[kChunk], d[kChunk];
+        h.get(xh);
         wv.get(w);
 #pragma unroll
         for (int j = 0; j < kChunk; ++j) {
-          xh[i][j] *= rstd;
-          dw[i][j] = fmaf(gr[i][j], xh[i][j], dw[i][j]);
+          xh[j] *= rstd;
+          if constexpr (!WIDE) xk[i][j] = xh[j];
+          d[j] = gr[i][j];
           gr[i][j] *= w[j];
-          along = fmaf(gr[i][j], xh[i][j], along);
+          along = fmaf(gr[i][j], xh[j], along);
+        }
+        if constexpr (WIDE) {
+          float4 u = wide_dw[2 * c], v = wide_dw[2 * c + 1];
+          u.x = fmaf(d[0], xh[0], u.x); u.y = fmaf(d[1], xh[1], u.y);
+          u.z = fmaf(d[2], xh[2], u.z); u.w = fmaf(d[3], xh[3], u.w);
+          v.x = fmaf(d[4], xh[4], v.x); v.y = fmaf(d[5], xh[5], v.y);
+          v.z = fmaf(d[6], xh[6], v.z); v.w = fmaf(d[7], xh[7], v.w);
+          wide_dw[2 * c] = u;
+          wide_dw[2 * c + 1] = v;
+        } else {
+#pragma unroll
+          for (int j = 0; j < kChunk; ++j) dw[i][j] = fmaf(d[j], xh[j], dw[i][j]);
         }
       }
     }
@@ -351,15 +404,25 @@ __global__ void __launch_bounds__(MAX_THREADS) k_rmsnorm_backward(const __grid_c
     for (int i = 0; i < VPT; ++i) {
       const int c = t + i * tpr;
       if (live && c < a.nchunks) {
-        float f[kChunk], o[kChunk];
+        float f[kChunk], o[kChunk], xh[kChunk];
         if (dhidden) {
-          dh[i].get(f);
+          if constexpr (WIDE) {
+            Chunk<T> late;
+            late.load(dhidden, c0 + c);
+            late.get(f);
+          } else {
+            dh[i].get(f);
+          }
         } else {
 #pragma unroll
           for (int j = 0; j < kChunk; ++j) f[j] = 0.0f;
         }
+        if constexpr (WIDE) hv[i].get(xh);
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j) o[j] = fmaf(rstd, gr[i][j] - xh[i][j] * along, f[j]);
+        for (int j = 0; j < kChunk; ++j) {
+          const float x = WIDE ? xh[j] * rstd : xk[WIDE ? 0 : i][j];
+          o[j] = fmaf(rstd, gr[i][j] - x * along, f[j]);
+        }
         Chunk<T> ov;
         ov.put(o);
         for (int q = 0; q < a.ndx[g]; ++q) ov.store(a.dx[g * a.nranks + q], c0 + c);
@@ -383,9 +446,14 @@ __global__ void __launch_bounds__(MAX_THREADS) k_rmsnorm_backward(const __grid_c
     for (int i = 0; i < VPT; ++i) {
       const int c = t + i * tpr;
       if (c < a.nchunks) {
-        Chunk<float> o;
-        o.put(dw[i]);
-        o.store(out, c);
+        if constexpr (WIDE) {
+          reinterpret_cast<float4*>(out)[2 * c] = wide_dw[2 * c];
+          reinterpret_cast<float4*>(out)[2 * c + 1] = wide_dw[2 * c + 1];
+        } else {
+          Chunk<float> o;
+          o.put(dw[i]);
+          o.store(out, c);
+        }
       }
     }
   }
@@ -445,17 +513,20 @@ __global__ void __launch_bounds__(256) k_quantize_rows(const __grid_constant__ Q
     for (int s = kBlockLanes / 2; s; s >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, s));
     if (mine) {
       const float s = scale_of(m);
-      q[row * a.nchunks + c] = to_e4m3(f, __frcp_rn(s));
+      q[row * a.nchunks + c] = to_e4m3(f, s);
       if (c % kBlockLanes == 0) scales[row * a.nblocks + c / kBlockLanes] = s;
     }
   }
 }
 
-// One scale per 128 rows x 128 columns: a block of 256 threads holds the tile (8 chunks a thread) in registers
-// between its maximum and its rounding. Grid x: tiles, row-major; grid y: tensors.
+// One scale per 128 rows x 128 columns: a block holds the tile in registers (kTileThreads threads, kTileChunks
+// chunks each) between its maximum and its rounding. 8192 x 32768 in bf16: 136 us (5.94 TB/s), bound by HBM; four
+// blocks of 256 threads an SM (512 or 1024 threads a tile: 154 to 217 us). Grid x: tiles, row-major; grid y: tensors.
+constexpr int kTileThreads = 256, kTileRows = kTileThreads / kBlockLanes, kTileChunks = 128 / kTileRows;
+
 template <typename T>
-__global__ void __launch_bounds__(256) k_quantize_tiles(const __grid_constant__ QuantArgs a) {
-  __shared__ float red[2][8];
+__global__ void __launch_bounds__(kTileThreads, 4) k_quantize_tiles(const __grid_constant__ QuantArgs a) {
+  __shared__ float red[2][kTileThreads / 32];
   const void* x = a.x[blockIdx.y];
   uint2* q = static_cast<uint2*>(a.q[blockIdx.y]);
   float* scales = a.scales[blockIdx.y];
@@ -465,15 +536,15 @@ __global__ void __launch_bounds__(256) k_quantize_tiles(const __grid_constant__ 
     const int64_t tr = tile / a.nblocks;
     const int c = static_cast<int>(tile - tr * a.nblocks) * kBlockLanes + (threadIdx.x & (kBlockLanes - 1));
     const int64_t r0 = tr * 128 + threadIdx.x / kBlockLanes;
-    Chunk<T> v[8];
+    Chunk<T> v[kTileChunks];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (c < a.nchunks && r0 + 16 * i < a.rows) v[i].load(x, (r0 + 16 * i) * a.nchunks + c);
+    for (int i = 0; i < kTileChunks; ++i) {
+      if (c < a.nchunks && r0 + kTileRows * i < a.rows) v[i].load(x, (r0 + kTileRows * i) * a.nchunks + c);
       else v[i].zero();
     }
     float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kTileChunks; ++i) {
       float f[kChunk];
       v[i].get(f);
       m = max_nan(m, chunk_amax(f));
@@ -483,14 +554,14 @@ __global__ void __launch_bounds__(256) k_quantize_tiles(const __grid_constant__ 
     if ((threadIdx.x & 31) == 0) red[turn][threadIdx.x >> 5] = m;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max_nan(m, red[turn][i]);
-    const float s = scale_of(m), inv = __frcp_rn(s);
+    for (int i = 0; i < kTileThreads / 32; ++i) m = max_nan(m, red[turn][i]);
+    const float s = scale_of(m);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (c < a.nchunks && r0 + 16 * i < a.rows) {
+    for (int i = 0; i < kTileChunks; ++i) {
+      if (c < a.nchunks && r0 + kTileRows * i < a.rows) {
         float f[kChunk];
         v[i].get(f);
-        q[(r0 + 16 * i) * a.nchunks + c] = to_e4m3(f, inv);
+        q[(r0 + kTileRows * i) * a.nchunks + c] = to_e4m3(f, s);
       }
     }
     if (threadIdx.x == 0) scales[tile] = s;
@@ -499,8 +570,8 @@ __global__ void __launch_bounds__(256) k_quantize_tiles(const __grid_constant__ 
 
 // --------------------------------------------------------------- launchers
 
-// Threads of a row: a power of two that covers its chunks, at most 512 while a thread then holds up to eight
-// chunks, else 1024 (rows of up to 65536 columns).
+// Threads of a row: a power of two that covers its chunks, at most 512, each with up to eight chunks (rows of up to
+// 32768 columns).
 struct RowShape {
   int tpr_log2, vpt, threads, rpb;
 };
@@ -508,7 +579,6 @@ RowShape row_shape(int nchunks) {
   RowShape s;
   s.tpr_log2 = 5;
   while (s.tpr_log2 < 9 && (1 << s.tpr_log2) < nchunks) ++s.tpr_log2;
-  if (nchunks > 8 * 512) s.tpr_log2 = 10;
   const int tpr = 1 << s.tpr_log2;
   s.vpt = 1;
   while (s.vpt * tpr < nchunks) s.vpt *= 2;
@@ -517,22 +587,21 @@ RowShape row_shape(int nchunks) {
   return s;
 }
 
-template <typename T, int NR, int VPT, int MT>
+template <typename T, int NR, int VPT>
 cudaError_t norm_go(const NormArgs& a, bool fp8, dim3 grid, int threads, cudaStream_t s) {
-  if (fp8) k_allreduce_rmsnorm<T, NR, VPT, true, MT><<<grid, threads, 0, s>>>(a);
-  else k_allreduce_rmsnorm<T, NR, VPT, false, MT><<<grid, threads, 0, s>>>(a);
+  if (fp8) k_allreduce_rmsnorm<T, NR, VPT, true><<<grid, threads, 0, s>>>(a);
+  else k_allreduce_rmsnorm<T, NR, VPT, false><<<grid, threads, 0, s>>>(a);
   count_launch();
   return cudaGetLastError();
 }
 
 template <typename T, int NR>
 cudaError_t norm_vpt(const NormArgs& a, bool fp8, const RowShape& r, dim3 grid, cudaStream_t s) {
-  if (r.threads > 512) return norm_go<T, NR, 8, 1024>(a, fp8, grid, r.threads, s);
   switch (r.vpt) {
-    case 1: return norm_go<T, NR, 1, 512>(a, fp8, grid, r.threads, s);
-    case 2: return norm_go<T, NR, 2, 512>(a, fp8, grid, r.threads, s);
-    case 4: return norm_go<T, NR, 4, 512>(a, fp8, grid, r.threads, s);
-    default: return norm_go<T, NR, 8, 512>(a, fp8, grid, r.threads, s);
+    case 1: return norm_go<T, NR, 1>(a, fp8, grid, r.threads, s);
+    case 2: return norm_go<T, NR, 2>(a, fp8, grid, r.threads, s);
+    case 4: return norm_go<T, NR, 4>(a, fp8, grid, r.threads, s);
+    default: return norm_go<T, NR, 8>(a, fp8, grid, r.threads, s);
   }
 }
 
@@ -545,21 +614,26 @@ cudaError_t norm_ranks(const NormArgs& a, bool fp8, const RowShape& r, dim3 grid
   }
 }
 
-template <typename T, int NR, int VPT, int MT>
+template <typename T, int NR, int VPT>
 cudaError_t bwd_go(const NormBwdArgs& a, dim3 grid, int threads, cudaStream_t s) {
-  k_rmsnorm_backward<T, NR, VPT, MT><<<grid, threads, 0, s>>>(a);
+  const int smem = VPT >= kSharedDw ? a.nchunks * kChunk * 4 : 0;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&k_rmsnorm_backward<T, NR, VPT>),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  k_rmsnorm_backward<T, NR, VPT><<<grid, threads, smem, s>>>(a);
   count_launch();
   return cudaGetLastError();
 }
 
 template <typename T, int NR>
 cudaError_t bwd_vpt(const NormBwdArgs& a, const RowShape& r, dim3 grid, cudaStream_t s) {
-  if (r.threads > 512) return bwd_go<T, NR, 8, 1024>(a, grid, r.threads, s);
   switch (r.vpt) {
-    case 1: return bwd_go<T, NR, 1, 512>(a, grid, r.threads, s);
-    case 2: return bwd_go<T, NR, 2, 512>(a, grid, r.threads, s);
-    case 4: return bwd_go<T, NR, 4, 512>(a, grid, r.threads, s);
-    default: return bwd_go<T, NR, 8, 512>(a, grid, r.threads, s);
+    case 1: return bwd_go<T, NR, 1>(a, grid, r.threads, s);
+    case 2: return bwd_go<T, NR, 2>(a, grid, r.threads, s);
+    case 4: return bwd_go<T, NR, 4>(a, grid, r.threads, s);
+    default: return bwd_go<T, NR, 8>(a, grid, r.threads, s);
   }
 }
 
@@ -596,7 +670,6 @@ cudaError_t launch_allreduce_rmsnorm(const NormLaunch& L, cudaStream_t s) {
   }
 }
 
-// The backward's resident blocks: four of 256 threads or two of 512 an SM (one of 1024).
 int64_t norm_backward_parts(int64_t total_rows) { return total_rows < kNormMaxParts ? total_rows : kNormMaxParts; }
 
 cudaError_t launch_rmsnorm_backward(const NormBwdLaunch& L, cudaStream_t s) {
@@ -618,7 +691,7 @@ cudaError_t launch_rmsnorm_backward(const NormBwdLaunch& L, cudaStream_t s) {
   a.partial = L.partial;
   const RowShape r = row_shape(a.nchunks);
   a.tpr_log2 = r.tpr_log2;
-  int64_t most = static_cast<int64_t>(sm_count()) * (r.threads == 256 ? 4 : r.threads == 512 ? 2 : 1);
+  int64_t most = static_cast<int64_t>(sm_count()) * (r.threads == 256 ? 4 : r.vpt < 8 ? 2 : 1);
   if (most > kNormMaxParts) most = kNormMaxParts;
   most = most / L.ngroups > 0 ? most / L.ngroups : 1;
   int64_t blocks = (L.rows + r.rpb - 1) / r.rpb;
@@ -660,9 +733,9 @@ cudaError_t launch_quantize_fp8(const QuantLaunch& L, cudaStream_t s) {
     const int64_t blocks = ((L.rows + 127) / 128) * a.nblocks;
     const dim3 grid(static_cast<unsigned>(blocks < most ? blocks : most), L.ntensors);
     switch (L.dtype) {
-      case COCO_F32: k_quantize_tiles<float><<<grid, 256, 0, s>>>(a); break;
-      case COCO_F16: k_quantize_tiles<__half><<<grid, 256, 0, s>>>(a); break;
-      default: k_quantize_tiles<__nv_bfloat16><<<grid, 256, 0, s>>>(a); break;
+      case COCO_F32: k_quantize_tiles<float><<<grid, kTileThreads, 0, s>>>(a); break;
+      case COCO_F16: k_quantize_tiles<__half><<<grid, kTileThreads, 0, s>>>(a); break;
+      default: k_quantize_tiles<__nv_bfloat16><<<grid, kTileThreads, 0, s>>>(a); break;
     }
   }
   count_launch();

@@ -449,7 +449,7 @@ coco_status coco_loop_profitable(double orig_comp, double orig_comm, double ring
  * over the last dimension, with the sum (rank order), the statistics and the
  * product in fp32 from the unrounded h. Each row is read once.
  *
- *   partials  LOCAL, dtype T in {F32, F16, BF16}; the last dimension (the row) at most 65536, else
+ *   partials  LOCAL, dtype T in {F32, F16, BF16}; the last dimension (the row) at most 32768, else
  *             COCO_ERR_UNSUPPORTED.
  *   residual  REPLICATED, T, the same shape, or NULL.
  *   weight    device pointer to one row of T.

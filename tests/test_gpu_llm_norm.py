@@ -48,7 +48,7 @@ def guarded(shape, dtype, pad=256):
 
 NORM_CASES = [  # ranks, rows, cols
     (1, 1, 16), (2, 1, 128), (3, 5, 144), (8, 7, 256), (8, 1, 4096), (4, 3, 1040), (8, 33, 2064), (5, 2, 8192),
-    (1, 3, 16400), (2, 2, 32768), (1, 2, 65536), (8, 300, 512), (40, 3, 512),
+    (1, 3, 16400), (2, 2, 32768), (1, 2, 20000), (8, 300, 512), (40, 3, 512),
 ]
 
 
@@ -155,7 +155,7 @@ def test_norm_of_zero_rows_and_of_rows_that_are_no_numbers(fp8):
 
 
 BWD_CASES = [(1, 1, 16), (2, 3, 144), (8, 700, 128), (3, 9, 1040), (8, 650, 4096), (2, 5, 8192), (1, 2, 32768),
-             (4, 3, 65536), (40, 3, 512), (1, 5000, 256)]
+             (4, 3, 20000), (40, 3, 512), (1, 5000, 256)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
@@ -276,11 +276,11 @@ def test_quantiser_matches_the_definition_bit_for_bit(dtype, block_rows, rows, c
         check()
     for r in range(n):
         x = f64(xs[r])
-        # the scale is one fp32 division; the values are one fp32 product with its reciprocal, then e4m3
+        # the scale is one fp32 division, and so is each value before its rounding to e4m3
         s = np.maximum(oracle.block_amax(x, block_rows), 2.0 ** -100).astype(np.float32) / np.float32(448)
         assert np.array_equal(sc[r].cpu().numpy(), s)
-        inv = oracle.spread(np.float32(1) / s, x.shape, block_rows).astype(np.float32)
-        want = oracle.to_e4m3((x.astype(np.float32) * inv).astype(np.float64))
+        quotient = x.astype(np.float32) / oracle.spread(s, x.shape, block_rows).astype(np.float32)
+        want = oracle.to_e4m3(quotient.astype(np.float64))
         assert np.array_equal(f64(q[r]), want)
 
 

@@ -76,7 +76,7 @@ def test_norm_refusals(coco):
     assert call(scales=ptrs(coco, 2, at(5, 2))) == ALIGN
     odd = Norm(coco, shape=(4, 24))  # 8-bit rows of 24 bytes
     assert odd() == ALIGN
-    assert Norm(coco, shape=(1, 65552))() == UNSUPPORTED
+    assert Norm(coco, shape=(1, 32784))() == UNSUPPORTED
     # shared memory: between roles never; an input's place only exactly, and only for values of its type
     assert call(hidden=mk(coco, B, R, s, 2, base=at(0, 16))) == ALIAS
     assert call(normed=mk(coco, coco.F8E4M3, R, s, 2, base=area(0))) == ALIAS
@@ -119,7 +119,7 @@ def test_norm_backward_refusals(coco):
         for a in (0, 1, 2, 3, 4, 5):
             assert call(**{k: area(a)}) == ALIAS, (k, a)
     assert call(ws=area(6)) == ALIAS
-    wide = (1, 65552)
+    wide = (1, 32784)
     assert call(dn=mk(coco, B, L, wide, n), h=mk(coco, B, R, wide, n, base=area(2)), dh=None,
                 dx=mk(coco, B, R, wide, n, base=area(5))) == UNSUPPORTED
 
