@@ -15,6 +15,14 @@ libcoco; every arithmetic step runs in the library's kernels.
   AllGather of X along x, Looped AllGather-Einsum of W1 along y (contracting
   dimension, Addition), AllGather of W2 along y, Looped Einsum-ReduceScatter
   along x (the subgroup ReduceScatter of the figure).
+
+and, past the pages, a mixture-of-experts layer of a tensor-parallel language
+model (N logical ranks, each with a slice of every expert's hidden dimension),
+whose products, norms and their gradients are the library's; rows are gathered,
+activated and combined by PyTorch between them:
+
+* ``moe_layer_fp8``: its forward in 8 bits, as it serves (one token or many);
+* ``moe_layer_train``: its forward and backward in 16 bits, as it trains.
 """
 
 import torch
@@ -153,3 +161,114 @@ def mlp_2d(x_blocks, w1_blocks, w2_blocks, m_x, n_y, bufs=None, stream=None, sid
                                coco.sliced(mesh_order(bufs["w2f"], m_x, n_y, "y"), 0, ngroups=n_y),
                                coco.sliced(mesh_order(bufs["y"], m_x, n_y, "y"), 1, ngroups=n_y), main)
     return bufs
+
+
+def route(expert_of, experts):
+    """Rows sorted by expert for ``expert_of`` [tokens, choices] (int64, on the device; nothing comes back to the
+    host). Returns (token_of_row [rows], row_of_choice [tokens, choices], offsets [experts + 1] int32)."""
+    flat = expert_of.reshape(-1)
+    order = torch.argsort(flat, stable=True)
+    row_of = torch.empty_like(order)
+    row_of[order] = torch.arange(order.numel(), device=order.device)
+    counts = (flat[:, None] == torch.arange(experts, device=flat.device)).sum(0)
+    offsets = torch.cat([counts.new_zeros(1), counts.cumsum(0)]).to(torch.int32)
+    return order // expert_of.shape[1], row_of.view(expert_of.shape), offsets
+
+
+def _scales_like(q):
+    return _empty((*q.shape[:-1], (q.shape[-1] + 127) // 128), torch.float32, q.device)
+
+
+def norm_fp8(partials, residual, weight, eps, stream=None):
+    """A layer's tail: the AllReduce of ``partials``, the residual, the norm. Returns (hidden, normed in 8 bits, its
+    scales), one copy each."""
+    n = len(partials)
+    hidden = torch.empty_like(partials[0])
+    normed = torch.empty_like(hidden, dtype=torch.float8_e4m3fn)
+    scales = _scales_like(normed)
+    coco.coco_allreduce_rmsnorm(coco.local(partials), None if residual is None else coco.replicated([residual] * n),
+                                weight, eps, coco.replicated([hidden] * n), coco.replicated([normed] * n),
+                                [scales] * n, None, stream)
+    return hidden, normed, scales
+
+
+def quantize_weights(tensors, stream=None):
+    """Weights (one tensor per rank) in 8 bits with a scale per 128 x 128 block: once, when they are loaded."""
+    q = [torch.empty_like(t, dtype=torch.float8_e4m3fn) for t in tensors]
+    shape = tensors[0].shape
+    s = [_empty((*shape[:-2], (shape[-2] + 127) // 128, (shape[-1] + 127) // 128), torch.float32, t.device) for t in q]
+    coco.coco_quantize_fp8(coco.local(tensors), 128, coco.local(q), s, stream)
+    return q, s
+
+
+def moe_layer_fp8(partials, residual, weight, eps, expert_of, gates, up, up_scales, down, down_scales, next_weight):
+    """From the partials of the products before it to what the next layer reads:
+
+        h = AllReduce(partials) + residual,  x = norm(h)
+        y_r = sum over a token's choices of gate * relu(x @ up_r[expert]) @ down_r[expert]      (rank r's part)
+        (h', x') = norm(AllReduce(y) + h)
+
+    ``expert_of``, ``gates``: [tokens, choices]; ``up[r]``: [experts, H, F / N] and ``down[r]``: [experts, F / N, H]
+    in 8 bits with their scales (``quantize_weights``). Runs on the current stream. Returns (h', x' in 8 bits, its
+    scales)."""
+    n, dev = len(partials), partials[0].device
+    hidden, x, xs = norm_fp8(partials, residual, weight, eps)
+    token_of, row_of, offsets = route(expert_of, up[0].shape[0])
+    offsets = offsets.repeat(n, 1)
+    rows = x.view(torch.uint8)[token_of].view(x.dtype)
+    row_scales = xs[token_of]
+    mid = [_empty((rows.shape[0], up[0].shape[2]), torch.bfloat16, dev) for _ in range(n)]
+    coco.coco_grouped_einsum("tk,ekn->tn", coco.replicated([rows] * n), [row_scales] * n, coco.local(up), up_scales,
+                             offsets, coco.local(mid))
+    for m in mid:
+        m.relu_()
+    q = [torch.empty_like(m, dtype=torch.float8_e4m3fn) for m in mid]
+    qs = [_scales_like(t) for t in q]
+    coco.coco_quantize_fp8(coco.local(mid), 1, coco.local(q), qs)
+    out = [_empty((rows.shape[0], down[0].shape[2]), torch.bfloat16, dev) for _ in range(n)]
+    coco.coco_grouped_einsum("tk,ekn->tn", coco.local(q), qs, coco.local(down), down_scales, offsets, coco.local(out))
+    y = [(o[row_of].float() * gates[..., None]).sum(1).to(hidden.dtype) for o in out]
+    return norm_fp8(y, hidden, next_weight, eps)
+
+
+def moe_layer_train(partials, residual, weight, eps, expert_of, up, down, dout):
+    """The same layer in 16 bits (gates of one), forward and backward: the forward's sum h + AllReduce(y), and for the
+    gradient ``dout`` of that sum the gradients of each partial and of the residual (one tensor), of the norm's
+    weight (fp32) and of every rank's experts. Returns a dict: out, dx, dweight, dup, ddown, and what the forward kept
+    of the hidden units: mid (a row per choice, by expert) and row_of_choice."""
+    n, dev = len(partials), partials[0].device
+    tokens, hid = partials[0].shape
+    dt = partials[0].dtype
+    hidden, x = torch.empty_like(partials[0]), torch.empty_like(partials[0])
+    rstd = _empty((tokens,), torch.float32, dev)
+    coco.coco_allreduce_rmsnorm(coco.local(partials), coco.replicated([residual] * n), weight, eps,
+                                coco.replicated([hidden] * n), coco.replicated([x] * n), None, rstd)
+    token_of, row_of, offsets = route(expert_of, up[0].shape[0])
+    offsets = offsets.repeat(n, 1)
+    rows, f = token_of.numel(), up[0].shape[2]
+    xr = coco.replicated([x[token_of]] * n)
+    mid = [_empty((rows, f), dt, dev) for _ in range(n)]
+    coco.coco_grouped_einsum("tk,ekn->tn", xr, None, coco.local(up), None, offsets, coco.local(mid))
+    act = [m.relu() for m in mid]
+    y = [_empty((rows, hid), dt, dev) for _ in range(n)]
+    coco.coco_grouped_einsum("tk,ekn->tn", coco.local(act), None, coco.local(down), None, offsets, coco.local(y))
+    out = torch.empty_like(hidden)
+    coco.coco_fused_allreduce(coco.local([o[row_of].float().sum(1).to(dt) for o in y]), None,
+                              coco.replicated([hidden] * n), 0.0, 0, coco.replicated([out] * n))
+    # backward: every rank's part of the sum has the gradient dout
+    drow = coco.replicated([dout[token_of]] * n)
+    ddown, dact = [torch.empty_like(w) for w in down], [torch.empty_like(m) for m in mid]
+    coco.coco_grouped_einsum("tk,tn->ekn", coco.local(act), None, drow, None, offsets, coco.local(ddown))
+    coco.coco_grouped_einsum("tk,enk->tn", drow, None, coco.local(down), None, offsets, coco.local(dact))
+    dmid = coco.local([torch.where(m > 0, d, torch.zeros_like(d)) for m, d in zip(mid, dact)])
+    dup, dxr = [torch.empty_like(w) for w in up], [_empty((rows, hid), dt, dev) for _ in range(n)]
+    coco.coco_grouped_einsum("tk,tn->ekn", xr, None, dmid, None, offsets, coco.local(dup))
+    coco.coco_grouped_einsum("tk,enk->tn", dmid, None, coco.local(up), None, offsets, coco.local(dxr))
+    dnormed = [d[row_of].float().sum(1).to(dt) for d in dxr]
+    dx, dweight = torch.empty_like(hidden), _empty((hid,), torch.float32, dev)
+    space = _empty((coco.coco_allreduce_rmsnorm_backward_bytes(tokens, hid),), torch.uint8, dev)
+    coco.coco_allreduce_rmsnorm_backward(coco.local(dnormed), coco.replicated([dout] * n),
+                                         coco.replicated([hidden] * n), weight, rstd, coco.replicated([dx] * n),
+                                         dweight, space)
+    return {"out": out, "dx": dx, "dweight": dweight, "dup": dup, "ddown": ddown, "mid": mid,
+            "row_of_choice": row_of}

@@ -68,6 +68,8 @@ from .llm import (
     allreduce_rmsnorm,
     allreduce_rmsnorm_backward,
     grouped_einsum,
+    moe_layer,
+    moe_layer_backward,
 )
 from .scattered import (
     buckets as scattered_buckets,
@@ -99,4 +101,5 @@ __all__ = [
     "loop_profitable",
     "e4m3_table", "to_e4m3", "block_amax", "scales_of", "spread", "quantize", "dequantize",
     "allreduce_rmsnorm", "allreduce_rmsnorm_backward", "grouped_einsum",
+    "moe_layer", "moe_layer_backward",
 ]

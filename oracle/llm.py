@@ -101,3 +101,36 @@ def grouped_einsum(form, lhs, rhs, offsets):
         else:
             out[a:b] = lhs[a:b] @ (rhs[e] if form == "kn" else rhs[e].T)
     return out
+
+
+def moe_layer(partials, residual, weight, eps, expert_of, gates, up, down):
+    """(h, x, sum of the ranks' outputs) of a mixture-of-experts layer: per token and choice, a loop."""
+    h, x, _ = allreduce_rmsnorm(partials, residual, weight, eps)
+    y = np.zeros_like(h)
+    for t in range(h.shape[0]):
+        for j in range(expert_of.shape[1]):
+            e = int(expert_of[t, j])
+            for u, d in zip(up, down):
+                y[t] += gates[t, j] * (np.maximum(x[t] @ u[e], 0.0) @ d[e])
+    return h, x, y
+
+
+def moe_layer_backward(partials, residual, weight, eps, expert_of, up, down, dout, active=None):
+    """Gradients of sum(dout * (h + y)) (gates of one): (of h, of the weight, of up per rank, of down per rank).
+
+    ``active[r][t, j]``: which hidden units of rank r are positive for choice j of token t, where another forward
+    decided that (a unit within rounding of zero has two gradients); by default this one's."""
+    h, x, rstd = allreduce_rmsnorm(partials, residual, weight, eps)
+    dx, dup, ddown = np.zeros_like(h), [np.zeros_like(u) for u in up], [np.zeros_like(d) for d in down]
+    for t in range(h.shape[0]):
+        for j in range(expert_of.shape[1]):
+            e = int(expert_of[t, j])
+            for r, (u, d) in enumerate(zip(up, down)):
+                mid = x[t] @ u[e]
+                on = mid > 0 if active is None else active[r][t, j]
+                dmid = (d[e] @ dout[t]) * on
+                ddown[r][e] += np.outer(mid * on, dout[t])
+                dup[r][e] += np.outer(x[t], dmid)
+                dx[t] += u[e] @ dmid
+    dh, dw = allreduce_rmsnorm_backward([dx], dout, h, rstd, weight)
+    return dh, dw, dup, ddown

@@ -75,3 +75,34 @@ def test_grouped_products_by_brute_force():
     assert np.allclose(oracle.grouped_einsum("kn", lhs, rhs, off), out)
     assert np.allclose(oracle.grouped_einsum("nk", lhs, rhs.transpose(0, 2, 1), off), out)
     assert np.allclose(oracle.grouped_einsum("grad", lhs, dy, off), grad)
+
+
+def test_moe_layer_by_grouped_products_and_its_gradient_by_differences():
+    rng = np.random.default_rng(5)
+    t, hid, f, e, n = 6, 8, 5, 3, 2
+    parts, res = [rng.standard_normal((t, hid)) for _ in range(n)], rng.standard_normal((t, hid))
+    w, dout = rng.standard_normal(hid), rng.standard_normal((t, hid))
+    up, down = [rng.standard_normal((e, hid, f)) for _ in range(n)], [rng.standard_normal((e, f, hid)) for _ in range(n)]
+    expert_of = rng.integers(0, e, (t, 2))
+    gates = rng.uniform(0, 1, (t, 2))
+    h, x, y = oracle.moe_layer(parts, res, w, 1e-3, expert_of, gates, up, down)
+    order = np.argsort(expert_of.ravel(), kind="stable")
+    off = np.concatenate([[0], np.cumsum(np.bincount(expert_of.ravel(), minlength=e))])
+    want = np.zeros_like(y)
+    for u, d in zip(up, down):
+        o = oracle.grouped_einsum("kn", np.maximum(oracle.grouped_einsum("kn", x[order // 2], u, off), 0), d, off)
+        np.add.at(want, order // 2, o * gates.ravel()[order][:, None])
+    assert np.allclose(y, want)
+
+    def loss(p0, weight, u0, d0):
+        hh, _, yy = oracle.moe_layer([p0] + parts[1:], res, weight, 1e-3, expert_of, np.ones((t, 2)), [u0] + up[1:],
+                                     [d0] + down[1:])
+        return np.sum(dout * (hh + yy))
+
+    grads = oracle.moe_layer_backward(parts, res, w, 1e-3, expert_of, up, down, dout)
+    at = [parts[0], w, up[0], down[0]]
+    for i, g in enumerate([grads[0], grads[1], grads[2][0], grads[3][0]]):
+        d, s = rng.standard_normal(g.shape), 1e-6
+        hi, lo = list(at), list(at)
+        hi[i], lo[i] = at[i] + s * d, at[i] - s * d
+        assert np.isclose((loss(*hi) - loss(*lo)) / (2 * s), np.sum(g * d), rtol=1e-6, atol=1e-6), i
