@@ -46,8 +46,8 @@ constexpr int THREADS = 32 * (FIRST_EPI_WARP + EPI_WARPS);
 constexpr int STRIP = 32 * 128;  // an epilogue warp's staging: 32 rows x 128 bytes
 constexpr int STRIP_OFF = STAGES * STAGE_BYTES;
 constexpr int BAR_OFF = STRIP_OFF + EPI_WARPS * STRIP;
-// full, empty and cleared per stage; full and empty per accumulator buffer and half; drain
-constexpr int NUM_BARS = 3 * STAGES + 9;
+// full, empty and cleared per stage, accumulator full x2, empty x2, drain
+constexpr int NUM_BARS = 3 * STAGES + 5;
 constexpr int SMEM_BYTES = BAR_OFF + 8 * NUM_BARS + 16 + 1024;  // + alignment slack
 static_assert(SMEM_BYTES <= 232448, "shared memory over the per-CTA limit");
 constexpr uint32_t TMEM_COLS = 512;
@@ -69,7 +69,6 @@ struct GroupedParams {
   uint32_t idesc;
   uint32_t bstep;      // B's descriptor advance per MMA, in 16-byte units
   uint32_t blead;      // B's leading byte offset >> 4
-  uint32_t bhalf;      // block scales: from the first 64 columns of a CTA's B to the others, in 16-byte units
   int32_t split;       // few-row kernel: CTAs of a cluster that share a tile's k range
 };
 static_assert(sizeof(GroupedParams) <= 32000, "kernel parameter block too large");
@@ -153,18 +152,18 @@ __device__ __forceinline__ int walk_total(const GroupedParams& P, int tm, int tn
 
 // ------------------------------------------------------------ PTX (this file)
 
-// D (+)= A B over the pair, e4m3 operands (kind::f8f6f4, K = 32) or 16-bit ones (kind::f16, K = 16).
+// D (+)= A B of this CTA, e4m3 operands (kind::f8f6f4, K = 32) or 16-bit ones (kind::f16, K = 16).
 template <bool E4M3>
-__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_one(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   if constexpr (E4M3)
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
   else
-    umma_pair(d, a, b, idesc, accumulate);
+    umma(d, a, b, idesc, accumulate);
 }
 
 // The bounded waits of tc_ptx.h without a function call: ptxas cannot split registers between warps
@@ -278,10 +277,9 @@ __device__ __forceinline__ void clear_rest(const GroupedParams& P, int64_t threa
 
 // ------------------------------------------------------------ pair kernel
 
-template <bool SCALED, bool GRAD>
+template <bool GRAD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     k_grouped_pair(const __grid_constant__ GroupedParams P) {
-  static_assert(!(SCALED && GRAD), "weight gradients have 16-bit operands");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -289,10 +287,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
   auto clear_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };  // weight gradients: an expert's last block
-  // accumulator buffer a; block scales: its half h (columns 128 h .. 128 h + 127) by itself
-  auto tfull_bar = [&](int a, int h) { return bar0 + 8u * (3 * STAGES + 2 * a + h); };
-  auto tempty_bar = [&](int a, int h) { return bar0 + 8u * (3 * STAGES + 4 + 2 * a + h); };
-  const uint32_t drain_bar = bar0 + 8u * (3 * STAGES + 8);
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (3 * STAGES + a); };
+  auto tempty_bar = [&](int a) { return bar0 + 8u * (3 * STAGES + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (3 * STAGES + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + BAR_OFF + 8 * NUM_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + BAR_OFF + 8 * NUM_BARS + 4);
 
@@ -309,11 +306,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       mbar_init(empty_bar(s), 1);
       mbar_init(clear_bar(s), 1);
     }
-    for (int a = 0; a < 2; ++a)
-      for (int h = 0; h < 2; ++h) {
-        mbar_init(tfull_bar(a, h), 1);
-        mbar_init(tempty_bar(a, h), SCALED ? EPI_WARPS : 2 * EPI_WARPS);  // CTA 0's: epilogue warps of both CTAs
-      }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), 2 * EPI_WARPS);  // CTA 0's: the epilogue warps of both CTAs
+    }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -331,11 +327,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   int dummy = 0;
   volatile int* never = &dummy;
 
-  // Registers, block scales: an epilogue thread holds 128 sums. The launch's 384 threads have 168 each; the four warps in
-  // front give up what the eight epilogue warps take (128 x 72 + 256 x 216 = 384 x 168). Neither side may spill: a few
-  // reloads in the MMA warp's loop or the sums' cost the block-scaled product 20 to 60 %.
   if (warp < FIRST_EPI_WARP) {
-    if constexpr (SCALED) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0) {
       // ------------------------------------------------------ TMA producer
       const bool leader = elect_one();
@@ -393,8 +385,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
               tma_load_3d_pair(sa, ma, fb, k0, arow, 0);
               if (P.form == GRP_NK) {
                 tma_load_3d_pair(sb, mb, fb, k0, bcol, t.e);
-              } else if constexpr (SCALED) {
-                tma_load_3d_pair(sb, mb, fb, bcol, k0, t.e);
               } else {
                 tma_load_3d_pair(sb, mb, fb, bcol, k0, t.e);
                 tma_load_3d_pair(sb + B_BYTES / 2, mb, fb, bcol + 64, k0, t.e);
@@ -441,22 +431,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           if constexpr (GRAD) return walk_find<GRAD>(P, w, u, t, TILE_M, TILE_N);
           else return u < total;
         };
-        auto take_acc = [&](int h) {
-          if (!wait_bar_warp(tempty_bar(acc, h), accph ^ 1u, abort_flag)) {
-            if (leader) fail();
-            return false;
-          }
-          tc_fence_after();
-          return true;
-        };
-        auto next_acc = [&]() {
-          acc ^= 1;
-          if (acc == 0) accph ^= 1u;
-        };
         for (int u = cluster_id; ok && more(u); u += nclusters) {
           const int kblocks = GRAD ? (t.r1 - t.r0 + P.bk - 1) / P.bk : P.kblocks;
           if (GRAD && kblocks == 0) continue;  // no rows: the epilogue stores zeros
-          if (!SCALED && !take_acc(0)) { ok = false; break; }
+          if (!wait_bar_warp(tempty_bar(acc), accph ^ 1u, abort_flag)) {
+            if (leader) fail();
+            ok = false;
+            break;
+          }
+          tc_fence_after();
           for (int kb = 0; kb < kblocks; ++kb) {
             if (!wait_bar_warp(full_bar(stage), phase, abort_flag)) {
               if (leader) fail();
@@ -466,37 +449,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             tc_fence_after();
             const uint64_t off = static_cast<uint64_t>(stage * kStageDesc);
             const uint64_t ad = ad0 + off, bd = bd0 + off;
-            if constexpr (SCALED) {
-              for (int h = 0; h < 2; ++h) {
-                if (!take_acc(h)) { ok = false; break; }
-                if (leader) {
+            if (leader) {
 #pragma unroll
-                  for (int k = 0; k < 4; ++k)
-                    mma_pair<true>(tmem_base + acc * TILE_N + 128 * h, ad + astep * k, bd + P.bhalf * h + bstep * k,
-                                   idesc, k != 0);
-                  umma_commit_pair(tfull_bar(acc, h), kPair);
-                }
-                __syncwarp();
-                any_mma = true;
-              }
-              if (!ok) break;
-              if (leader) umma_commit_pair(empty_bar(stage), kPair);
-              next_acc();
-            } else {
-              if (leader) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  mma_pair<false>(tmem_base + acc * TILE_N, ad + astep * k, bd + bstep * k, idesc, (kb | k) != 0);
-                umma_commit_pair(empty_bar(stage), kPair);
-              }
-              any_mma = true;
+              for (int k = 0; k < 4; ++k)
+                umma_pair(tmem_base + acc * TILE_N, ad + astep * k, bd + bstep * k, idesc, (kb | k) != 0);
+              umma_commit_pair(empty_bar(stage), kPair);
             }
+            any_mma = true;
             __syncwarp();
             if (++stage == STAGES) { stage = 0; phase ^= 1u; }
           }
-          if (!SCALED && ok) {
-            if (leader) umma_commit_pair(tfull_bar(acc, 0), kPair);
-            next_acc();
+          if (ok) {
+            if (leader) umma_commit_pair(tfull_bar(acc), kPair);
+            acc ^= 1;
+            if (acc == 0) accph ^= 1u;
           }
           __syncwarp();
         }
@@ -544,20 +510,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
   } else {
     // --------------------------------------------------------- epilogue
-    if constexpr (SCALED) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int quarter = warp & 3;                       // TMEM lanes 32*quarter .. +31 belong to this warp
     const int half = (warp - FIRST_EPI_WARP) >> 2;      // columns 128*half .. +127 of the tile
     const uint32_t strip = sbase + STRIP_OFF + (warp - FIRST_EPI_WARP) * STRIP;
     const uint32_t tacc = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128;
-    const int hb = SCALED ? half : 0;  // the half whose barriers this warp follows
-    const uint32_t tempty0 = rank == 0 ? 0 : mapa_rank0(tempty_bar(0, hb));
+    const uint32_t tempty0 = rank == 0 ? 0 : mapa_rank0(tempty_bar(0));
     Walk w;
     walk_load<GRAD>(P, w, 0, 0, TILE_M, TILE_N);
     Tile t;
     int acc = 0;
     uint32_t accph = 0;
     auto wait_acc = [&]() {
-      const bool ready = __all_sync(0xffffffffu, wait_bar(tfull_bar(acc, hb), accph, abort_flag));
+      const bool ready = __all_sync(0xffffffffu, wait_bar(tfull_bar(acc), accph, abort_flag));
       if (!ready && lane == 0) fail();
       tc_fence_after();
       return ready;
@@ -566,125 +530,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if (rank == 0) mbar_arrive_relaxed(tempty_bar(acc, hb));
-        else mbar_arrive_cluster_relaxed(tempty0 + 16u * acc);
+        if (rank == 0) mbar_arrive_relaxed(tempty_bar(acc));
+        else mbar_arrive_cluster_relaxed(tempty0 + 8u * acc);
       }
       acc ^= 1;
       if (acc == 0) accph ^= 1u;
     };
     bool ok = true;
     for (int u = cluster_id; ok && walk_find<GRAD>(P, w, u, t, TILE_M, TILE_N); u += nclusters) {
-      if constexpr (SCALED) {
-        uint64_t sum[64];  // pairs of fp32 sums of neighbouring columns
+      const int esize = P.out_dtype == COCO_F32 ? 4 : 2;
+      const int64_t pitch = static_cast<int64_t>(P.n) * esize;
+      const int m_end = GRAD ? P.k : t.r1 - t.r0;             // rows of the expert's output
+      const int row = t.m0 + 128 * rank + quarter * 32;       // this warp's first one
+      const int rows = min(32, m_end - row);                  // (may be negative: nothing to store)
+      const int col = t.n0 + 128 * half;
+      const int64_t out_row = (GRAD ? static_cast<int64_t>(t.e) * P.k : static_cast<int64_t>(t.r0)) + row;
+      char* out = static_cast<char*>(P.out[t.p]) + out_row * pitch + static_cast<int64_t>(col) * esize;
+      const int64_t bytes = pitch - static_cast<int64_t>(col) * esize;  // left of the row
+      const bool none = GRAD && t.r1 == t.r0;
+      if (!none && !wait_acc()) { ok = false; break; }
+      const uint32_t ta = tacc + acc * TILE_N;
+      const int strips = esize == 4 ? 4 : 2;
+      for (int c = 0; c < strips; ++c) {
+        uint32_t p[32];
+        if (none) {
 #pragma unroll
-        for (int j = 0; j < 64; ++j) sum[j] = 0ull;
-        // The half's 128 columns are 64 of CTA 0's columns of B and 64 of CTA 1's: tile columns 64 half .. + 63
-        // and 128 + 64 half .. + 63, in two different blocks of 128. This lane's row of lhs scales, and the two
-        // blocks' scales (out of range: any valid ones).
-        const int my_row = t.r0 + t.m0 + 128 * rank + quarter * 32 + lane;
-        const float* sa = P.sa[t.p] + static_cast<int64_t>(min(my_row, P.rows - 1)) * P.kscales;
-        const float* sb0 = P.sb[t.p] + static_cast<int64_t>(t.e) * P.kscales * P.nscales +
-                           static_cast<int64_t>(t.n0 / 128) * P.sb_n;
-        const float* sb1 = sb0 + (t.n0 / 128 + 1 < P.nscales ? P.sb_n : 0);
-        const int64_t sb_k = P.sb_k;
-        park(strip, 0, w.base); park(strip, 1, w.r0); park(strip, 2, w.r1); park(strip, 3, w.tiles);
-        park(strip, 4, w.upto); park(strip, 5, t.p); park(strip, 6, t.r0); park(strip, 7, t.r1);
-        park(strip, 8, t.m0); park(strip, 9, t.n0); park(strip, 10, u);
-        float a_s = __ldg(sa), b_s0 = __ldg(sb0), b_s1 = __ldg(sb1);
-        for (int left = P.kblocks; left > 0; --left) {
-          const float s0 = a_s * b_s0, s1 = a_s * b_s1;
-          if (left > 1) {  // the next block's scales, ahead of its sums
-            a_s = __ldg(++sa);
-            b_s0 = __ldg(sb0 += sb_k);
-            b_s1 = __ldg(sb1 += sb_k);
-          }
-          if (!wait_acc()) { ok = false; break; }
-          const uint32_t ta = tacc + acc * TILE_N;
-          const uint64_t ss0 = pack2(__float_as_uint(s0), __float_as_uint(s0));
-          const uint64_t ss1 = pack2(__float_as_uint(s1), __float_as_uint(s1));
-          // (every sum is pinned behind its load by asm volatile: moved on, the sums' operands do not fit the registers)
+          for (int j = 0; j < 32; ++j) p[j] = 0u;
+        } else if (esize == 4) {
+          tmem_ld32(ta + 32 * c, p);
+          tmem_ld_wait();
+        } else {
+          uint32_t r0[32], r1[32];
+          tmem_ld32(ta + 64 * c, r0);
+          tmem_ld32(ta + 64 * c + 32, r1);
+          tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            uint32_t r[16];
-            tmem_ld16(ta + 16 * c, r);
-            tmem_ld_wait();
-            if (c == 7) free_acc();
-#pragma unroll
-            for (int j = 0; j < 8; ++j) add_scaled(sum[8 * c + j], r[2 * j], r[2 * j + 1], c < 4 ? ss0 : ss1);
+          for (int j = 0; j < 16; ++j) {
+            p[j] = cvt_pair(__uint_as_float(r0[2 * j]), __uint_as_float(r0[2 * j + 1]), P.out_dtype);
+            p[16 + j] = cvt_pair(__uint_as_float(r1[2 * j]), __uint_as_float(r1[2 * j + 1]), P.out_dtype);
           }
         }
-        if (!ok) break;
-        w.base = unpark(strip, 0); w.r0 = unpark(strip, 1); w.r1 = unpark(strip, 2); w.tiles = unpark(strip, 3);
-        w.upto = unpark(strip, 4); t.p = unpark(strip, 5); t.r0 = unpark(strip, 6); t.r1 = unpark(strip, 7);
-        t.m0 = unpark(strip, 8); t.n0 = unpark(strip, 9); u = unpark(strip, 10);
-        __syncwarp();  // (the strip is written again below)
-        const int row = t.m0 + 128 * rank + quarter * 32;  // this warp's first one
-        const int rows = min(32, t.r1 - t.r0 - row);       // (may be negative: nothing to store)
-        const int esize = P.out_dtype == COCO_F32 ? 4 : 2;
-        const int64_t pitch = static_cast<int64_t>(P.n) * esize;
-        const int64_t first = static_cast<int64_t>(t.n0 + 64 * half) * esize;
-        char* out = static_cast<char*>(P.out[t.p]) + (static_cast<int64_t>(t.r0) + row) * pitch + first;
-        const int64_t left = pitch - first;  // bytes from the first column to the row's end
-        if (rows > 0 && left > 0) {
-          if (esize == 4) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t p[32];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) unpack2(sum[16 * c + j], p[2 * j], p[2 * j + 1]);
-              const int at = (c >> 1) * 512 + (c & 1) * 128;
-              store_strip(strip, p, out + at, pitch, rows, left - at);
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              uint32_t p[32];
-#pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                uint32_t x, y;
-                unpack2(sum[32 * c + j], x, y);
-                p[j] = cvt_pair(__uint_as_float(x), __uint_as_float(y), P.out_dtype);
-              }
-              store_strip(strip, p, out + 256 * c, pitch, rows, left - 256 * c);
-            }
-          }
-        }
-      } else {
-        const int esize = P.out_dtype == COCO_F32 ? 4 : 2;
-        const int64_t pitch = static_cast<int64_t>(P.n) * esize;
-        const int m_end = GRAD ? P.k : t.r1 - t.r0;             // rows of the expert's output
-        const int row = t.m0 + 128 * rank + quarter * 32;       // this warp's first one
-        const int rows = min(32, m_end - row);                  // (may be negative: nothing to store)
-        const int col = t.n0 + 128 * half;
-        const int64_t out_row = (GRAD ? static_cast<int64_t>(t.e) * P.k : static_cast<int64_t>(t.r0)) + row;
-        char* out = static_cast<char*>(P.out[t.p]) + out_row * pitch + static_cast<int64_t>(col) * esize;
-        const int64_t bytes = pitch - static_cast<int64_t>(col) * esize;  // left of the row
-        const bool none = GRAD && t.r1 == t.r0;
-        if (!none && !wait_acc()) { ok = false; break; }
-        const uint32_t ta = tacc + acc * TILE_N;
-        const int strips = esize == 4 ? 4 : 2;
-        for (int c = 0; c < strips; ++c) {
-          uint32_t p[32];
-          if (none) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) p[j] = 0u;
-          } else if (esize == 4) {
-            tmem_ld32(ta + 32 * c, p);
-            tmem_ld_wait();
-          } else {
-            uint32_t r0[32], r1[32];
-            tmem_ld32(ta + 64 * c, r0);
-            tmem_ld32(ta + 64 * c + 32, r1);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              p[j] = cvt_pair(__uint_as_float(r0[2 * j]), __uint_as_float(r0[2 * j + 1]), P.out_dtype);
-              p[16 + j] = cvt_pair(__uint_as_float(r1[2 * j]), __uint_as_float(r1[2 * j + 1]), P.out_dtype);
-            }
-          }
-          if (!none && c == strips - 1) free_acc();
-          if (rows > 0 && bytes > 128 * c) store_strip(strip, p, out + 128 * c, pitch, rows, bytes - 128 * c);
-        }
+        if (!none && c == strips - 1) free_acc();
+        if (rows > 0 && bytes > 128 * c) store_strip(strip, p, out + 128 * c, pitch, rows, bytes - 128 * c);
       }
     }
     if (!GRAD && P.offsets)
@@ -699,6 +586,277 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     __syncwarp();
     tc_fence_after();
     tmem_dealloc<true>(tmem_base, TMEM_COLS);
+  }
+}
+
+// ------------------------------------------------------ block-scaled kernel
+//
+// k_grouped_scaled (e4m3, many rows): one 256 x 256 tile per cluster of two CTAs and step, as k_grouped_pair, but
+// each CTA issues its own MMAs (M = 128, N = 256) on its own rows. The block's product has to be added up and its
+// TMEM buffer handed back every 128 k, and with one MMA over both CTAs that hand-over crossed CTAs both ways
+// (commit to the other's epilogue, arrivals back), some thousand cycles of every two blocks' 1024: 8192^3 took
+// 424 us. Here it stays within the CTA. The two still share what they read: each loads 128 of the tile's columns
+// of rhs and multicasts them to both, so a CTA reads 32 KB a block as in the pair.
+//   warp 0        TMA producer: lhs rows to itself, its half of the rhs columns to both CTAs; 4 stages of 48 KB.
+//   warp 1        issues the MMAs and owns TMEM (two buffers of 256 columns).
+//   warps 4..11   two per TMEM lane quarter, 128 columns each: sums of the scaled blocks in registers, then stores.
+
+constexpr int S_STAGE = A_BYTES + 2 * B_BYTES, S_STAGES = 4;
+constexpr int S_STRIP_OFF = S_STAGES * S_STAGE;
+constexpr int S_BAR_OFF = S_STRIP_OFF + EPI_WARPS * STRIP;
+constexpr int S_NUM_BARS = 2 * S_STAGES + 5;  // full, empty per stage; accumulators full x2, empty x2; drain
+constexpr int S_SMEM_BYTES = S_BAR_OFF + 8 * S_NUM_BARS + 16 + 1024;
+static_assert(S_SMEM_BYTES <= 232448, "shared memory over the per-CTA limit");
+
+// A tile copy to the same place in every CTA of `mask`, counted on each one's own mbarrier at the same offset.
+__device__ __forceinline__ void tma_load_3d_both(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
+                                                 int c2, uint16_t mask) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, "
+      "{%3, %4, %5}], [%2], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "h"(mask)
+      : "memory");
+}
+// Arrive on the mbarrier at offset `bar` of every CTA in `mask` once this thread's MMAs issued so far are done.
+__device__ __forceinline__ void umma_commit_both(uint32_t bar, uint16_t mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(mask)
+      : "memory");
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    k_grouped_scaled(const __grid_constant__ GroupedParams P) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + S_BAR_OFF;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (S_STAGES + s); };
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * S_STAGES + a); };
+  auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * S_STAGES + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * S_STAGES + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S_BAR_OFF + 8 * S_NUM_BARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S_BAR_OFF + 8 * S_NUM_BARS + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int cluster_id = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+  constexpr uint16_t kBoth = 0x3;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S_STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 2);  // both CTAs' MMAs have read the stage: each holds what the other's producer sends
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), EPI_WARPS);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc<false>(smem_u32(tmem_slot), TMEM_COLS);
+  tc_fence_before();
+  cluster_sync();  // the peer's barriers exist before copies and commits reach them
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  auto fail = [&]() {
+    *abort_flag = 1;
+    atomicCAS(P.err, 0u, static_cast<unsigned int>(COCO_ERR_TIMEOUT));
+  };
+  int dummy = 0;
+  volatile int* never = &dummy;
+
+  // Registers: an epilogue thread holds 128 sums. The launch's 384 threads have 168 each; the four warps in front
+  // give up what the eight epilogue warps take (128 x 88 + 256 x 208 = 384 x 168). Neither side may spill: a few
+  // reloads in the MMA warp's loop or the sums' cost 20 to 60 %.
+  if (warp < FIRST_EPI_WARP) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 0) {
+      // ------------------------------------------------------ TMA producer
+      const bool leader = elect_one();
+      Walk w;
+      walk_load<false>(P, w, 0, 0, TILE_M, TILE_N);
+      Tile t;
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, parity = 0;
+      bool ok = true;
+      for (int u = cluster_id; ok && walk_find<false>(P, w, u, t, TILE_M, TILE_N); u += nclusters) {
+        const CUtensorMap *ma = &P.a[t.p], *mb = &P.b[t.p];
+        const int arow = t.r0 + t.m0 + 128 * rank, bcol = t.n0 + 128 * rank;
+        for (int kb = 0; kb < P.kblocks; ++kb) {
+          if (!wait_bar_warp(empty_bar(stage), phase ^ 1u, abort_flag)) {
+            if (leader) fail();
+            ok = false;
+            break;
+          }
+          if (leader) {
+            const uint32_t sa = sbase + stage * S_STAGE, sb = sa + A_BYTES + rank * B_BYTES;
+            const int k0 = kb * 128;
+            mbar_expect_tx(full_bar(stage), S_STAGE);  // its rows, and both halves of the columns
+            tma_load_3d(sa, ma, full_bar(stage), k0, arow, 0);
+            if (P.form == GRP_NK) tma_load_3d_both(sb, mb, full_bar(stage), k0, bcol, t.e, kBoth);
+            else tma_load_3d_both(sb, mb, full_bar(stage), bcol, k0, t.e, kBoth);
+          }
+          __syncwarp();
+          issued |= 1u << stage;
+          parity = (parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == S_STAGES) { stage = 0; phase ^= 1u; }
+        }
+      }
+      if (!ok)  // let copies in flight land
+        for (int s = 0; s < S_STAGES; ++s)
+          if ((issued >> s) & 1u) wait_bar_warp(full_bar(s), (parity >> s) & 1u, never);
+    } else if (warp == 1) {
+      // ------------------------------------------------------- MMA issuer
+      const bool leader = elect_one();
+      const uint32_t idesc = P.idesc, bstep = P.bstep;
+      const uint64_t ad0 = tile_desc(sbase, 1), bd0 = tile_desc(sbase + A_BYTES, P.blead);
+      // (every tile has the same blocks: this warp needs no more than the tiles' number)
+      const int total = walk_total<false>(P, TILE_M, TILE_N);
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, accph = 0;
+      bool ok = true, any_mma = false;
+      for (int u = cluster_id; ok && u < total; u += nclusters) {
+        for (int kb = 0; kb < P.kblocks; ++kb) {
+          if (!wait_bar_warp(tempty_bar(acc), accph ^ 1u, abort_flag) ||
+              !wait_bar_warp(full_bar(stage), phase, abort_flag)) {
+            if (leader) fail();
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (leader) {
+            const uint64_t off = static_cast<uint64_t>(stage * (S_STAGE >> 4));
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_one<true>(tmem_base + acc * TILE_N, ad0 + off + 2 * k, bd0 + off + bstep * k, idesc, k != 0);
+            umma_commit(tfull_bar(acc));
+            umma_commit_both(empty_bar(stage), kBoth);
+          }
+          __syncwarp();
+          any_mma = true;
+          acc ^= 1;
+          if (acc == 0) accph ^= 1u;
+          if (++stage == S_STAGES) { stage = 0; phase ^= 1u; }
+        }
+      }
+      if (!ok && any_mma) {  // wait for the MMAs already issued before TMEM is freed
+        if (leader) umma_commit(drain_bar);
+        __syncwarp();
+        wait_bar_warp(drain_bar, 0, never);
+      }
+    }
+  } else {
+    // --------------------------------------------------------- epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int quarter = warp & 3;                   // TMEM lanes 32*quarter .. +31 belong to this warp
+    const int half = (warp - FIRST_EPI_WARP) >> 2;  // columns 128*half .. +127 of the tile: one block of rhs scales
+    const uint32_t strip = sbase + S_STRIP_OFF + (warp - FIRST_EPI_WARP) * STRIP;
+    const uint32_t tacc = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128;
+    Walk w;
+    walk_load<false>(P, w, 0, 0, TILE_M, TILE_N);
+    Tile t;
+    int acc = 0;
+    uint32_t accph = 0;
+    bool ok = true;
+    for (int u = cluster_id; ok && walk_find<false>(P, w, u, t, TILE_M, TILE_N); u += nclusters) {
+      uint64_t sum[64];  // pairs of fp32 sums of neighbouring columns
+#pragma unroll
+      for (int j = 0; j < 64; ++j) sum[j] = 0ull;
+      // this lane's row of lhs scales, and the columns' block of rhs scales (out of range: any valid ones)
+      const int my_row = t.r0 + t.m0 + 128 * rank + quarter * 32 + lane;
+      const float* sa = P.sa[t.p] + static_cast<int64_t>(min(my_row, P.rows - 1)) * P.kscales;
+      const float* sb = P.sb[t.p] + static_cast<int64_t>(t.e) * P.kscales * P.nscales +
+                        static_cast<int64_t>(min(t.n0 / 128 + half, P.nscales - 1)) * P.sb_n;
+      const int64_t sb_k = P.sb_k;
+      park(strip, 0, w.base); park(strip, 1, w.r0); park(strip, 2, w.r1); park(strip, 3, w.tiles);
+      park(strip, 4, w.upto); park(strip, 5, t.p); park(strip, 6, t.r0); park(strip, 7, t.r1);
+      park(strip, 8, t.m0); park(strip, 9, t.n0); park(strip, 10, u);
+      float a_s = __ldg(sa), b_s = __ldg(sb);
+      for (int left = P.kblocks; left > 0; --left) {
+        const float s = a_s * b_s;
+        if (left > 1) {  // the next block's scales, ahead of its sums
+          a_s = __ldg(++sa);
+          b_s = __ldg(sb += sb_k);
+        }
+        const bool ready = __all_sync(0xffffffffu, wait_bar(tfull_bar(acc), accph, abort_flag));
+        if (!ready) {
+          if (lane == 0) fail();
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t ta = tacc + acc * TILE_N;
+        const uint64_t ss = pack2(__float_as_uint(s), __float_as_uint(s));
+        // (every sum is pinned behind its load by asm volatile: moved on, the sums' operands do not fit the registers)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t r[16];
+          tmem_ld16(ta + 16 * c, r);
+          tmem_ld_wait();
+          if (c == 7) {  // the buffer is read: hand it back
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_relaxed(tempty_bar(acc));
+            acc ^= 1;
+            if (acc == 0) accph ^= 1u;
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) add_scaled(sum[8 * c + j], r[2 * j], r[2 * j + 1], ss);
+        }
+      }
+      if (!ok) break;
+      w.base = unpark(strip, 0); w.r0 = unpark(strip, 1); w.r1 = unpark(strip, 2); w.tiles = unpark(strip, 3);
+      w.upto = unpark(strip, 4); t.p = unpark(strip, 5); t.r0 = unpark(strip, 6); t.r1 = unpark(strip, 7);
+      t.m0 = unpark(strip, 8); t.n0 = unpark(strip, 9); u = unpark(strip, 10);
+      __syncwarp();  // (the strip is written again below)
+      const int row = t.m0 + 128 * rank + quarter * 32;  // this warp's first one
+      const int rows = min(32, t.r1 - t.r0 - row);       // (may be negative: nothing to store)
+      const int esize = P.out_dtype == COCO_F32 ? 4 : 2;
+      const int64_t pitch = static_cast<int64_t>(P.n) * esize;
+      const int64_t first = static_cast<int64_t>(t.n0 + 128 * half) * esize;
+      char* out = static_cast<char*>(P.out[t.p]) + (static_cast<int64_t>(t.r0) + row) * pitch + first;
+      const int64_t bytes = pitch - first;  // from the first column to the row's end
+      if (rows > 0 && bytes > 0) {
+        if (esize == 4) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t p[32];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) unpack2(sum[16 * c + j], p[2 * j], p[2 * j + 1]);
+            store_strip(strip, p, out + 128 * c, pitch, rows, bytes - 128 * c);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t p[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              uint32_t x, y;
+              unpack2(sum[32 * c + j], x, y);
+              p[j] = cvt_pair(__uint_as_float(x), __uint_as_float(y), P.out_dtype);
+            }
+            store_strip(strip, p, out + 128 * c, pitch, rows, bytes - 128 * c);
+          }
+        }
+      }
+    }
+    if (P.offsets)
+      clear_rest(P, static_cast<int64_t>(blockIdx.x) * (32 * EPI_WARPS) + threadIdx.x - 32 * FIRST_EPI_WARP,
+                 static_cast<int64_t>(gridDim.x) * (32 * EPI_WARPS));
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no CTA leaves while its peer's copies or commits may still reach it
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc<false>(tmem_base, TMEM_COLS);
   }
 }
 
@@ -732,19 +890,6 @@ struct FewCfg {
   static_assert(SMEM_BYTES <= 232448, "shared memory over the per-CTA limit");
 };
 constexpr int FEW_N = 128;
-
-template <bool E4M3>
-__device__ __forceinline__ void mma_one(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  if constexpr (E4M3)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-  else
-    umma(d, a, b, idesc, accumulate);
-}
 
 __device__ __forceinline__ uint32_t mapa(uint32_t addr, int cta) {
   uint32_t r;
@@ -1168,11 +1313,10 @@ cudaError_t launch_grouped(const GroupedLaunch& L, cudaStream_t s, unsigned int*
   P.split = few.split;
   // few rows: the rhs is the M side and the lhs the N side
   P.idesc = few.rows ? instruction(L.in_dtype, L.form != GRP_NK, false, FEW_N, few.rows)
-                     : instruction(L.in_dtype, grad, L.form != GRP_NK, TILE_M, fp8 ? 128 : TILE_N);
+                     : instruction(L.in_dtype, grad, L.form != GRP_NK, fp8 ? 128 : TILE_M, TILE_N);
   // rows along k: an MMA's k values are 32 (e4m3) or 16 rows of 128 bytes; else 32 bytes of a row
   P.bstep = L.form == GRP_NK ? 2 : fp8 ? 256 : 128;
   P.blead = L.form == GRP_NK ? 1 : fp8 ? B_BYTES >> 4 : (B_BYTES / 2) >> 4;
-  P.bhalf = (L.form == GRP_NK ? 64 * BKB : 64) >> 4;  // 64 rows, or 64 bytes of every row
   for (int p = 0; p < L.nprob; ++p) {
     P.out[p] = L.out[p];
     P.sa[p] = L.lhs_scales[p];
@@ -1201,12 +1345,11 @@ cudaError_t launch_grouped(const GroupedLaunch& L, cudaStream_t s, unsigned int*
   const int64_t units = L.nprob * mts * ((L.n + TILE_N - 1) / TILE_N);
   const int pairs = sm_count() / 2;
   const int grid = 2 * static_cast<int>(units < pairs ? units : pairs);
-  void (*kernel)(const GroupedParams) = fp8    ? k_grouped_pair<true, false>
-                                        : grad ? k_grouped_pair<false, true>
-                                               : k_grouped_pair<false, false>;
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), fp8 ? 0 : grad ? 1 : 2, SMEM_BYTES);
+  void (*kernel)(const GroupedParams) = fp8 ? k_grouped_scaled : grad ? k_grouped_pair<true> : k_grouped_pair<false>;
+  const int smem = fp8 ? S_SMEM_BYTES : SMEM_BYTES;
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), fp8 ? 0 : grad ? 1 : 2, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, THREADS, SMEM_BYTES, s>>>(P);
+  kernel<<<grid, THREADS, smem, s>>>(P);
   count_launch();
   return cudaGetLastError();
 }
