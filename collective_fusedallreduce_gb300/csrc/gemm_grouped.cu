@@ -14,13 +14,17 @@
 // and a ballot give the expert, so neither a table nor a launch per expert is
 // needed and empty experts cost one lane of one read.
 //
-// k_grouped_pair (many rows): CTA pairs, persistent, one 256 x 256 output tile
-// per pair and step (tcgen05 cta_group::2: M = 256, N = 256; each CTA holds 128
-// rows of A, 128 columns of B and its 128 rows of the accumulator).
+// k_grouped_pair (16-bit operands): CTA pairs, persistent, one tile of up to
+// 256 x 256 per pair and step (tcgen05 cta_group::2: M = 256, N up to 256; each
+// CTA holds 128 rows of A, half of B's and its 128 rows of the accumulator).
+// In products A is the weights (256 of their columns n) and B an expert's rows:
+// an MMA's N goes in steps of 32, so an expert's last tile costs what its rows
+// cost and not 256 (32 experts of 126 to 4000 rows: a quarter of the work). In
+// weight gradients A holds lhs columns, B rhs columns, and the rows are summed.
 //   warp 0        TMA producer: k-blocks 128 bytes deep into a ring of 6 stages of 32 KB.
 //   warp 1        issues the MMAs (CTA 0 of the pair) and owns TMEM.
 //   warps 2, 3    in weight gradients: clear what a k-block holds of the next expert's rows.
-//   warps 4..11   two per TMEM lane quarter, 128 columns each: sum of the scaled blocks, conversion, stores.
+//   warps 4..11   two per TMEM lane quarter, 128 columns each: conversion and stores.
 // Every mbarrier wait is bounded by %globaltimer as in the other tensor-core
 // kernels: on expiry COCO_ERR_TIMEOUT is recorded, the roles drain and return.
 
@@ -67,8 +71,8 @@ struct GroupedParams {
   int32_t kscales, nscales;
   int32_t sb_k, sb_n;  // steps of the rhs scales along k and n
   uint32_t idesc;
-  uint32_t bstep;      // B's descriptor advance per MMA, in 16-byte units
-  uint32_t blead;      // B's leading byte offset >> 4
+  uint32_t bstep;      // the rhs tile's descriptor advance per MMA, in 16-byte units
+  uint32_t blead;      // its leading byte offset >> 4
   int32_t split;       // few-row kernel: CTAs of a cluster that share a tile's k range
 };
 static_assert(sizeof(GroupedParams) <= 32000, "kernel parameter block too large");
@@ -139,6 +143,9 @@ __device__ __forceinline__ bool walk_find(const GroupedParams& P, Walk& w, int u
   t.n0 = nt * tn;
   return true;
 }
+
+// Rows of an expert that its tile t covers, as the N of an MMA over two CTAs takes them: a multiple of 32.
+__device__ __forceinline__ int mma_rows(const Tile& t) { return min(TILE_M, (t.r1 - t.r0 - t.m0 + 31) & ~31); }
 
 // The number of all units: for a warp whose work is the same for every tile.
 template <bool GRAD>
@@ -261,6 +268,44 @@ __device__ __forceinline__ void store_strip(uint32_t strip, const uint32_t (&p)[
   __syncwarp();
 }
 
+// Writes 32 rows of 32 columns held one column per lane (row j in r[j]): turned in shared memory, so that a store
+// instruction covers whole 64-byte (fp32: 128-byte) pieces of rows; bounded as above.
+__device__ __forceinline__ void store_turned(uint32_t strip, const uint32_t (&r)[32], char* out, int64_t pitch,
+                                             int rows, int64_t bytes, int dtype) {
+  int lane;
+  asm volatile("mov.u32 %0, %%laneid;" : "=r"(lane));
+  if (dtype == COCO_F32) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(strip + j * 128 + lane * 4), "r"(r[j]) : "memory");
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = i * 4 + (lane >> 3), at = (lane & 7) * 16;
+      const uint4 v = ld_shared_v4(strip + row * 128 + at);
+      if (row < rows && at < bytes) *reinterpret_cast<uint4*>(out + row * pitch + at) = v;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      const uint32_t two = cvt_pair(__uint_as_float(r[j]), __uint_as_float(r[j + 1]), dtype);
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(strip + j * 64 + lane * 2), "h"(static_cast<uint16_t>(two))
+                   : "memory");
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(strip + j * 64 + 64 + lane * 2),
+                   "h"(static_cast<uint16_t>(two >> 16))
+                   : "memory");
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = i * 8 + (lane >> 2), at = (lane & 3) * 16;
+      const uint4 v = ld_shared_v4(strip + row * 64 + at);
+      if (row < rows && at < bytes) *reinterpret_cast<uint4*>(out + row * pitch + at) = v;
+    }
+  }
+  __syncwarp();
+}
+
 // Rows of no expert are zero. Every thread of `nthreads` takes its share.
 __device__ __forceinline__ void clear_rest(const GroupedParams& P, int64_t thread, int64_t nthreads) {
   const int64_t pitch = static_cast<int64_t>(P.n) * (P.out_dtype == COCO_F32 ? 4 : 2) / 16;
@@ -342,7 +387,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const CUtensorMap *ma = &P.a[t.p], *mb = &P.b[t.p];
         const int kblocks = GRAD ? (t.r1 - t.r0 + P.bk - 1) / P.bk : P.kblocks;
         const bool ragged = GRAD && (t.r1 - t.r0) % P.bk != 0;
-        const int arow = t.r0 + t.m0 + 128 * rank, acol = t.m0 + 128 * rank, bcol = t.n0 + 128 * rank;
+        const int acol = t.m0 + 128 * rank, bcol = t.n0 + 128 * rank;  // (products: bcol of the weights, the A side)
+        const int share = GRAD ? 0 : mma_rows(t) / 2;                  // rows of the tile that this CTA loads
+        const int boxes = (share + 63) / 64;
         for (int kb = 0; kb < kblocks; ++kb) {
           if (!wait_bar_warp(empty_bar(stage), phase ^ 1u, abort_flag)) {
             if (leader) fail();
@@ -380,15 +427,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
               }
             } else {
               const uint32_t fb = mapa_rank0(full_bar(stage));
-              if (rank == 0) mbar_expect_tx(full_bar(stage), 2 * STAGE_BYTES);
+              if (rank == 0) mbar_expect_tx(full_bar(stage), 2 * (A_BYTES + boxes * (B_BYTES / 2)));
               const int k0 = kb * P.bk;
-              tma_load_3d_pair(sa, ma, fb, k0, arow, 0);
               if (P.form == GRP_NK) {
-                tma_load_3d_pair(sb, mb, fb, k0, bcol, t.e);
+                tma_load_3d_pair(sa, mb, fb, k0, bcol, t.e);
               } else {
-                tma_load_3d_pair(sb, mb, fb, bcol, k0, t.e);
-                tma_load_3d_pair(sb + B_BYTES / 2, mb, fb, bcol + 64, k0, t.e);
+                tma_load_3d_pair(sa, mb, fb, bcol, k0, t.e);
+                tma_load_3d_pair(sa + A_BYTES / 2, mb, fb, bcol + 64, k0, t.e);
               }
+              for (int j = 0; j < boxes; ++j)
+                tma_load_3d_pair(sb + j * (B_BYTES / 2), ma, fb, k0, t.r0 + t.m0 + rank * share + 64 * j, 0);
             }
           }
           __syncwarp();
@@ -411,27 +459,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       // ------------------------------------------------------- MMA issuer
       if (rank == 0) {
         const bool leader = elect_one();
-        const uint32_t idesc = P.idesc, bstep = P.bstep;
-        // A: rows of 128 bytes of k (32 bytes an MMA), or in weight gradients rows along k (16 rows an MMA)
-        constexpr uint32_t astep = GRAD ? 128 : 2;
-        const uint64_t ad0 = tile_desc(sbase, GRAD ? (A_BYTES / 2) >> 4 : 1);
-        const uint64_t bd0 = tile_desc(sbase + A_BYTES, P.blead);
+        // rows of 128 bytes of k: 32 bytes an MMA; rows along k: 16 rows an MMA
+        const uint32_t astep = GRAD ? 128 : P.bstep, bstep = GRAD ? P.bstep : 2;
+        const uint64_t ad0 = tile_desc(sbase, GRAD ? (A_BYTES / 2) >> 4 : P.blead);
+        const uint64_t bd0 = tile_desc(sbase + A_BYTES, GRAD ? P.blead : 1);
         constexpr uint32_t kStageDesc = static_cast<uint32_t>(STAGE_BYTES >> 4);
-        // (only weight gradients' tiles differ in length: the others need no more than their number)
-        const int total = GRAD ? 0 : walk_total<GRAD>(P, TILE_M, TILE_N);
         Walk w;
-        if constexpr (GRAD) walk_load<GRAD>(P, w, 0, 0, TILE_M, TILE_N);
+        walk_load<GRAD>(P, w, 0, 0, TILE_M, TILE_N);
         Tile t;
         int stage = 0;
         uint32_t phase = 0;
         int acc = 0;
         uint32_t accph = 0;
         bool ok = true, any_mma = false;
-        auto more = [&](int u) {
-          if constexpr (GRAD) return walk_find<GRAD>(P, w, u, t, TILE_M, TILE_N);
-          else return u < total;
-        };
-        for (int u = cluster_id; ok && more(u); u += nclusters) {
+        for (int u = cluster_id; ok && walk_find<GRAD>(P, w, u, t, TILE_M, TILE_N); u += nclusters) {
+          const uint32_t idesc = GRAD ? P.idesc : P.idesc | (static_cast<uint32_t>(mma_rows(t) >> 3) << 17);
           const int kblocks = GRAD ? (t.r1 - t.r0 + P.bk - 1) / P.bk : P.kblocks;
           if (GRAD && kblocks == 0) continue;  // no rows: the epilogue stores zeros
           if (!wait_bar_warp(tempty_bar(acc), accph ^ 1u, abort_flag)) {
@@ -540,38 +582,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     for (int u = cluster_id; ok && walk_find<GRAD>(P, w, u, t, TILE_M, TILE_N); u += nclusters) {
       const int esize = P.out_dtype == COCO_F32 ? 4 : 2;
       const int64_t pitch = static_cast<int64_t>(P.n) * esize;
-      const int m_end = GRAD ? P.k : t.r1 - t.r0;             // rows of the expert's output
-      const int row = t.m0 + 128 * rank + quarter * 32;       // this warp's first one
-      const int rows = min(32, m_end - row);                  // (may be negative: nothing to store)
-      const int col = t.n0 + 128 * half;
-      const int64_t out_row = (GRAD ? static_cast<int64_t>(t.e) * P.k : static_cast<int64_t>(t.r0)) + row;
-      char* out = static_cast<char*>(P.out[t.p]) + out_row * pitch + static_cast<int64_t>(col) * esize;
-      const int64_t bytes = pitch - static_cast<int64_t>(col) * esize;  // left of the row
-      const bool none = GRAD && t.r1 == t.r0;
-      if (!none && !wait_acc()) { ok = false; break; }
-      const uint32_t ta = tacc + acc * TILE_N;
-      const int strips = esize == 4 ? 4 : 2;
-      for (int c = 0; c < strips; ++c) {
-        uint32_t p[32];
-        if (none) {
+      if constexpr (GRAD) {
+        const int row = t.m0 + 128 * rank + quarter * 32;  // this warp's first row (of lhs columns)
+        const int rows = min(32, P.k - row);               // (may be negative: nothing to store)
+        const int64_t at = static_cast<int64_t>(t.n0 + 128 * half) * esize;
+        char* out = static_cast<char*>(P.out[t.p]) + (static_cast<int64_t>(t.e) * P.k + row) * pitch + at;
+        const int64_t bytes = pitch - at;  // left of the row
+        const bool none = t.r1 == t.r0;    // no rows: the gradient is zero
+        if (!none && !wait_acc()) { ok = false; break; }
+        const uint32_t ta = tacc + acc * TILE_N;
+        const int strips = esize == 4 ? 4 : 2;
+        for (int c = 0; c < strips; ++c) {
+          uint32_t p[32];
+          if (none) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) p[j] = 0u;
-        } else if (esize == 4) {
-          tmem_ld32(ta + 32 * c, p);
-          tmem_ld_wait();
-        } else {
-          uint32_t r0[32], r1[32];
-          tmem_ld32(ta + 64 * c, r0);
-          tmem_ld32(ta + 64 * c + 32, r1);
-          tmem_ld_wait();
+            for (int j = 0; j < 32; ++j) p[j] = 0u;
+          } else if (esize == 4) {
+            tmem_ld32(ta + 32 * c, p);
+            tmem_ld_wait();
+          } else {
+            uint32_t r0[32], r1[32];
+            tmem_ld32(ta + 64 * c, r0);
+            tmem_ld32(ta + 64 * c + 32, r1);
+            tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            p[j] = cvt_pair(__uint_as_float(r0[2 * j]), __uint_as_float(r0[2 * j + 1]), P.out_dtype);
-            p[16 + j] = cvt_pair(__uint_as_float(r1[2 * j]), __uint_as_float(r1[2 * j + 1]), P.out_dtype);
+            for (int j = 0; j < 16; ++j) {
+              p[j] = cvt_pair(__uint_as_float(r0[2 * j]), __uint_as_float(r0[2 * j + 1]), P.out_dtype);
+              p[16 + j] = cvt_pair(__uint_as_float(r1[2 * j]), __uint_as_float(r1[2 * j + 1]), P.out_dtype);
+            }
           }
+          if (!none && c == strips - 1) free_acc();
+          if (rows > 0 && bytes > 128 * c) store_strip(strip, p, out + 128 * c, pitch, rows, bytes - 128 * c);
         }
-        if (!none && c == strips - 1) free_acc();
-        if (rows > 0 && bytes > 128 * c) store_strip(strip, p, out + 128 * c, pitch, rows, bytes - 128 * c);
+      } else {
+        // lanes are the output's columns, TMEM columns its rows: this warp's 32 columns of up to 128 rows
+        const int rows = min(128, t.r1 - t.r0 - t.m0 - 128 * half);  // (may be negative: nothing to store)
+        const int64_t at = static_cast<int64_t>(t.n0 + 128 * rank + 32 * quarter) * esize;
+        const int64_t row = static_cast<int64_t>(t.r0) + t.m0 + 128 * half;
+        char* out = static_cast<char*>(P.out[t.p]) + row * pitch + at;
+        const int64_t bytes = pitch - at;
+        if (!wait_acc()) { ok = false; break; }
+        const uint32_t ta = tacc + acc * TILE_N;
+        if (rows <= 0) free_acc();
+        for (int c = 0; c < rows; c += 32) {
+          uint32_t r[32];
+          tmem_ld32(ta + c, r);
+          tmem_ld_wait();
+          if (c + 32 >= rows) free_acc();
+          if (bytes > 0) store_turned(strip, r, out + c * pitch, pitch, rows - c, bytes, P.out_dtype);
+        }
       }
     }
     if (!GRAD && P.offsets)
@@ -1311,9 +1370,11 @@ cudaError_t launch_grouped(const GroupedLaunch& L, cudaStream_t s, unsigned int*
   P.sb_n = L.form == GRP_NK ? P.kscales : 1;
   const Choice few = grad ? Choice{0, 1, 0} : choose(L, P.kblocks);
   P.split = few.split;
-  // few rows: the rhs is the M side and the lhs the N side
+  // few rows, and pairs: the rhs is the M side and the lhs the N side
   P.idesc = few.rows ? instruction(L.in_dtype, L.form != GRP_NK, false, FEW_N, few.rows)
-                     : instruction(L.in_dtype, grad, L.form != GRP_NK, fp8 ? 128 : TILE_M, TILE_N);
+            : fp8    ? instruction(L.in_dtype, false, L.form != GRP_NK, 128, TILE_N)
+            : grad   ? instruction(L.in_dtype, true, true, TILE_M, TILE_N)
+                     : instruction(L.in_dtype, L.form != GRP_NK, false, TILE_M, 0);  // (N by tile)
   // rows along k: an MMA's k values are 32 (e4m3) or 16 rows of 128 bytes; else 32 bytes of a row
   P.bstep = L.form == GRP_NK ? 2 : fp8 ? 256 : 128;
   P.blead = L.form == GRP_NK ? 1 : fp8 ? B_BYTES >> 4 : (B_BYTES / 2) >> 4;
@@ -1327,7 +1388,7 @@ cudaError_t launch_grouped(const GroupedLaunch& L, cudaStream_t s, unsigned int*
       good = encode(&P.a[p], L.lhs[p], L.in_dtype, L.k, L.rows, 1, 64, 64) &&
              encode(&P.b[p], L.rhs[p], L.in_dtype, L.n, L.rows, 1, 64, 64);
     else
-      good = encode(&P.a[p], L.lhs[p], L.in_dtype, L.k, L.rows, 1, bk, few.rows ? few.rows : 128) &&
+      good = encode(&P.a[p], L.lhs[p], L.in_dtype, L.k, L.rows, 1, bk, few.rows ? few.rows : fp8 ? 128 : 64) &&
              (L.form == GRP_NK ? encode(&P.b[p], L.rhs[p], L.in_dtype, L.k, L.n, L.experts, bk, 128)
                                : encode(&P.b[p], L.rhs[p], L.in_dtype, L.n, L.k, L.experts, bk, bk));
     if (!good) return cudaErrorNotSupported;
