@@ -1290,16 +1290,19 @@ struct Choice {
 };
 
 // The time of each kernel is the k-blocks that its busiest SM goes through, times what one takes there, and the
-// choice is the least product. Measured on a GB300, in ns a k-block (128 bytes of k): pairs 450 to 570 in e4m3 and
-// 290 to 420 in 16 bits, by how many run; few rows 250 / 230 with 16 and 350 / 260 with 64 rows while the weights
-// come from few SMs, and the HBM's time for 16 KB from each active SM (some 350 with all of them) beyond that; 1900
-// once for a shared k range. Both sides, one call from a graph, k = n = 4096 in e4m3: 1 row 7.3 us (16 rows, four
-// CTAs a tile) and 18.3 us (pairs); 64 rows 9.7 and 19.1; 256 rows 17.5 and 19.2; 512 rows 31.1 and 19.6. 64
-// experts, k 4096, n 2048 stored [n][k]: 32 rows 29.6 and 36.8 us, 256 rows 81 and 110, 1024 rows 117 and 115,
-// 4096 rows 296 and 133.
+// choice is the least product. Measured on a GB300, in ns a k-block (128 bytes of k): two CTAs on 256 rows 480 in
+// e4m3, 370 in 16 bits; few rows from the first figure on one SM to the second on all of them (then HBM counts):
+// 16 rows 250 to 360 in e4m3, 230 to 350 in 16 bits; 64 rows 360 to 500 and 260 to 390; e4m3 weights stored [k][n]
+// are the slow operand side of these MMAs: 330 to 510 and 460 to 700. A shared k range costs 1900 once.
+// Both sides, one call from a graph, e4m3 [n][k], k = n = 4096: 1 row 7.3 us (16 rows, four CTAs a tile) and 16.5
+// (256 rows); 64 rows 9.8 and 17.0; 128 rows 13.4 and 17.3; 256 rows 17.5 and 17.3; 512 rows 31.1 and 17.7. 64
+// experts, k 4096, n 2048: 32 rows 29.5 and 35.1 us, 256 rows 81 and 104, 1024 rows 118 and 108; stored [k][n] 32
+// rows 40.3 and 34.3, 256 rows 115 and 103.
 Choice choose(const GroupedLaunch& L, int kblocks) {
-  const bool fp8 = L.in_dtype == COCO_F8E4M3;
-  const int64_t pair_ns = fp8 ? 520 : 400, few16_ns = fp8 ? 250 : 230, few64_ns = fp8 ? 350 : 260, split_ns = 1900;
+  const bool fp8 = L.in_dtype == COCO_F8E4M3, kn8 = fp8 && L.form == GRP_KN;
+  const int64_t pair_ns = fp8 ? 480 : 370, split_ns = 1900;
+  const int64_t one_sm[2] = {kn8 ? 330 : fp8 ? 250 : 230, kn8 ? 460 : fp8 ? 360 : 260};
+  const int64_t all_sms[2] = {kn8 ? 510 : fp8 ? 360 : 350, kn8 ? 700 : fp8 ? 500 : 390};
   const int sms = sm_count();
   auto tiles = [&](int tm, int tn) {  // at most one partly filled tile per expert beyond the full ones
     const int64_t by_rows = static_cast<int64_t>(L.rows / tm) + (L.experts < L.rows ? L.experts : L.rows);
@@ -1314,9 +1317,10 @@ Choice choose(const GroupedLaunch& L, int kblocks) {
     for (int split = 1; split <= 8 && split <= kblocks; split *= 2) {
       if (split > 1 && units * split > sms) break;  // (a cluster that shares a tile has no second one)
       const int64_t active = units * split < sms ? units * split : sms;
-      const int64_t hbm = active * 16384 / 7000, lat = rows == 16 ? few16_ns : few64_ns;
-      const int64_t ns = waves(units * split, sms) * ((kblocks + split - 1) / split) * (hbm > lat ? hbm : lat) +
-                         (split > 1 ? split_ns : 0);
+      const int i = rows == 16 ? 0 : 1;
+      const int64_t block_ns = one_sm[i] + (all_sms[i] - one_sm[i]) * active / sms;
+      const int64_t ns =
+          waves(units * split, sms) * ((kblocks + split - 1) / split) * block_ns + (split > 1 ? split_ns : 0);
       if (ns < least) {
         least = ns;
         best = Choice{rows, split, units};

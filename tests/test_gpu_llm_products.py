@@ -43,6 +43,8 @@ PRODUCTS = [  # ranks, m, k, n
     (1, 1, 16, 16), (1, 1, 128, 128), (2, 1, 4096, 512), (1, 7, 144, 272), (1, 16, 1024, 128), (3, 17, 528, 144),
     (1, 33, 400, 2064), (1, 64, 2048, 256), (1, 65, 256, 400), (2, 129, 640, 528), (1, 200, 1296, 1040),
     (1, 256, 512, 256), (1, 300, 384, 1552), (8, 333, 528, 272), (1, 1000, 768, 2048), (1, 2049, 272, 4112),
+    # many blocks through the rings of the few-row kernels; more tiles than pairs of SMs with many blocks each
+    (1, 5, 4096, 8208), (1, 50, 2064, 10256), (1, 2500, 1040, 2576),
 ]
 
 
@@ -149,6 +151,8 @@ GROUPED = [  # counts (rows of each expert), rows before the first and after the
     ([1], 0, 0, 16, 16), ([1, 0, 2], 0, 0, 128, 128), ([0, 0, 5, 0], 2, 3, 144, 272), ([3] * 40, 0, 0, 256, 144),
     ([37, 0, 200, 1, 64], 0, 5, 528, 400), ([129, 255, 256, 257], 0, 0, 384, 528), ([1000, 3, 0, 77], 9, 0, 272, 1040),
     ([0, 0], 4, 4, 128, 256), ([16] * 65, 0, 0, 128, 144), ([640, 700], 0, 0, 1024, 512),
+    # enough columns for 256-row tiles: experts that end after 1, 31, 33, 44, 65 and 256 rows of one
+    ([300, 1, 515, 0, 77, 256, 31, 321], 3, 2, 272, 4112), ([289, 5, 0, 1121], 0, 1, 1040, 2064),
 ]
 
 
