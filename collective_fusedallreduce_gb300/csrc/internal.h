@@ -90,7 +90,7 @@ struct NormLaunch {
 };
 cudaError_t launch_allreduce_rmsnorm(const NormLaunch& L, cudaStream_t s);
 
-constexpr int64_t kNormMaxParts = 608;  // workspace rows of the weight's gradient, at least COCO_MAX_PTRS
+constexpr int64_t kNormMaxParts = 304;  // workspace rows of the weight's gradient, at least COCO_MAX_PTRS
 
 struct NormBwdLaunch {
   const void* in[COCO_MAX_PTRS];

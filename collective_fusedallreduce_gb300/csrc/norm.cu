@@ -150,14 +150,17 @@ __device__ __forceinline__ uint2 to_e4m3(const float (&f)[kChunk], float scale) 
 
 // The sum of `v` over the threads of a row (tpr of them, a power of two and at least a warp), the same
 // value in each: within warps by shuffles, across warps through shared memory in warp order. Consecutive
-// calls alternate between the two halves of `red` (`turn`), so one barrier a call is enough.
-__device__ __forceinline__ float row_sum(float v, int tpr, float (*red)[32], int turn) {
+// calls alternate between the two halves of `red` (`turn`), so one barrier a call is enough. Rows that share a
+// block have a barrier each (named ones, from 1 on), so that they do not wait for one another.
+__device__ __forceinline__ float row_sum(float v, int tpr, int slot, float (*red)[32], int turn) {
 #pragma unroll
   for (int m = 16; m; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
   if (tpr == 32) return v;
   const int warp = threadIdx.x >> 5, warps = tpr >> 5;
   if ((threadIdx.x & 31) == 0) red[turn][warp] = v;
-  __syncthreads();
+  // (one row a block, or more rows than there are named barriers: all threads together)
+  if (blockDim.x == tpr || blockDim.x > 15 * tpr) __syncthreads();
+  else asm volatile("bar.sync %0, %1;" ::"r"(1 + slot), "r"(tpr) : "memory");
   const int first = warp & ~(warps - 1);
   float s = red[turn][first];
   for (int i = 1; i < warps; ++i) s += red[turn][first + i];
@@ -256,7 +259,7 @@ __global__ void __launch_bounds__(512, VPT == 1 && NR > 0 && sizeof(T) == 2 ? 4 
         for (int j = 0; j < kChunk; ++j) h[i][j] = 0.0f;
       }
     }
-    ss = row_sum(ss, tpr, red, turn);
+    ss = row_sum(ss, tpr, slot, red, turn);
     const float rstd = rsqrtf(ss / static_cast<float>(a.cols) + a.eps);
     if (live && t == 0 && a.rstd) a.rstd[g * a.rows + row] = rstd;
 #pragma unroll
@@ -305,9 +308,10 @@ __global__ void __launch_bounds__(512, VPT == 1 && NR > 0 && sizeof(T) == 2 ? 4 
 //
 // With xhat = h * rstd and g = dy * w (dy: the sum of the ranks' gradients):
 //   dx = rstd * (g - xhat * mean(g * xhat)) + dhidden,   dw = sum over rows of dy * xhat.
-// Blocks stay on the device and walk rows; a thread keeps the dw sums of its own columns in registers over
-// all its rows and writes them once to the workspace ([blocks][cols]), which k_norm_dweight adds in block
-// order: no atomics, so repeated calls give the same bits.
+// One block an SM walks rows, as many at a time as its threads hold; a thread keeps the dw sums of its own columns
+// in registers over all its rows, the block's rows join them in shared memory, and the block writes them once to
+// the workspace ([blocks][cols]), which k_norm_dweight adds in block order: no atomics, so repeated calls give the
+// same bits.
 
 struct NormBwdArgs {
   const void* in[COCO_MAX_PTRS];
@@ -324,15 +328,23 @@ struct NormBwdArgs {
   float* partial;  // [gridDim.y * gridDim.x][cols]
 };
 
-// Rows so wide that a thread has kSharedDw chunks or more keep the dw sums in shared memory (each thread its own
-// columns') and read dhidden only when it is added: their registers hold the row's g and h.
-constexpr int kSharedDw = 4;
+// THREADS and blocks an SM, by the registers: 16-bit rows of one chunk a thread fit 64, so 1024 threads; with two
+// chunks (rows of up to 8192 columns) two blocks of 512, the dw sums in shared memory (WIDE; each thread its own
+// columns') and dhidden read only when it is added; beyond, 1024 threads a row of two or four chunks, the latter
+// reading hidden again (from L2) instead of keeping it. fp32 rows: 512 threads, WIDE from four chunks on.
+template <typename T, int VPT, int THREADS>
+struct BwdShape {
+  static constexpr bool WIDE = VPT > (sizeof(T) == 2 ? 1 : 2);
+  static constexpr bool AGAIN = THREADS == 1024 && VPT == 4;
+  static constexpr int BLOCKS = THREADS == 512 && VPT <= 2 && sizeof(T) == 2 ? 2 : 1;
+};
 
-template <typename T, int NR, int VPT>
-__global__ void __launch_bounds__(512) k_rmsnorm_backward(const __grid_constant__ NormBwdArgs a) {
-  constexpr bool WIDE = VPT >= kSharedDw;
+template <typename T, int NR, int VPT, int THREADS>
+__global__ void __launch_bounds__(THREADS, BwdShape<T, VPT, THREADS>::BLOCKS)
+    k_rmsnorm_backward(const __grid_constant__ NormBwdArgs a) {
+  constexpr bool WIDE = BwdShape<T, VPT, THREADS>::WIDE, AGAIN = BwdShape<T, VPT, THREADS>::AGAIN;
   __shared__ float red[2][32];
-  __shared__ float slots[VPT == 1 ? 256 * kChunk : 1];  // several rows a block (narrow rows): their dw, to be joined
+  __shared__ float slots[VPT == 1 ? THREADS * kChunk : 1];  // the dw of a block's rows, to be joined
   extern __shared__ float4 wide_dw[];                   // [2 * nchunks]
   const int g = blockIdx.y;
   const int tpr = 1 << a.tpr_log2;
@@ -358,9 +370,21 @@ __global__ void __launch_bounds__(512) k_rmsnorm_backward(const __grid_constant_
     const int64_t row = base + slot;
     const bool live = row < a.rows;
     const int64_t c0 = row * a.nchunks;
+    // The block's next row is brought to L2 meanwhile: a row's loads, its barrier and its stores do not overlap, and
+    // there are no registers to load a row ahead (or to have more blocks on the SM).
+    const int64_t ahead = row + static_cast<int64_t>(gridDim.x) * rpb;
+    if (ahead < a.rows)
+      for (int i = t; i < a.nranks + 2; i += tpr) {
+        const void* p = i < a.nranks ? in[i] : i == a.nranks ? hidden : dhidden;
+        const int bytes = a.cols * static_cast<int>(sizeof(T));
+        if (p)
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(static_cast<const char*>(p) + ahead * bytes),
+                       "r"(bytes)
+                       : "memory");
+      }
     const float rstd = live ? a.rstd[g * a.rows + row] : 0.0f;
     float gr[VPT][kChunk];
-    Chunk<T> hv[WIDE ? VPT : 1], dh[WIDE ? 1 : VPT];  // (narrow rows keep xhat itself)
+    Chunk<T> hv[WIDE && !AGAIN ? VPT : 1], dh[WIDE ? 1 : VPT];  // (narrow rows keep xhat itself)
     float xk[WIDE ? 1 : VPT][kChunk];
     float along = 0.0f;
 #pragma unroll
@@ -368,7 +392,7 @@ __global__ void __launch_bounds__(512) k_rmsnorm_backward(const __grid_constant_
       const int c = t + i * tpr;
       if (live && c < a.nchunks) {
         Chunk<T> wv;
-        Chunk<T>& h = hv[WIDE ? i : 0];
+        Chunk<T>& h = hv[WIDE && !AGAIN ? i : 0];
         h.load(hidden, c0 + c);
         if constexpr (!WIDE)
           if (dhidden) dh[i].load(dhidden, c0 + c);
@@ -399,7 +423,7 @@ __global__ void __launch_bounds__(512) k_rmsnorm_backward(const __grid_constant_
         }
       }
     }
-    along = row_sum(along, tpr, red, turn) * inv_cols;
+    along = row_sum(along, tpr, slot, red, turn) * inv_cols;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = t + i * tpr;
@@ -417,7 +441,12 @@ __global__ void __launch_bounds__(512) k_rmsnorm_backward(const __grid_constant_
 #pragma unroll
           for (int j = 0; j < kChunk; ++j) f[j] = 0.0f;
         }
-        if constexpr (WIDE) hv[i].get(xh);
+        if constexpr (AGAIN) {
+          hv[0].load(hidden, c0 + c);
+          hv[0].get(xh);
+        } else if constexpr (WIDE) {
+          hv[i].get(xh);
+        }
 #pragma unroll
         for (int j = 0; j < kChunk; ++j) {
           const float x = WIDE ? xh[j] * rstd : xk[WIDE ? 0 : i][j];
@@ -431,7 +460,7 @@ __global__ void __launch_bounds__(512) k_rmsnorm_backward(const __grid_constant_
   }
   float* out = a.partial + (static_cast<int64_t>(g) * gridDim.x + blockIdx.x) * a.cols;
   if constexpr (VPT == 1) {
-    if (rpb > 1) {  // (blocks of at most 256 threads)
+    if (rpb > 1) {
 #pragma unroll
       for (int j = 0; j < kChunk; ++j) slots[threadIdx.x * kChunk + j] = dw[0][j];
       __syncthreads();
@@ -465,8 +494,10 @@ __global__ void __launch_bounds__(1024) k_norm_dweight(const float* __restrict__
   __shared__ float part[32][33];
   const int c = blockIdx.x * 32 + threadIdx.x;
   float s = 0.0f;
-  if (c < cols)
+  if (c < cols) {
+#pragma unroll 5
     for (int p = threadIdx.y; p < nparts; p += 32) s += partial[static_cast<int64_t>(p) * cols + c];
+  }
   part[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
   if (threadIdx.y == 0 && c < cols) {
@@ -614,35 +645,53 @@ cudaError_t norm_ranks(const NormArgs& a, bool fp8, const RowShape& r, dim3 grid
   }
 }
 
-template <typename T, int NR, int VPT>
-cudaError_t bwd_go(const NormBwdArgs& a, dim3 grid, int threads, cudaStream_t s) {
-  const int smem = VPT >= kSharedDw ? a.nchunks * kChunk * 4 : 0;
+template <typename T, int NR, int VPT, int THREADS>
+cudaError_t bwd_go(const NormBwdArgs& a, int groups, int* parts, cudaStream_t s) {
+  using S = BwdShape<T, VPT, THREADS>;
+  // (as many blocks as stay on the device, each with at most its share of the rows)
+  const int rpb = THREADS >> a.tpr_log2;
+  int64_t most = sm_count() * S::BLOCKS < kNormMaxParts ? sm_count() * S::BLOCKS : kNormMaxParts;
+  most = most / groups > 0 ? most / groups : 1;
+  const int64_t want = (a.rows + rpb - 1) / rpb;
+  const dim3 grid(static_cast<unsigned>(want < most ? want : most), groups);
+  const int smem = S::WIDE ? a.nchunks * kChunk * 4 : 0;
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&k_rmsnorm_backward<T, NR, VPT>),
+    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&k_rmsnorm_backward<T, NR, VPT, THREADS>),
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  k_rmsnorm_backward<T, NR, VPT><<<grid, threads, smem, s>>>(a);
+  *parts = static_cast<int>(grid.x) * groups;
+  k_rmsnorm_backward<T, NR, VPT, THREADS><<<grid, THREADS, smem, s>>>(a);
   count_launch();
   return cudaGetLastError();
 }
 
 template <typename T, int NR>
-cudaError_t bwd_vpt(const NormBwdArgs& a, const RowShape& r, dim3 grid, cudaStream_t s) {
-  switch (r.vpt) {
-    case 1: return bwd_go<T, NR, 1>(a, grid, r.threads, s);
-    case 2: return bwd_go<T, NR, 2>(a, grid, r.threads, s);
-    case 4: return bwd_go<T, NR, 4>(a, grid, r.threads, s);
-    default: return bwd_go<T, NR, 8>(a, grid, r.threads, s);
+cudaError_t bwd_vpt(NormBwdArgs& a, int groups, int* parts, cudaStream_t s) {
+  const RowShape r = row_shape(a.nchunks);
+  a.tpr_log2 = r.tpr_log2;
+  if constexpr (sizeof(T) == 2) {
+    if (a.nchunks > 1024) {
+      a.tpr_log2 = 10;
+      return a.nchunks <= 2048 ? bwd_go<T, NR, 2, 1024>(a, groups, parts, s) : bwd_go<T, NR, 4, 1024>(a, groups, parts, s);
+    }
+    return r.vpt == 1 ? bwd_go<T, NR, 1, 1024>(a, groups, parts, s) : bwd_go<T, NR, 2, 512>(a, groups, parts, s);
+  } else {
+    switch (r.vpt) {
+      case 1: return bwd_go<T, NR, 1, 512>(a, groups, parts, s);
+      case 2: return bwd_go<T, NR, 2, 512>(a, groups, parts, s);
+      case 4: return bwd_go<T, NR, 4, 512>(a, groups, parts, s);
+      default: return bwd_go<T, NR, 8, 512>(a, groups, parts, s);
+    }
   }
 }
 
 template <typename T>
-cudaError_t bwd_ranks(const NormBwdArgs& a, const RowShape& r, dim3 grid, cudaStream_t s) {
+cudaError_t bwd_ranks(NormBwdArgs& a, int groups, int* parts, cudaStream_t s) {
   switch (a.nranks) {
-    case 1: return bwd_vpt<T, 1>(a, r, grid, s);
-    case 8: return bwd_vpt<T, 8>(a, r, grid, s);
-    default: return bwd_vpt<T, 0>(a, r, grid, s);
+    case 1: return bwd_vpt<T, 1>(a, groups, parts, s);
+    case 8: return bwd_vpt<T, 8>(a, groups, parts, s);
+    default: return bwd_vpt<T, 0>(a, groups, parts, s);
   }
 }
 
@@ -689,22 +738,15 @@ cudaError_t launch_rmsnorm_backward(const NormBwdLaunch& L, cudaStream_t s) {
   a.weight = L.weight;
   a.rstd = L.rstd;
   a.partial = L.partial;
-  const RowShape r = row_shape(a.nchunks);
-  a.tpr_log2 = r.tpr_log2;
-  int64_t most = static_cast<int64_t>(sm_count()) * (r.threads == 256 ? 4 : r.vpt < 8 ? 2 : 1);
-  if (most > kNormMaxParts) most = kNormMaxParts;
-  most = most / L.ngroups > 0 ? most / L.ngroups : 1;
-  int64_t blocks = (L.rows + r.rpb - 1) / r.rpb;
-  if (blocks > most) blocks = most;
-  const dim3 grid(static_cast<unsigned>(blocks), L.ngroups);
+  int parts = 0;
   cudaError_t e;
   switch (L.dtype) {
-    case COCO_F32: e = bwd_ranks<float>(a, r, grid, s); break;
-    case COCO_F16: e = bwd_ranks<__half>(a, r, grid, s); break;
-    default: e = bwd_ranks<__nv_bfloat16>(a, r, grid, s); break;
+    case COCO_F32: e = bwd_ranks<float>(a, L.ngroups, &parts, s); break;
+    case COCO_F16: e = bwd_ranks<__half>(a, L.ngroups, &parts, s); break;
+    default: e = bwd_ranks<__nv_bfloat16>(a, L.ngroups, &parts, s); break;
   }
   if (e != cudaSuccess) return e;
-  k_norm_dweight<<<(L.cols + 31) / 32, dim3(32, 32), 0, s>>>(L.partial, static_cast<int>(blocks) * L.ngroups, L.cols,
+  k_norm_dweight<<<(L.cols + 31) / 32, dim3(32, 32), 0, s>>>(L.partial, parts, L.cols,
                                                             L.dweight);
   count_launch();
   return cudaGetLastError();
