@@ -150,8 +150,9 @@ __device__ __forceinline__ uint2 to_e4m3(const float (&f)[kChunk], float scale) 
 
 // The sum of `v` over the threads of a row (tpr of them, a power of two and at least a warp), the same
 // value in each: within warps by shuffles, across warps through shared memory in warp order. Consecutive
-// calls alternate between the two halves of `red` (`turn`), so one barrier a call is enough. Rows that share a
-// block have a barrier each (named ones, from 1 on), so that they do not wait for one another.
+// calls alternate between the two halves of `red` (`turn`), so one barrier a call is enough. OWN_BARRIERS: rows
+// that share a block have a barrier each (named ones, from 1 on), so that they do not wait for one another.
+template <bool OWN_BARRIERS>
 __device__ __forceinline__ float row_sum(float v, int tpr, int slot, float (*red)[32], int turn) {
 #pragma unroll
   for (int m = 16; m; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
@@ -159,7 +160,7 @@ __device__ __forceinline__ float row_sum(float v, int tpr, int slot, float (*red
   const int warp = threadIdx.x >> 5, warps = tpr >> 5;
   if ((threadIdx.x & 31) == 0) red[turn][warp] = v;
   // (one row a block, or more rows than there are named barriers: all threads together)
-  if (blockDim.x == tpr || blockDim.x > 15 * tpr) __syncthreads();
+  if (!OWN_BARRIERS || blockDim.x == tpr || blockDim.x > 15 * tpr) __syncthreads();
   else asm volatile("bar.sync %0, %1;" ::"r"(1 + slot), "r"(tpr) : "memory");
   const int first = warp & ~(warps - 1);
   float s = red[turn][first];
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(512, VPT == 1 && NR > 0 && sizeof(T) == 2 ? 4 
         for (int j = 0; j < kChunk; ++j) h[i][j] = 0.0f;
       }
     }
-    ss = row_sum(ss, tpr, slot, red, turn);
+    ss = row_sum<false>(ss, tpr, slot, red, turn);
     const float rstd = rsqrtf(ss / static_cast<float>(a.cols) + a.eps);
     if (live && t == 0 && a.rstd) a.rstd[g * a.rows + row] = rstd;
 #pragma unroll
@@ -308,7 +309,7 @@ __global__ void __launch_bounds__(512, VPT == 1 && NR > 0 && sizeof(T) == 2 ? 4 
 //
 // With xhat = h * rstd and g = dy * w (dy: the sum of the ranks' gradients):
 //   dx = rstd * (g - xhat * mean(g * xhat)) + dhidden,   dw = sum over rows of dy * xhat.
-// One block an SM walks rows, as many at a time as its threads hold; a thread keeps the dw sums of its own columns
+// One or two blocks an SM walk rows, as many at a time as their threads hold; a thread keeps the dw sums of its own columns
 // in registers over all its rows, the block's rows join them in shared memory, and the block writes them once to
 // the workspace ([blocks][cols]), which k_norm_dweight adds in block order: no atomics, so repeated calls give the
 // same bits.
@@ -328,10 +329,12 @@ struct NormBwdArgs {
   float* partial;  // [gridDim.y * gridDim.x][cols]
 };
 
-// THREADS and blocks an SM, by the registers: 16-bit rows of one chunk a thread fit 64, so 1024 threads; with two
-// chunks (rows of up to 8192 columns) two blocks of 512, the dw sums in shared memory (WIDE; each thread its own
-// columns') and dhidden read only when it is added; beyond, 1024 threads a row of two or four chunks, the latter
-// reading hidden again (from L2) instead of keeping it. fp32 rows: 512 threads, WIDE from four chunks on.
+// THREADS and blocks an SM, by the registers (64 for 1024 threads an SM): 16-bit rows of up to 8192 columns have
+// two blocks of 512 threads, with two chunks a thread keeping the dw sums in shared memory (WIDE; each thread its own
+// columns') and reading dhidden only when it is added; wider ones 1024 threads a row of two or four chunks, the
+// latter reading hidden again (from L2) instead of keeping it. fp32 rows: 512 threads, WIDE from four chunks on.
+// Measured: 8192 x 4096 fp16 on eight ranks 119 us (6.21 TB/s), 16384 x 1024 on two 38 us, 777 x 8192 on two 22 us,
+// 4096 x 16384 bf16 on one 113 us, 2048 x 32768 141 us; HBM bounds the first, latency between a row's phases the rest.
 template <typename T, int VPT, int THREADS>
 struct BwdShape {
   static constexpr bool WIDE = VPT > (sizeof(T) == 2 ? 1 : 2);
@@ -423,7 +426,7 @@ __global__ void __launch_bounds__(THREADS, BwdShape<T, VPT, THREADS>::BLOCKS)
         }
       }
     }
-    along = row_sum(along, tpr, slot, red, turn) * inv_cols;
+    along = row_sum<true>(along, tpr, slot, red, turn) * inv_cols;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = t + i * tpr;
@@ -675,7 +678,7 @@ cudaError_t bwd_vpt(NormBwdArgs& a, int groups, int* parts, cudaStream_t s) {
       a.tpr_log2 = 10;
       return a.nchunks <= 2048 ? bwd_go<T, NR, 2, 1024>(a, groups, parts, s) : bwd_go<T, NR, 4, 1024>(a, groups, parts, s);
     }
-    return r.vpt == 1 ? bwd_go<T, NR, 1, 1024>(a, groups, parts, s) : bwd_go<T, NR, 2, 512>(a, groups, parts, s);
+    return r.vpt == 1 ? bwd_go<T, NR, 1, 512>(a, groups, parts, s) : bwd_go<T, NR, 2, 512>(a, groups, parts, s);
   } else {
     switch (r.vpt) {
       case 1: return bwd_go<T, NR, 1, 512>(a, groups, parts, s);

@@ -93,7 +93,7 @@ def test_norm_backward_refusals(coco):
     B, R, L = coco.BF16, coco.REPLICATED, coco.LOCAL
     s, n = (6, 256), 2
     need = coco.coco_allreduce_rmsnorm_backward_bytes(6, 256)
-    assert need == 6 * 256 * 4 and coco.coco_allreduce_rmsnorm_backward_bytes(10 ** 6, 64) == 152 * 64 * 4
+    assert need == 6 * 256 * 4 and coco.coco_allreduce_rmsnorm_backward_bytes(10 ** 6, 64) == 304 * 64 * 4
     assert coco.coco_allreduce_rmsnorm_backward_bytes(-1, 8) == 0
     assert coco.coco_allreduce_rmsnorm_backward_bytes(4, 1 << 20) == 0
     good = dict(dn=mk(coco, B, L, s, n, base=area(0)), dh=mk(coco, B, R, s, n, base=area(1)),
