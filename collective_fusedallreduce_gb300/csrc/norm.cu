@@ -333,7 +333,7 @@ struct NormBwdArgs {
 // two blocks of 512 threads, with two chunks a thread keeping the dw sums in shared memory (WIDE; each thread its own
 // columns') and reading dhidden only when it is added; wider ones 1024 threads a row of two or four chunks, the
 // latter reading hidden again (from L2) instead of keeping it. fp32 rows: 512 threads, WIDE from four chunks on.
-// Measured: 8192 x 4096 fp16 on eight ranks 119 us (6.21 TB/s), 16384 x 1024 on two 38 us, 777 x 8192 on two 22 us,
+// Measured: 8192 x 4096 fp16 on eight ranks 117 us (6.3 TB/s), 16384 x 1024 on two 38 us, 777 x 8192 on two 22 us,
 // 4096 x 16384 bf16 on one 113 us, 2048 x 32768 141 us; HBM bounds the first, latency between a row's phases the rest.
 template <typename T, int VPT, int THREADS>
 struct BwdShape {
@@ -374,9 +374,11 @@ __global__ void __launch_bounds__(THREADS, BwdShape<T, VPT, THREADS>::BLOCKS)
     const bool live = row < a.rows;
     const int64_t c0 = row * a.nchunks;
     // The block's next row is brought to L2 meanwhile: a row's loads, its barrier and its stores do not overlap, and
-    // there are no registers to load a row ahead (or to have more blocks on the SM).
+    // there are no registers to load a row ahead (or to have more blocks on the SM). Rows of one chunk a thread on
+    // eight ranks or more have enough loads under way without (8192 x 2048: 60 us, with it 65; 16384 x 1024 on two
+    // ranks: 43 us, with it 38).
     const int64_t ahead = row + static_cast<int64_t>(gridDim.x) * rpb;
-    if (ahead < a.rows)
+    if (ahead < a.rows && (VPT > 1 || a.nranks < 8))
       for (int i = t; i < a.nranks + 2; i += tpr) {
         const void* p = i < a.nranks ? in[i] : i == a.nranks ? hidden : dhidden;
         const int bytes = a.cols * static_cast<int>(sizeof(T));
