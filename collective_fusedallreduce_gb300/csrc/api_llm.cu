@@ -38,6 +38,16 @@ bool any_overlap(const std::vector<Range>& a, const std::vector<Range>& b) {
   return false;
 }
 
+// No C++ exception leaves an entry point: running out of host memory is reported as the CUDA error of that name.
+template <typename F>
+coco_status guarded(F&& f) {
+  try {
+    return f();
+  } catch (...) {
+    return cuda_status(cudaErrorMemoryAllocation);
+  }
+}
+
 // Rows and columns of a per-rank tensor (all leading dimensions are rows).
 void rows_cols(const TInfo& t, int64_t* rows, int64_t* cols) {
   *cols = t.local[t.ndim - 1];
@@ -55,10 +65,10 @@ coco_status check_ptr(const void* p, uintptr_t align) {
 
 // -------------------------------------------------------------------- norm
 
-COCO_EXPORT coco_status coco_allreduce_rmsnorm(const coco_tensor* partials, const coco_tensor* residual,
-                                               const void* weight, float eps, const coco_tensor* hidden,
-                                               const coco_tensor* normed, float* const* scales, float* rstd,
-                                               void* stream) {
+static coco_status allreduce_rmsnorm_impl(const coco_tensor* partials, const coco_tensor* residual,
+                                          const void* weight, float eps, const coco_tensor* hidden,
+                                          const coco_tensor* normed, float* const* scales, float* rstd,
+                                          void* stream) {
   TInfo in, res, hid, nrm;
   coco_status st;
   if ((st = check_tensor(partials, &in)) != COCO_OK) return st;
@@ -143,15 +153,24 @@ COCO_EXPORT coco_status coco_allreduce_rmsnorm(const coco_tensor* partials, cons
   return cuda_status(launch_allreduce_rmsnorm(L, static_cast<cudaStream_t>(stream)));
 }
 
+COCO_EXPORT coco_status coco_allreduce_rmsnorm(const coco_tensor* partials, const coco_tensor* residual,
+                                               const void* weight, float eps, const coco_tensor* hidden,
+                                               const coco_tensor* normed, float* const* scales, float* rstd,
+                                               void* stream) {
+  return guarded([&] {
+    return allreduce_rmsnorm_impl(partials, residual, weight, eps, hidden, normed, scales, rstd, stream);
+  });
+}
+
 COCO_EXPORT size_t coco_allreduce_rmsnorm_backward_bytes(int64_t rows, int64_t cols) {
   if (rows < 0 || cols < 0 || rows > (int64_t(1) << 40) || cols > kNormMaxCols) return 0;
   return static_cast<size_t>(norm_backward_parts(rows)) * static_cast<size_t>(cols) * 4;
 }
 
-COCO_EXPORT coco_status coco_allreduce_rmsnorm_backward(const coco_tensor* dnormed, const coco_tensor* dhidden,
-                                                        const coco_tensor* hidden, const void* weight,
-                                                        const float* rstd, const coco_tensor* dx, float* dweight,
-                                                        void* workspace, size_t workspace_bytes, void* stream) {
+static coco_status allreduce_rmsnorm_backward_impl(const coco_tensor* dnormed, const coco_tensor* dhidden,
+                                                   const coco_tensor* hidden, const void* weight,
+                                                   const float* rstd, const coco_tensor* dx, float* dweight,
+                                                   void* workspace, size_t workspace_bytes, void* stream) {
   TInfo in, dh, hid, o;
   coco_status st;
   if ((st = check_tensor(dnormed, &in)) != COCO_OK) return st;
@@ -221,10 +240,20 @@ COCO_EXPORT coco_status coco_allreduce_rmsnorm_backward(const coco_tensor* dnorm
   return cuda_status(launch_rmsnorm_backward(L, s));
 }
 
+COCO_EXPORT coco_status coco_allreduce_rmsnorm_backward(const coco_tensor* dnormed, const coco_tensor* dhidden,
+                                                        const coco_tensor* hidden, const void* weight,
+                                                        const float* rstd, const coco_tensor* dx, float* dweight,
+                                                        void* workspace, size_t workspace_bytes, void* stream) {
+  return guarded([&] {
+    return allreduce_rmsnorm_backward_impl(dnormed, dhidden, hidden, weight, rstd, dx, dweight, workspace,
+                                           workspace_bytes, stream);
+  });
+}
+
 // --------------------------------------------------------------- quantiser
 
-COCO_EXPORT coco_status coco_quantize_fp8(const coco_tensor* x, int32_t block_rows, const coco_tensor* q,
-                                          float* const* scales, void* stream) {
+static coco_status quantize_fp8_impl(const coco_tensor* x, int32_t block_rows, const coco_tensor* q,
+                                     float* const* scales, void* stream) {
   TInfo in, o;
   coco_status st;
   if ((st = check_tensor(x, &in)) != COCO_OK) return st;
@@ -277,6 +306,11 @@ COCO_EXPORT coco_status coco_quantize_fp8(const coco_tensor* x, int32_t block_ro
   return COCO_OK;
 }
 
+COCO_EXPORT coco_status coco_quantize_fp8(const coco_tensor* x, int32_t block_rows, const coco_tensor* q,
+                                          float* const* scales, void* stream) {
+  return guarded([&] { return quantize_fp8_impl(x, block_rows, q, scales, stream); });
+}
+
 // ---------------------------------------------------------------- products
 
 namespace {
@@ -302,7 +336,8 @@ coco_status run_grouped(const TInfo& lhs, const TInfo& rhs, const TInfo& out, co
   tensor_ranges(rhs, &ins, rhs.layout == COCO_REPLICATED);
   if (fp8) {
     const int64_t kb = blocks128(L->k), nb = blocks128(L->n);
-    if (lhs.numel > 0 && (st = check_scales(lhs_scales, lhs, L->rows * kb * 4, lhs.layout == COCO_REPLICATED, &ins)) != COCO_OK)
+    if (lhs.numel > 0 &&
+        (st = check_scales(lhs_scales, lhs, L->rows * kb * 4, lhs.layout == COCO_REPLICATED, &ins)) != COCO_OK)
       return st;
     if (rhs.numel > 0 && (st = check_scales(rhs_scales, rhs, static_cast<int64_t>(L->experts) * kb * nb * 4,
                                             rhs.layout == COCO_REPLICATED, &ins)) != COCO_OK)
@@ -344,9 +379,9 @@ coco_status run_grouped(const TInfo& lhs, const TInfo& rhs, const TInfo& out, co
 
 }  // namespace
 
-COCO_EXPORT coco_status coco_einsum_fp8(const char* spec, const coco_tensor* lhs, const float* const* lhs_scales,
-                                        const coco_tensor* rhs, const float* const* rhs_scales,
-                                        const coco_tensor* out, void* stream) {
+static coco_status einsum_fp8_impl(const char* spec, const coco_tensor* lhs, const float* const* lhs_scales,
+                                   const coco_tensor* rhs, const float* const* rhs_scales,
+                                   const coco_tensor* out, void* stream) {
   const bool kn = spec && same_spec(spec, "mk,kn->mn"), nk = spec && same_spec(spec, "mk,nk->mn");
   if (!kn && !nk) return COCO_ERR_UNSUPPORTED;
   TInfo a, b, o;
@@ -376,9 +411,15 @@ COCO_EXPORT coco_status coco_einsum_fp8(const char* spec, const coco_tensor* lhs
   return run_grouped(a, b, o, lhs_scales, rhs_scales, 0, &L, stream);
 }
 
-COCO_EXPORT coco_status coco_grouped_einsum(const char* spec, const coco_tensor* lhs, const float* const* lhs_scales,
-                                            const coco_tensor* rhs, const float* const* rhs_scales,
-                                            const int32_t* offsets, const coco_tensor* out, void* stream) {
+COCO_EXPORT coco_status coco_einsum_fp8(const char* spec, const coco_tensor* lhs, const float* const* lhs_scales,
+                                        const coco_tensor* rhs, const float* const* rhs_scales,
+                                        const coco_tensor* out, void* stream) {
+  return guarded([&] { return einsum_fp8_impl(spec, lhs, lhs_scales, rhs, rhs_scales, out, stream); });
+}
+
+static coco_status grouped_einsum_impl(const char* spec, const coco_tensor* lhs, const float* const* lhs_scales,
+                                       const coco_tensor* rhs, const float* const* rhs_scales,
+                                       const int32_t* offsets, const coco_tensor* out, void* stream) {
   int form;
   if (spec && same_spec(spec, "tk,ekn->tn")) form = GRP_KN;
   else if (spec && same_spec(spec, "tk,enk->tn")) form = GRP_NK;
@@ -420,4 +461,10 @@ COCO_EXPORT coco_status coco_grouped_einsum(const char* spec, const coco_tensor*
   L.offsets = offsets;
   return run_grouped(a, b, o, lhs_scales, rhs_scales,
                      static_cast<int64_t>(a.nranks) * a.ngroups * (experts + 1) * 4, &L, stream);
+}
+
+COCO_EXPORT coco_status coco_grouped_einsum(const char* spec, const coco_tensor* lhs, const float* const* lhs_scales,
+                                            const coco_tensor* rhs, const float* const* rhs_scales,
+                                            const int32_t* offsets, const coco_tensor* out, void* stream) {
+  return guarded([&] { return grouped_einsum_impl(spec, lhs, lhs_scales, rhs, rhs_scales, offsets, out, stream); });
 }

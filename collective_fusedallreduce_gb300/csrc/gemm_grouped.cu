@@ -944,7 +944,7 @@ struct FewCfg {
   static constexpr uint32_t COLS = ACCS * ROWS < 32 ? 32 : ACCS * ROWS;
   static constexpr int RED_OFF = STAGES * STAGE;
   static constexpr int BAR_OFF = RED_OFF + RED_BYTES;
-  static constexpr int NUM_BARS = 2 * STAGES + 2 * ACCS + 2;         // full, empty; accumulators full, empty; drain; sums
+  static constexpr int NUM_BARS = 2 * STAGES + 2 * ACCS + 2;  // full, empty; accumulators full, empty; drain; sums
   static constexpr int SMEM_BYTES = BAR_OFF + 8 * NUM_BARS + 16 + 1024;
   static_assert(SMEM_BYTES <= 232448, "shared memory over the per-CTA limit");
 };
@@ -1000,7 +1000,8 @@ __device__ __forceinline__ void store_one(void* out, int64_t i, int dtype, float
 }
 
 template <bool SCALED, int ROWS>
-__global__ void __launch_bounds__(FewCfg<SCALED, ROWS>::THREADS, 1) k_grouped_few(const __grid_constant__ GroupedParams P) {
+__global__ void __launch_bounds__(FewCfg<SCALED, ROWS>::THREADS, 1)
+    k_grouped_few(const __grid_constant__ GroupedParams P) {
   using C = FewCfg<SCALED, ROWS>;
   constexpr int STAGES_ = C::STAGES, ACCS = C::ACCS;
   extern __shared__ uint8_t smem_raw[];
@@ -1019,6 +1020,9 @@ __global__ void __launch_bounds__(FewCfg<SCALED, ROWS>::THREADS, 1) k_grouped_fe
   const int split = P.split;
   const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int cluster_id = blockIdx.x / split, nclusters = gridDim.x / split;
+  // A cluster that shares a tile's k range has one tile at most (the launch has as many clusters as there can be
+  // tiles); offsets that descend could number more, which are left out rather than mixed into the first one's sums.
+  const int u_end = split > 1 ? nclusters : INT32_MAX;
   // this CTA's part of every tile's k range
   const int kb0 = static_cast<int>(static_cast<int64_t>(P.kblocks) * rank / split);
   const int kb1 = static_cast<int>(static_cast<int64_t>(P.kblocks) * (rank + 1) / split);
@@ -1061,7 +1065,7 @@ __global__ void __launch_bounds__(FewCfg<SCALED, ROWS>::THREADS, 1) k_grouped_fe
     int stage = 0;
     uint32_t phase = 0, issued = 0, parity = 0;
     bool ok = true;
-    for (int u = cluster_id; ok && walk_find<false>(P, w, u, t, ROWS, FEW_N); u += nclusters) {
+    for (int u = cluster_id; ok && u < u_end && walk_find<false>(P, w, u, t, ROWS, FEW_N); u += nclusters) {
       const CUtensorMap *mx = &P.a[t.p], *mw = &P.b[t.p];
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!wait_bar_warp(empty_bar(stage), phase ^ 1u, abort_flag)) {
@@ -1095,7 +1099,7 @@ __global__ void __launch_bounds__(FewCfg<SCALED, ROWS>::THREADS, 1) k_grouped_fe
     const bool leader = elect_one();
     const uint32_t idesc = P.idesc, wstep = P.bstep;
     const uint64_t wd0 = tile_desc(sbase, P.blead), xd0 = tile_desc(sbase + C::W_BYTES, 1);
-    const int total = walk_total<false>(P, ROWS, FEW_N);
+    const int total = min(walk_total<false>(P, ROWS, FEW_N), u_end);
     int stage = 0, acc = 0;
     uint32_t phase = 0, accph = 0;
     bool ok = true, any_mma = false;
@@ -1161,7 +1165,7 @@ __global__ void __launch_bounds__(FewCfg<SCALED, ROWS>::THREADS, 1) k_grouped_fe
       if (lane == 0) mbar_arrive_relaxed(tempty_bar(acc));
       if (++acc == ACCS) { acc = 0; accph ^= 1u; }
     };
-    for (int u = cluster_id; ok && walk_find<false>(P, w, u, t, ROWS, FEW_N); u += nclusters) {
+    for (int u = cluster_id; ok && u < u_end && walk_find<false>(P, w, u, t, ROWS, FEW_N); u += nclusters) {
       float sum[PW];
       uint32_t r[PW];
       if constexpr (SCALED) {
@@ -1225,6 +1229,7 @@ __global__ void __launch_bounds__(FewCfg<SCALED, ROWS>::THREADS, 1) k_grouped_fe
         }
       }
     }
+    if (!ok && split > 1) wait_bar_cluster(red_bar, 0, never);  // let the peers' sums land
     if (P.offsets)
       clear_rest(P, static_cast<int64_t>(blockIdx.x) * (C::THREADS - 64) + threadIdx.x - 64,
                  static_cast<int64_t>(gridDim.x) * (C::THREADS - 64));
@@ -1398,8 +1403,9 @@ cudaError_t launch_grouped(const GroupedLaunch& L, cudaStream_t s, unsigned int*
     if (!good) return cudaErrorNotSupported;
   }
   if (few.rows) {
-    const cudaError_t e = few.rows == 16 ? (fp8 ? launch_few<true, 16>(P, few, 3, s) : launch_few<false, 16>(P, few, 4, s))
-                                         : (fp8 ? launch_few<true, 64>(P, few, 5, s) : launch_few<false, 64>(P, few, 6, s));
+    cudaError_t e;
+    if (few.rows == 16) e = fp8 ? launch_few<true, 16>(P, few, 3, s) : launch_few<false, 16>(P, few, 4, s);
+    else e = fp8 ? launch_few<true, 64>(P, few, 5, s) : launch_few<false, 64>(P, few, 6, s);
     if (e != cudaSuccess) return e;
     count_launch();
     return cudaGetLastError();

@@ -19,6 +19,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "internal.h"
 
 namespace coco {
@@ -44,15 +46,19 @@ __device__ __forceinline__ uint4 ld_stream(const void* p) {
 template <typename T>
 struct Chunk {
   uint4 v;
-  __device__ __forceinline__ void load(const void* base, int64_t c) { v = ld_stream(static_cast<const uint4*>(base) + c); }
-  __device__ __forceinline__ void load_cached(const void* base, int64_t c) { v = static_cast<const uint4*>(base)[c]; }
+  __device__ __forceinline__ void load(const void* base, int64_t c) {
+    v = ld_stream(static_cast<const uint4*>(base) + c);
+  }
+  __device__ __forceinline__ void load_cached(const void* base, int64_t c) {
+    v = static_cast<const uint4*>(base)[c];
+  }
   __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ void get(float (&f)[kChunk]) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float2 p;
-      if constexpr (sizeof(T) == 2 && std::is_same<T, __half>::value) p = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      if constexpr (std::is_same<T, __half>::value) p = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
       else p = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
       f[2 * i] = p.x;
       f[2 * i + 1] = p.y;
@@ -223,7 +229,8 @@ struct NormArgs {
 // registers) took 8192 x 4096 fp16 on eight ranks, eight copies, from 233 to 213 us (6.64 TB/s); three had not
 // been enough.
 template <typename T, int NR, int VPT, bool FP8>
-__global__ void __launch_bounds__(512, VPT == 1 && NR > 0 && sizeof(T) == 2 ? 4 : 1) k_allreduce_rmsnorm(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(512, VPT == 1 && NR > 0 && sizeof(T) == 2 ? 4 : 1)
+    k_allreduce_rmsnorm(const __grid_constant__ NormArgs a) {
   __shared__ float red[2][32];
   const int g = blockIdx.y;
   const int tpr = 1 << a.tpr_log2;
@@ -309,8 +316,8 @@ __global__ void __launch_bounds__(512, VPT == 1 && NR > 0 && sizeof(T) == 2 ? 4 
 //
 // With xhat = h * rstd and g = dy * w (dy: the sum of the ranks' gradients):
 //   dx = rstd * (g - xhat * mean(g * xhat)) + dhidden,   dw = sum over rows of dy * xhat.
-// One or two blocks an SM walk rows, as many at a time as their threads hold; a thread keeps the dw sums of its own columns
-// in registers over all its rows, the block's rows join them in shared memory, and the block writes them once to
+// One or two blocks an SM walk rows, as many at a time as their threads hold; a thread keeps the dw sums of its own
+// columns in registers over all its rows, the block's rows join them in shared memory, and the block writes them once to
 // the workspace ([blocks][cols]), which k_norm_dweight adds in block order: no atomics, so repeated calls give the
 // same bits.
 
@@ -678,7 +685,8 @@ cudaError_t bwd_vpt(NormBwdArgs& a, int groups, int* parts, cudaStream_t s) {
   if constexpr (sizeof(T) == 2) {
     if (a.nchunks > 1024) {
       a.tpr_log2 = 10;
-      return a.nchunks <= 2048 ? bwd_go<T, NR, 2, 1024>(a, groups, parts, s) : bwd_go<T, NR, 4, 1024>(a, groups, parts, s);
+      return a.nchunks <= 2048 ? bwd_go<T, NR, 2, 1024>(a, groups, parts, s)
+                               : bwd_go<T, NR, 4, 1024>(a, groups, parts, s);
     }
     return r.vpt == 1 ? bwd_go<T, NR, 1, 512>(a, groups, parts, s) : bwd_go<T, NR, 2, 512>(a, groups, parts, s);
   } else {
