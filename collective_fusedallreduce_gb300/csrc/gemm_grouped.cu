@@ -83,6 +83,7 @@ struct Tile {
   int p, e;    // problem and expert
   int r0, r1;  // the expert's rows
   int m0, n0;  // the tile's first row (of the expert; weight gradients: first row of k) and column
+  int first = 0, end = 0;  // the expert's units
 };
 
 // A warp's view of 32 consecutive (problem, expert) pairs: lane l holds pair base + l.
@@ -121,25 +122,33 @@ __device__ __forceinline__ void walk_load(const GroupedParams& P, Walk& w, int b
 // The tile of unit u (ascending from call to call), or false past the last one. The whole warp calls it.
 template <bool GRAD>
 __device__ __forceinline__ bool walk_find(const GroupedParams& P, Walk& w, int u, Tile& t, int tm, int tn) {
-  for (;;) {
-    const int last = __shfl_sync(0xffffffffu, w.upto, 31);
-    if (u < last) break;
-    if (w.base + 32 >= P.nprob * P.experts) return false;
-    walk_load<GRAD>(P, w, w.base + 32, last, tm, tn);
+  if (u >= t.end) {  // (else the same expert as last time)
+    for (;;) {
+      const int last = __shfl_sync(0xffffffffu, w.upto, 31);
+      if (u < last) break;
+      if (w.base + 32 >= P.nprob * P.experts) return false;
+      walk_load<GRAD>(P, w, w.base + 32, last, tm, tn);
+    }
+    const int f = __ffs(__ballot_sync(0xffffffffu, u < w.upto)) - 1;
+    const int pe = w.base + f;
+    t.p = pe / P.experts;
+    t.e = pe - t.p * P.experts;
+    t.r0 = __shfl_sync(0xffffffffu, w.r0, f);
+    t.r1 = __shfl_sync(0xffffffffu, w.r1, f);
+    t.end = __shfl_sync(0xffffffffu, w.upto, f);
+    t.first = t.end - __shfl_sync(0xffffffffu, w.tiles, f);
   }
-  const int f = __ffs(__ballot_sync(0xffffffffu, u < w.upto)) - 1;
-  const int pe = w.base + f;
-  t.p = pe / P.experts;
-  t.e = pe - t.p * P.experts;
-  t.r0 = __shfl_sync(0xffffffffu, w.r0, f);
-  t.r1 = __shfl_sync(0xffffffffu, w.r1, f);
-  const int local = u - (__shfl_sync(0xffffffffu, w.upto, f) - __shfl_sync(0xffffffffu, w.tiles, f));
+  // tiles in groups of GROUP_MT m-tiles, n-major inside a group
   const int mts = ((GRAD ? P.k : t.r1 - t.r0) + tm - 1) / tm, nts = (P.n + tn - 1) / tn;
-  const int group = local / (GROUP_MT * nts);
-  const int gm = min(GROUP_MT, mts - group * GROUP_MT);
-  const int in_g = local - group * GROUP_MT * nts;
-  const int nt = in_g / gm;
-  t.m0 = (group * GROUP_MT + in_g - nt * gm) * tm;
+  int in_g = u - t.first, gm = mts, mt = 0;
+  if (mts > GROUP_MT) {
+    const int group = in_g / (GROUP_MT * nts);
+    in_g -= group * GROUP_MT * nts;
+    mt = group * GROUP_MT;
+    gm = min(GROUP_MT, mts - mt);
+  }
+  const int nt = gm == GROUP_MT ? in_g / GROUP_MT : in_g / gm;
+  t.m0 = (mt + in_g - nt * gm) * tm;
   t.n0 = nt * tn;
   return true;
 }
@@ -591,28 +600,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const bool none = t.r1 == t.r0;    // no rows: the gradient is zero
         if (!none && !wait_acc()) { ok = false; break; }
         const uint32_t ta = tacc + acc * TILE_N;
-        const int strips = esize == 4 ? 4 : 2;
-        for (int c = 0; c < strips; ++c) {
-          uint32_t p[32];
-          if (none) {
+        if (esize == 4) {
+          for (int c = 0; c < 4; ++c) {
+            uint32_t p[32];
+            if (none) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) p[j] = 0u;
-          } else if (esize == 4) {
-            tmem_ld32(ta + 32 * c, p);
-            tmem_ld_wait();
-          } else {
-            uint32_t r0[32], r1[32];
-            tmem_ld32(ta + 64 * c, r0);
-            tmem_ld32(ta + 64 * c + 32, r1);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              p[j] = cvt_pair(__uint_as_float(r0[2 * j]), __uint_as_float(r0[2 * j + 1]), P.out_dtype);
-              p[16 + j] = cvt_pair(__uint_as_float(r1[2 * j]), __uint_as_float(r1[2 * j + 1]), P.out_dtype);
+              for (int j = 0; j < 32; ++j) p[j] = 0u;
+            } else {
+              tmem_ld32(ta + 32 * c, p);
+              tmem_ld_wait();
+              if (c == 3) free_acc();
             }
+            if (rows > 0 && bytes > 128 * c) store_strip(strip, p, out + 128 * c, pitch, rows, bytes - 128 * c);
           }
-          if (!none && c == strips - 1) free_acc();
-          if (rows > 0 && bytes > 128 * c) store_strip(strip, p, out + 128 * c, pitch, rows, bytes - 128 * c);
+        } else {  // (the accumulator is read, and handed back, before the first store)
+          uint32_t p[2][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t r[32];
+            if (none) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) r[j] = 0u;
+            } else {
+              tmem_ld32(ta + 32 * c, r);
+              tmem_ld_wait();
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              p[c / 2][16 * (c & 1) + j] =
+                  cvt_pair(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]), P.out_dtype);
+          }
+          if (!none) free_acc();
+          if (rows > 0 && bytes > 0) store_strip(strip, p[0], out, pitch, rows, bytes);
+          if (rows > 0 && bytes > 128) store_strip(strip, p[1], out + 128, pitch, rows, bytes - 128);
         }
       } else {
         // lanes are the output's columns, TMEM columns its rows: this warp's 32 columns of up to 128 rows
@@ -834,7 +854,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const int64_t sb_k = P.sb_k;
       park(strip, 0, w.base); park(strip, 1, w.r0); park(strip, 2, w.r1); park(strip, 3, w.tiles);
       park(strip, 4, w.upto); park(strip, 5, t.p); park(strip, 6, t.r0); park(strip, 7, t.r1);
-      park(strip, 8, t.m0); park(strip, 9, t.n0); park(strip, 10, u);
+      park(strip, 8, t.m0); park(strip, 9, t.n0); park(strip, 10, u); park(strip, 11, t.first);
+      park(strip, 12, t.end); park(strip, 13, t.e);
       float a_s = __ldg(sa), b_s = __ldg(sb);
       for (int left = P.kblocks; left > 0; --left) {
         const float s = a_s * b_s;
@@ -871,7 +892,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (!ok) break;
       w.base = unpark(strip, 0); w.r0 = unpark(strip, 1); w.r1 = unpark(strip, 2); w.tiles = unpark(strip, 3);
       w.upto = unpark(strip, 4); t.p = unpark(strip, 5); t.r0 = unpark(strip, 6); t.r1 = unpark(strip, 7);
-      t.m0 = unpark(strip, 8); t.n0 = unpark(strip, 9); u = unpark(strip, 10);
+      t.m0 = unpark(strip, 8); t.n0 = unpark(strip, 9); u = unpark(strip, 10); t.first = unpark(strip, 11);
+      t.end = unpark(strip, 12); t.e = unpark(strip, 13);
       __syncwarp();  // (the strip is written again below)
       const int row = t.m0 + 128 * rank + quarter * 32;  // this warp's first one
       const int rows = min(32, t.r1 - t.r0 - row);       // (may be negative: nothing to store)
