@@ -256,7 +256,9 @@ __device__ __forceinline__ int unpark(uint32_t strip, int i) {
 }
 
 // Writes 32 rows x 128 bytes held one row per lane: through shared memory, so that each store instruction
-// covers four whole 128-byte lines, and bounded by rows and bytes, so that a tile may end anywhere.
+// covers four whole 128-byte lines, and bounded by rows and bytes, so that a tile may end anywhere. AT_ONCE: 8, or
+// 4 in the kernel whose registers hold sums meanwhile.
+template <int AT_ONCE = 8>
 __device__ __forceinline__ void store_strip(uint32_t strip, const uint32_t (&p)[32], char* out, int64_t pitch,
                                             int rows, int64_t bytes) {
   // The lane is read anew (volatile): the two dozen addresses below would otherwise be computed once, ahead of the
@@ -267,12 +269,20 @@ __device__ __forceinline__ void store_strip(uint32_t strip, const uint32_t (&p)[
   for (int c = 0; c < 8; ++c)
     st_shared_v4(strip + lane * 128 + ((c ^ (lane & 7)) << 4), p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
   __syncwarp();
+  // (AT_ONCE loads before their stores: one at a time, each waited for shared memory)
   const int ch = lane & 7;
+  char* o = out + (lane >> 3) * pitch + ch * 16;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int row = i * 4 + (lane >> 3);
-    const uint4 v = ld_shared_v4(strip + row * 128 + ((ch ^ (row & 7)) << 4));
-    if (row < rows && ch * 16 < bytes) *reinterpret_cast<uint4*>(out + row * pitch + ch * 16) = v;
+  for (int i0 = 0; i0 < 8; i0 += AT_ONCE) {
+    uint4 v[AT_ONCE];
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) {
+      const int row = (i0 + i) * 4 + (lane >> 3);
+      v[i] = ld_shared_v4(strip + row * 128 + ((ch ^ (row & 7)) << 4));
+    }
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i, o += 4 * pitch)
+      if ((i0 + i) * 4 + (lane >> 3) < rows && ch * 16 < bytes) *reinterpret_cast<uint4*>(o) = v[i];
   }
   __syncwarp();
 }
@@ -288,12 +298,14 @@ __device__ __forceinline__ void store_turned(uint32_t strip, const uint32_t (&r)
     for (int j = 0; j < 32; ++j)
       asm volatile("st.shared.u32 [%0], %1;" ::"r"(strip + j * 128 + lane * 4), "r"(r[j]) : "memory");
     __syncwarp();
+    const int row0 = lane >> 3, at = (lane & 7) * 16;
+    uint4 v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int row = i * 4 + (lane >> 3), at = (lane & 7) * 16;
-      const uint4 v = ld_shared_v4(strip + row * 128 + at);
-      if (row < rows && at < bytes) *reinterpret_cast<uint4*>(out + row * pitch + at) = v;
-    }
+    for (int i = 0; i < 8; ++i) v[i] = ld_shared_v4(strip + (i * 4 + row0) * 128 + at);
+    char* o = out + row0 * pitch + at;
+#pragma unroll
+    for (int i = 0; i < 8; ++i, o += 4 * pitch)
+      if (i * 4 + row0 < rows && at < bytes) *reinterpret_cast<uint4*>(o) = v[i];
   } else {
 #pragma unroll
     for (int j = 0; j < 32; j += 2) {
@@ -305,12 +317,14 @@ __device__ __forceinline__ void store_turned(uint32_t strip, const uint32_t (&r)
                    : "memory");
     }
     __syncwarp();
+    const int row0 = lane >> 2, at = (lane & 3) * 16;
+    uint4 v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = i * 8 + (lane >> 2), at = (lane & 3) * 16;
-      const uint4 v = ld_shared_v4(strip + row * 64 + at);
-      if (row < rows && at < bytes) *reinterpret_cast<uint4*>(out + row * pitch + at) = v;
-    }
+    for (int i = 0; i < 4; ++i) v[i] = ld_shared_v4(strip + (i * 8 + row0) * 64 + at);
+    char* o = out + row0 * pitch + at;
+#pragma unroll
+    for (int i = 0; i < 4; ++i, o += 8 * pitch)
+      if (i * 8 + row0 < rows && at < bytes) *reinterpret_cast<uint4*>(o) = v[i];
   }
   __syncwarp();
 }
@@ -909,7 +923,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             uint32_t p[32];
 #pragma unroll
             for (int j = 0; j < 16; ++j) unpack2(sum[16 * c + j], p[2 * j], p[2 * j + 1]);
-            store_strip(strip, p, out + 128 * c, pitch, rows, bytes - 128 * c);
+            store_strip<4>(strip, p, out + 128 * c, pitch, rows, bytes - 128 * c);
           }
         } else {
 #pragma unroll
@@ -921,7 +935,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
               unpack2(sum[32 * c + j], x, y);
               p[j] = cvt_pair(__uint_as_float(x), __uint_as_float(y), P.out_dtype);
             }
-            store_strip(strip, p, out + 128 * c, pitch, rows, bytes - 128 * c);
+            store_strip<4>(strip, p, out + 128 * c, pitch, rows, bytes - 128 * c);
           }
         }
       }
