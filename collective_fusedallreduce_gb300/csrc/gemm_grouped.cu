@@ -21,6 +21,9 @@
 // an MMA's N goes in steps of 32, so an expert's last tile costs what its rows
 // cost and not 256 (32 experts of 126 to 4000 rows: a quarter of the work). In
 // weight gradients A holds lhs columns, B rhs columns, and the rows are summed.
+// 16384 rows over 32 uneven experts, k 4096, n 2048 in bf16: 188 us (1.46
+// PFLOP/s), its weight gradient 205 us, of which storing 537 MB is a good part
+// (64 rows an expert: 97 us); one expert of 16384 rows 145 and 154 us.
 //   warp 0        TMA producer: k-blocks 128 bytes deep into a ring of 6 stages of 32 KB.
 //   warp 1        issues the MMAs (CTA 0 of the pair) and owns TMEM.
 //   warps 2, 3    in weight gradients: clear what a k-block holds of the next expert's rows.
@@ -83,7 +86,6 @@ struct Tile {
   int p, e;    // problem and expert
   int r0, r1;  // the expert's rows
   int m0, n0;  // the tile's first row (of the expert; weight gradients: first row of k) and column
-  int first = 0, end = 0;  // the expert's units
 };
 
 // A warp's view of 32 consecutive (problem, expert) pairs: lane l holds pair base + l.
@@ -122,33 +124,25 @@ __device__ __forceinline__ void walk_load(const GroupedParams& P, Walk& w, int b
 // The tile of unit u (ascending from call to call), or false past the last one. The whole warp calls it.
 template <bool GRAD>
 __device__ __forceinline__ bool walk_find(const GroupedParams& P, Walk& w, int u, Tile& t, int tm, int tn) {
-  if (u >= t.end) {  // (else the same expert as last time)
-    for (;;) {
-      const int last = __shfl_sync(0xffffffffu, w.upto, 31);
-      if (u < last) break;
-      if (w.base + 32 >= P.nprob * P.experts) return false;
-      walk_load<GRAD>(P, w, w.base + 32, last, tm, tn);
-    }
-    const int f = __ffs(__ballot_sync(0xffffffffu, u < w.upto)) - 1;
-    const int pe = w.base + f;
-    t.p = pe / P.experts;
-    t.e = pe - t.p * P.experts;
-    t.r0 = __shfl_sync(0xffffffffu, w.r0, f);
-    t.r1 = __shfl_sync(0xffffffffu, w.r1, f);
-    t.end = __shfl_sync(0xffffffffu, w.upto, f);
-    t.first = t.end - __shfl_sync(0xffffffffu, w.tiles, f);
+  for (;;) {
+    const int last = __shfl_sync(0xffffffffu, w.upto, 31);
+    if (u < last) break;
+    if (w.base + 32 >= P.nprob * P.experts) return false;
+    walk_load<GRAD>(P, w, w.base + 32, last, tm, tn);
   }
-  // tiles in groups of GROUP_MT m-tiles, n-major inside a group
+  const int f = __ffs(__ballot_sync(0xffffffffu, u < w.upto)) - 1;
+  const int pe = w.base + f;
+  t.p = pe / P.experts;
+  t.e = pe - t.p * P.experts;
+  t.r0 = __shfl_sync(0xffffffffu, w.r0, f);
+  t.r1 = __shfl_sync(0xffffffffu, w.r1, f);
+  const int local = u - (__shfl_sync(0xffffffffu, w.upto, f) - __shfl_sync(0xffffffffu, w.tiles, f));
   const int mts = ((GRAD ? P.k : t.r1 - t.r0) + tm - 1) / tm, nts = (P.n + tn - 1) / tn;
-  int in_g = u - t.first, gm = mts, mt = 0;
-  if (mts > GROUP_MT) {
-    const int group = in_g / (GROUP_MT * nts);
-    in_g -= group * GROUP_MT * nts;
-    mt = group * GROUP_MT;
-    gm = min(GROUP_MT, mts - mt);
-  }
-  const int nt = gm == GROUP_MT ? in_g / GROUP_MT : in_g / gm;
-  t.m0 = (mt + in_g - nt * gm) * tm;
+  const int group = local / (GROUP_MT * nts);
+  const int gm = min(GROUP_MT, mts - group * GROUP_MT);
+  const int in_g = local - group * GROUP_MT * nts;
+  const int nt = in_g / gm;
+  t.m0 = (group * GROUP_MT + in_g - nt * gm) * tm;
   t.n0 = nt * tn;
   return true;
 }
@@ -256,9 +250,7 @@ __device__ __forceinline__ int unpark(uint32_t strip, int i) {
 }
 
 // Writes 32 rows x 128 bytes held one row per lane: through shared memory, so that each store instruction
-// covers four whole 128-byte lines, and bounded by rows and bytes, so that a tile may end anywhere. AT_ONCE: 8, or
-// 4 in the kernel whose registers hold sums meanwhile.
-template <int AT_ONCE = 8>
+// covers four whole 128-byte lines, and bounded by rows and bytes, so that a tile may end anywhere.
 __device__ __forceinline__ void store_strip(uint32_t strip, const uint32_t (&p)[32], char* out, int64_t pitch,
                                             int rows, int64_t bytes) {
   // The lane is read anew (volatile): the two dozen addresses below would otherwise be computed once, ahead of the
@@ -269,21 +261,18 @@ __device__ __forceinline__ void store_strip(uint32_t strip, const uint32_t (&p)[
   for (int c = 0; c < 8; ++c)
     st_shared_v4(strip + lane * 128 + ((c ^ (lane & 7)) << 4), p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
   __syncwarp();
-  // (AT_ONCE loads before their stores: one at a time, each waited for shared memory)
+  // (all loads before the first store: one at a time, each waited for shared memory)
   const int ch = lane & 7;
+  uint4 v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = i * 4 + (lane >> 3);
+    v[i] = ld_shared_v4(strip + row * 128 + ((ch ^ (row & 7)) << 4));
+  }
   char* o = out + (lane >> 3) * pitch + ch * 16;
 #pragma unroll
-  for (int i0 = 0; i0 < 8; i0 += AT_ONCE) {
-    uint4 v[AT_ONCE];
-#pragma unroll
-    for (int i = 0; i < AT_ONCE; ++i) {
-      const int row = (i0 + i) * 4 + (lane >> 3);
-      v[i] = ld_shared_v4(strip + row * 128 + ((ch ^ (row & 7)) << 4));
-    }
-#pragma unroll
-    for (int i = 0; i < AT_ONCE; ++i, o += 4 * pitch)
-      if ((i0 + i) * 4 + (lane >> 3) < rows && ch * 16 < bytes) *reinterpret_cast<uint4*>(o) = v[i];
-  }
+  for (int i = 0; i < 8; ++i, o += 4 * pitch)
+    if (i * 4 + (lane >> 3) < rows && ch * 16 < bytes) *reinterpret_cast<uint4*>(o) = v[i];
   __syncwarp();
 }
 
@@ -688,8 +677,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 // each CTA issues its own MMAs (M = 128, N = 256) on its own rows. The block's product has to be added up and its
 // TMEM buffer handed back every 128 k, and with one MMA over both CTAs that hand-over crossed CTAs both ways
 // (commit to the other's epilogue, arrivals back), some thousand cycles of every two blocks' 1024: 8192^3 took
-// 424 us. Here it stays within the CTA. The two still share what they read: each loads 128 of the tile's columns
-// of rhs and multicasts them to both, so a CTA reads 32 KB a block as in the pair.
+// 424 us, and 386 us here (2.85 PFLOP/s from a graph; 440 to 460 in a long loop, at the power cap's 1.7 GHz), where
+// it stays within the CTA. Without the sums (a TMEM buffer handed back unread) the same loop takes 322 us, so what
+// bounds it is the power and the epilogue's loop: 8 TMEM loads, 64 packed multiply-adds and the hand-over a block.
+// The two CTAs still share what they read: each loads 128 of the tile's columns of rhs and multicasts them to both,
+// so a CTA reads 32 KB a block as in the pair.
 //   warp 0        TMA producer: lhs rows to itself, its half of the rhs columns to both CTAs; 4 stages of 48 KB.
 //   warp 1        issues the MMAs and owns TMEM (two buffers of 256 columns).
 //   warps 4..11   two per TMEM lane quarter, 128 columns each: sums of the scaled blocks in registers, then stores.
@@ -868,8 +860,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const int64_t sb_k = P.sb_k;
       park(strip, 0, w.base); park(strip, 1, w.r0); park(strip, 2, w.r1); park(strip, 3, w.tiles);
       park(strip, 4, w.upto); park(strip, 5, t.p); park(strip, 6, t.r0); park(strip, 7, t.r1);
-      park(strip, 8, t.m0); park(strip, 9, t.n0); park(strip, 10, u); park(strip, 11, t.first);
-      park(strip, 12, t.end); park(strip, 13, t.e);
+      park(strip, 8, t.m0); park(strip, 9, t.n0); park(strip, 10, u);
       float a_s = __ldg(sa), b_s = __ldg(sb);
       for (int left = P.kblocks; left > 0; --left) {
         const float s = a_s * b_s;
@@ -906,8 +897,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (!ok) break;
       w.base = unpark(strip, 0); w.r0 = unpark(strip, 1); w.r1 = unpark(strip, 2); w.tiles = unpark(strip, 3);
       w.upto = unpark(strip, 4); t.p = unpark(strip, 5); t.r0 = unpark(strip, 6); t.r1 = unpark(strip, 7);
-      t.m0 = unpark(strip, 8); t.n0 = unpark(strip, 9); u = unpark(strip, 10); t.first = unpark(strip, 11);
-      t.end = unpark(strip, 12); t.e = unpark(strip, 13);
+      t.m0 = unpark(strip, 8); t.n0 = unpark(strip, 9); u = unpark(strip, 10);
       __syncwarp();  // (the strip is written again below)
       const int row = t.m0 + 128 * rank + quarter * 32;  // this warp's first one
       const int rows = min(32, t.r1 - t.r0 - row);       // (may be negative: nothing to store)
@@ -923,7 +913,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             uint32_t p[32];
 #pragma unroll
             for (int j = 0; j < 16; ++j) unpack2(sum[16 * c + j], p[2 * j], p[2 * j + 1]);
-            store_strip<4>(strip, p, out + 128 * c, pitch, rows, bytes - 128 * c);
+            store_strip(strip, p, out + 128 * c, pitch, rows, bytes - 128 * c);
           }
         } else {
 #pragma unroll
@@ -935,7 +925,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
               unpack2(sum[32 * c + j], x, y);
               p[j] = cvt_pair(__uint_as_float(x), __uint_as_float(y), P.out_dtype);
             }
-            store_strip<4>(strip, p, out + 128 * c, pitch, rows, bytes - 128 * c);
+            store_strip(strip, p, out + 128 * c, pitch, rows, bytes - 128 * c);
           }
         }
       }
@@ -962,7 +952,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 // (ROWS = 16 or 64): out^T = rhs^T lhs^T, one CTA an MMA, no weight read twice, no idle rows to speak of.
 // Where there are fewer tiles than SMs, a cluster of `split` CTAs shares a tile's k range: each sends its fp32
 // sums for another's rows straight into that CTA's shared memory (st.async, counted on an mbarrier), which
-// adds them in rank order. No atomics, no workspace: repeated calls give the same bits.
+// adds them in rank order. No atomics, no workspace: repeated calls give the same bits. One row, k = n = 4096 in
+// e4m3: 7.3 us (2.3 TB/s), most of it the launch, the ring's first fill and the clusters' exchange; 32 rows over 64
+// experts, k 4096, n 2048: 30 us (5 TB/s of the weights met), the last wave of tiles being partly filled.
 //   warp 0        TMA producer, a ring of 128-byte deep k-blocks: 16 KB of weights, ROWS x 128 bytes of lhs.
 //   warp 1        issues the MMAs and owns TMEM.
 //   warps 2..     epilogue, one per TMEM lane quarter (ROWS = 64: two, 32 rows each): a lane holds one column n.
