@@ -677,9 +677,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 // each CTA issues its own MMAs (M = 128, N = 256) on its own rows. The block's product has to be added up and its
 // TMEM buffer handed back every 128 k, and with one MMA over both CTAs that hand-over crossed CTAs both ways
 // (commit to the other's epilogue, arrivals back), some thousand cycles of every two blocks' 1024: 8192^3 took
-// 424 us, and 386 us here (2.85 PFLOP/s from a graph; 440 to 460 in a long loop, at the power cap's 1.7 GHz), where
-// it stays within the CTA. Without the sums (a TMEM buffer handed back unread) the same loop takes 322 us, so what
-// bounds it is the power and the epilogue's loop: 8 TMEM loads, 64 packed multiply-adds and the hand-over a block.
+// 424 us, and 388 us here (2.83 PFLOP/s from a graph; 440 to 460 in a long loop, at the power cap's 1.7 GHz), where
+// it stays within the CTA. Without the sums (a TMEM buffer handed back unread) the loop took 322 us beside 378
+// with, so what bounds it is the power and the epilogue's loop: 8 TMEM loads, 64 packed multiply-adds and the
+// hand-over a block.
 // The two CTAs still share what they read: each loads 128 of the tile's columns of rhs and multicasts them to both,
 // so a CTA reads 32 KB a block as in the pair.
 //   warp 0        TMA producer: lhs rows to itself, its half of the rhs columns to both CTAs; 4 stages of 48 KB.
@@ -954,7 +955,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 // sums for another's rows straight into that CTA's shared memory (st.async, counted on an mbarrier), which
 // adds them in rank order. No atomics, no workspace: repeated calls give the same bits. One row, k = n = 4096 in
 // e4m3: 7.3 us (2.3 TB/s), most of it the launch, the ring's first fill and the clusters' exchange; 32 rows over 64
-// experts, k 4096, n 2048: 30 us (5 TB/s of the weights met), the last wave of tiles being partly filled.
+// experts, k 4096, n 2048: 34 us (4.5 TB/s of the weights met), the last wave of tiles being partly filled.
 //   warp 0        TMA producer, a ring of 128-byte deep k-blocks: 16 KB of weights, ROWS x 128 bytes of lhs.
 //   warp 1        issues the MMAs and owns TMEM.
 //   warps 2..     epilogue, one per TMEM lane quarter (ROWS = 64: two, 32 rows each): a lane holds one column n.

@@ -132,8 +132,9 @@ __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
 
 // Eight values over a block's scale, in e4m3 (round to nearest even). The quotient is the value times the
 // scale's rounded reciprocal, corrected by its own residual (Markstein, "Computation of elementary functions on
-// the IBM RISC System/6000 processor", 1990), which makes it the rounded quotient: with the product alone, one
-// value in some hundred thousand falls on the other side of a rounding boundary. An infinite scale keeps the
+// the IBM RISC System/6000 processor", 1990), which makes it the rounded quotient: with the product alone, some
+// values fall on the other side of a rounding boundary (8192 x 4096 in fp16 differed from rows that were divided by
+// 1.2e-4 in norm, and by 3.3e-6 with the correction). An infinite scale keeps the
 // uncorrected product (0, or NaN for the infinity itself).
 __device__ __forceinline__ uint2 to_e4m3(const float (&f)[kChunk], float scale) {
   const float inv = __frcp_rn(scale);
@@ -317,8 +318,8 @@ __global__ void __launch_bounds__(512, VPT == 1 && NR > 0 && sizeof(T) == 2 ? 4 
 // With xhat = h * rstd and g = dy * w (dy: the sum of the ranks' gradients):
 //   dx = rstd * (g - xhat * mean(g * xhat)) + dhidden,   dw = sum over rows of dy * xhat.
 // One or two blocks an SM walk rows, as many at a time as their threads hold; a thread keeps the dw sums of its own
-// columns in registers over all its rows, the block's rows join them in shared memory, and the block writes them once to
-// the workspace ([blocks][cols]), which k_norm_dweight adds in block order: no atomics, so repeated calls give the
+// columns in registers over all its rows, the block's rows join them in shared memory, and the block writes them once
+// to the workspace ([blocks][cols]), which k_norm_dweight adds in block order: no atomics, so repeated calls give the
 // same bits.
 
 struct NormBwdArgs {
@@ -340,7 +341,7 @@ struct NormBwdArgs {
 // two blocks of 512 threads, with two chunks a thread keeping the dw sums in shared memory (WIDE; each thread its own
 // columns') and reading dhidden only when it is added; wider ones 1024 threads a row of two or four chunks, the
 // latter reading hidden again (from L2) instead of keeping it. fp32 rows: 512 threads, WIDE from four chunks on.
-// Measured: 8192 x 4096 fp16 on eight ranks 117 us (6.3 TB/s), 16384 x 1024 on two 38 us, 777 x 8192 on two 22 us,
+// Measured: 8192 x 4096 fp16 on eight ranks 119 us (6.2 TB/s), 16384 x 1024 on two 38 us, 777 x 8192 on two 24 us,
 // 4096 x 16384 bf16 on one 113 us, 2048 x 32768 141 us; HBM bounds the first, latency between a row's phases the rest.
 template <typename T, int VPT, int THREADS>
 struct BwdShape {
