@@ -123,7 +123,8 @@ __device__ __forceinline__ void walk_load(const GroupedParams& P, Walk& w, int b
 
 // The tile of unit u (ascending from call to call), or false past the last one. The whole warp calls it.
 template <bool GRAD>
-__device__ __forceinline__ bool walk_find(const GroupedParams& P, Walk& w, int u, Tile& t, int tm, int tn) {
+__device__ __forceinline__ bool walk_find(const GroupedParams& P, Walk& w, int u, Tile& t, int tm, int tn,
+                                          int group_mt = GROUP_MT) {
   for (;;) {
     const int last = __shfl_sync(0xffffffffu, w.upto, 31);
     if (u < last) break;
@@ -138,11 +139,11 @@ __device__ __forceinline__ bool walk_find(const GroupedParams& P, Walk& w, int u
   t.r1 = __shfl_sync(0xffffffffu, w.r1, f);
   const int local = u - (__shfl_sync(0xffffffffu, w.upto, f) - __shfl_sync(0xffffffffu, w.tiles, f));
   const int mts = ((GRAD ? P.k : t.r1 - t.r0) + tm - 1) / tm, nts = (P.n + tn - 1) / tn;
-  const int group = local / (GROUP_MT * nts);
-  const int gm = min(GROUP_MT, mts - group * GROUP_MT);
-  const int in_g = local - group * GROUP_MT * nts;
+  const int group = local / (group_mt * nts);
+  const int gm = min(group_mt, mts - group * group_mt);
+  const int in_g = local - group * group_mt * nts;
   const int nt = in_g / gm;
-  t.m0 = (group * GROUP_MT + in_g - nt * gm) * tm;
+  t.m0 = (group * group_mt + in_g - nt * gm) * tm;
   t.n0 = nt * tn;
   return true;
 }
@@ -191,6 +192,16 @@ __device__ __forceinline__ bool wait_bar_warp(uint32_t bar, uint32_t parity, vol
   bool ok = true;
   if ((threadIdx.x & 31) == 0) ok = wait_bar(bar, parity, abort_flag);
   return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+
+// A producer warp's last step: every stage that it filled is read and handed back, so no commit's arrival is still on
+// its way when the CTA gives up its shared memory. `empty0`: the barrier of stage 0; `parity`: bit s is the phase of
+// the stage's last copies, which its hand-back completes. (After a failure a stage may never be multiplied. By the
+// time that the first wait for one has run out, all that was issued has long arrived.)
+__device__ __forceinline__ void await_hand_back(uint32_t empty0, int stages, uint32_t issued, uint32_t parity,
+                                                volatile int* never) {
+  for (int s = 0; s < stages; ++s)
+    if (((issued >> s) & 1u) && !wait_bar_warp(empty0 + 8u * s, (parity >> s) & 1u, never)) break;
 }
 
 // A descriptor of operand tiles in 128-byte swizzled rows (tcgen05 matrix descriptor: start address >> 4,
@@ -673,20 +684,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
 // ------------------------------------------------------ block-scaled kernel
 //
-// k_grouped_scaled (e4m3, many rows): one 256 x 256 tile per cluster of two CTAs and step, as k_grouped_pair, but
-// each CTA issues its own MMAs (M = 128, N = 256) on its own rows. The block's product has to be added up and its
-// TMEM buffer handed back every 128 k, and with one MMA over both CTAs that hand-over crossed CTAs both ways
-// (commit to the other's epilogue, arrivals back), some thousand cycles of every two blocks' 1024: 8192^3 took
-// 424 us, and 388 us here (2.83 PFLOP/s from a graph; 440 to 460 in a long loop, at the power cap's 1.7 GHz), where
-// it stays within the CTA. Without the sums (a TMEM buffer handed back unread) the loop took 322 us beside 378
-// with, so what bounds it is the power and the epilogue's loop: 8 TMEM loads, 64 packed multiply-adds and the
-// hand-over a block.
-// The two CTAs still share what they read: each loads 128 of the tile's columns of rhs and multicasts them to both,
-// so a CTA reads 32 KB a block as in the pair.
-//   warp 0        TMA producer: lhs rows to itself, its half of the rhs columns to both CTAs; 4 stages of 48 KB.
+// k_grouped_scaled (e4m3, many rows): one 128 x 256 tile per CTA and step (M = 128, N = 256), no CTA depending on
+// another. The block's product has to be added up and its TMEM buffer handed back every 128 k, and with one MMA over
+// two CTAs that hand-over crosses CTAs both ways (commit to the other's epilogue, arrivals back), some thousand cycles
+// of every two blocks' 1024. The price is that a CTA reads all 256 of its columns of rhs itself, 48 KB a block (L2 gives
+// them: 8192^3 takes 382 to 385 us, 2.87 PFLOP/s, from a graph, where two CTAs that each loaded half of the columns for
+// both took 388). Tiles of 128 rows also cost an expert's end half of what 256 would: 16384 rows over 32 uneven experts,
+// k 4096, n 2048: 131 to 142 us.
+//   warp 0        TMA producer: 128 rows of lhs and 256 columns of rhs; 4 stages of 48 KB.
 //   warp 1        issues the MMAs and owns TMEM (two buffers of 256 columns).
 //   warps 4..11   two per TMEM lane quarter, 128 columns each: sums of the scaled blocks in registers, then stores.
 
+constexpr int S_TILE_M = 128, S_GROUP_MT = 16;  // (as many rows to a raster group as k_grouped_pair's)
 constexpr int S_STAGE = A_BYTES + 2 * B_BYTES, S_STAGES = 4;
 constexpr int S_STRIP_OFF = S_STAGES * S_STAGE;
 constexpr int S_BAR_OFF = S_STRIP_OFF + EPI_WARPS * STRIP;
@@ -694,25 +703,7 @@ constexpr int S_NUM_BARS = 2 * S_STAGES + 5;  // full, empty per stage; accumula
 constexpr int S_SMEM_BYTES = S_BAR_OFF + 8 * S_NUM_BARS + 16 + 1024;
 static_assert(S_SMEM_BYTES <= 232448, "shared memory over the per-CTA limit");
 
-// A tile copy to the same place in every CTA of `mask`, counted on each one's own mbarrier at the same offset.
-__device__ __forceinline__ void tma_load_3d_both(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
-                                                 int c2, uint16_t mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, "
-      "{%3, %4, %5}], [%2], %6;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "h"(mask)
-      : "memory");
-}
-// Arrive on the mbarrier at offset `bar` of every CTA in `mask` once this thread's MMAs issued so far are done.
-__device__ __forceinline__ void umma_commit_both(uint32_t bar, uint16_t mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"(mask)
-      : "memory");
-}
-
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
-    k_grouped_scaled(const __grid_constant__ GroupedParams P) {
+__global__ void __launch_bounds__(THREADS, 1) k_grouped_scaled(const __grid_constant__ GroupedParams P) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -726,14 +717,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S_BAR_OFF + 8 * S_NUM_BARS + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = static_cast<int>(cluster_ctarank());
-  const int cluster_id = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
-  constexpr uint16_t kBoth = 0x3;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S_STAGES; ++s) {
       mbar_init(full_bar(s), 1);
-      mbar_init(empty_bar(s), 2);  // both CTAs' MMAs have read the stage: each holds what the other's producer sends
+      mbar_init(empty_bar(s), 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
@@ -741,11 +729,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");  // (for the copies and commits)
   }
   if (warp == 1) tmem_alloc<false>(smem_u32(tmem_slot), TMEM_COLS);
   tc_fence_before();
-  cluster_sync();  // the peer's barriers exist before copies and commits reach them
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
@@ -765,14 +753,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       // ------------------------------------------------------ TMA producer
       const bool leader = elect_one();
       Walk w;
-      walk_load<false>(P, w, 0, 0, TILE_M, TILE_N);
+      walk_load<false>(P, w, 0, 0, S_TILE_M, TILE_N);
       Tile t;
       int stage = 0;
       uint32_t phase = 0, issued = 0, parity = 0;
       bool ok = true;
-      for (int u = cluster_id; ok && walk_find<false>(P, w, u, t, TILE_M, TILE_N); u += nclusters) {
+      for (int u = blockIdx.x; ok && walk_find<false>(P, w, u, t, S_TILE_M, TILE_N, S_GROUP_MT); u += gridDim.x) {
         const CUtensorMap *ma = &P.a[t.p], *mb = &P.b[t.p];
-        const int arow = t.r0 + t.m0 + 128 * rank, bcol = t.n0 + 128 * rank;
+        const int arow = t.r0 + t.m0;
         for (int kb = 0; kb < P.kblocks; ++kb) {
           if (!wait_bar_warp(empty_bar(stage), phase ^ 1u, abort_flag)) {
             if (leader) fail();
@@ -780,12 +768,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             break;
           }
           if (leader) {
-            const uint32_t sa = sbase + stage * S_STAGE, sb = sa + A_BYTES + rank * B_BYTES;
+            const uint32_t sa = sbase + stage * S_STAGE, sb = sa + A_BYTES;
             const int k0 = kb * 128;
-            mbar_expect_tx(full_bar(stage), S_STAGE);  // its rows, and both halves of the columns
+            mbar_expect_tx(full_bar(stage), S_STAGE);
             tma_load_3d(sa, ma, full_bar(stage), k0, arow, 0);
-            if (P.form == GRP_NK) tma_load_3d_both(sb, mb, full_bar(stage), k0, bcol, t.e, kBoth);
-            else tma_load_3d_both(sb, mb, full_bar(stage), bcol, k0, t.e, kBoth);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int n0 = t.n0 + 128 * j;
+              if (P.form == GRP_NK) tma_load_3d(sb + j * B_BYTES, mb, full_bar(stage), k0, n0, t.e);
+              else tma_load_3d(sb + j * B_BYTES, mb, full_bar(stage), n0, k0, t.e);
+            }
           }
           __syncwarp();
           issued |= 1u << stage;
@@ -796,17 +788,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (!ok)  // let copies in flight land
         for (int s = 0; s < S_STAGES; ++s)
           if ((issued >> s) & 1u) wait_bar_warp(full_bar(s), (parity >> s) & 1u, never);
+      await_hand_back(empty_bar(0), S_STAGES, issued, parity, never);
     } else if (warp == 1) {
       // ------------------------------------------------------- MMA issuer
       const bool leader = elect_one();
       const uint32_t idesc = P.idesc, bstep = P.bstep;
       const uint64_t ad0 = tile_desc(sbase, 1), bd0 = tile_desc(sbase + A_BYTES, P.blead);
       // (every tile has the same blocks: this warp needs no more than the tiles' number)
-      const int total = walk_total<false>(P, TILE_M, TILE_N);
+      const int total = walk_total<false>(P, S_TILE_M, TILE_N);
       int stage = 0, acc = 0;
       uint32_t phase = 0, accph = 0;
       bool ok = true, any_mma = false;
-      for (int u = cluster_id; ok && u < total; u += nclusters) {
+      for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
         for (int kb = 0; kb < P.kblocks; ++kb) {
           if (!wait_bar_warp(tempty_bar(acc), accph ^ 1u, abort_flag) ||
               !wait_bar_warp(full_bar(stage), phase, abort_flag)) {
@@ -821,7 +814,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             for (int k = 0; k < 4; ++k)
               mma_one<true>(tmem_base + acc * TILE_N, ad0 + off + 2 * k, bd0 + off + bstep * k, idesc, k != 0);
             umma_commit(tfull_bar(acc));
-            umma_commit_both(empty_bar(stage), kBoth);
+            umma_commit(empty_bar(stage));
           }
           __syncwarp();
           any_mma = true;
@@ -844,17 +837,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const uint32_t strip = sbase + S_STRIP_OFF + (warp - FIRST_EPI_WARP) * STRIP;
     const uint32_t tacc = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128;
     Walk w;
-    walk_load<false>(P, w, 0, 0, TILE_M, TILE_N);
+    walk_load<false>(P, w, 0, 0, S_TILE_M, TILE_N);
     Tile t;
     int acc = 0;
     uint32_t accph = 0;
     bool ok = true;
-    for (int u = cluster_id; ok && walk_find<false>(P, w, u, t, TILE_M, TILE_N); u += nclusters) {
+    for (int u = blockIdx.x; ok && walk_find<false>(P, w, u, t, S_TILE_M, TILE_N, S_GROUP_MT); u += gridDim.x) {
       uint64_t sum[64];  // pairs of fp32 sums of neighbouring columns
 #pragma unroll
       for (int j = 0; j < 64; ++j) sum[j] = 0ull;
       // this lane's row of lhs scales, and the columns' block of rhs scales (out of range: any valid ones)
-      const int my_row = t.r0 + t.m0 + 128 * rank + quarter * 32 + lane;
+      const int my_row = t.r0 + t.m0 + quarter * 32 + lane;
       const float* sa = P.sa[t.p] + static_cast<int64_t>(min(my_row, P.rows - 1)) * P.kscales;
       const float* sb = P.sb[t.p] + static_cast<int64_t>(t.e) * P.kscales * P.nscales +
                         static_cast<int64_t>(min(t.n0 / 128 + half, P.nscales - 1)) * P.sb_n;
@@ -900,7 +893,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       w.upto = unpark(strip, 4); t.p = unpark(strip, 5); t.r0 = unpark(strip, 6); t.r1 = unpark(strip, 7);
       t.m0 = unpark(strip, 8); t.n0 = unpark(strip, 9); u = unpark(strip, 10);
       __syncwarp();  // (the strip is written again below)
-      const int row = t.m0 + 128 * rank + quarter * 32;  // this warp's first one
+      const int row = t.m0 + quarter * 32;  // this warp's first one
       const int rows = min(32, t.r1 - t.r0 - row);       // (may be negative: nothing to store)
       const int esize = P.out_dtype == COCO_F32 ? 4 : 2;
       const int64_t pitch = static_cast<int64_t>(P.n) * esize;
@@ -938,7 +931,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // no CTA leaves while its peer's copies or commits may still reach it
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
@@ -1318,7 +1310,7 @@ uint32_t instruction(int dtype, bool a_mn, bool b_mn, int m, int n) {
 
 // Which kernel, and how many CTAs share a tile's k range.
 struct Choice {
-  int rows;   // 16 or 64: k_grouped_few with that many rows a tile; 0: k_grouped_pair
+  int rows;   // 16 or 64: k_grouped_few with that many rows a tile; 0: k_grouped_pair or k_grouped_scaled
   int split;
   int64_t units;
 };
@@ -1344,8 +1336,8 @@ Choice choose(const GroupedLaunch& L, int kblocks) {
     return L.nprob * mts * ((L.n + tn - 1) / tn);
   };
   auto waves = [](int64_t n, int64_t at_once) { return (n + at_once - 1) / at_once; };
-  Choice best{0, 1, tiles(TILE_M, TILE_N)};
-  int64_t least = waves(best.units, sms / 2) * kblocks * pair_ns;
+  Choice best{0, 1, tiles(fp8 ? S_TILE_M : TILE_M, TILE_N)};
+  int64_t least = waves(best.units, fp8 ? sms : sms / 2) * kblocks * pair_ns;
   for (int rows : {16, 64}) {
     const int64_t units = tiles(rows, FEW_N);
     for (int split = 1; split <= 8 && split <= kblocks; split *= 2) {
@@ -1440,11 +1432,12 @@ cudaError_t launch_grouped(const GroupedLaunch& L, cudaStream_t s, unsigned int*
     return cudaGetLastError();
   }
   // at most one partly filled tile per expert beyond the full ones
-  const int64_t mts = grad ? static_cast<int64_t>(L.experts) * ((L.k + TILE_M - 1) / TILE_M)
-                           : static_cast<int64_t>(L.rows / TILE_M) + L.experts;
+  const int tm = fp8 ? S_TILE_M : TILE_M, ctas = fp8 ? 1 : 2;  // (a tile's CTAs)
+  const int64_t mts = grad ? static_cast<int64_t>(L.experts) * ((L.k + tm - 1) / tm)
+                           : static_cast<int64_t>(L.rows / tm) + L.experts;
   const int64_t units = L.nprob * mts * ((L.n + TILE_N - 1) / TILE_N);
-  const int pairs = sm_count() / 2;
-  const int grid = 2 * static_cast<int>(units < pairs ? units : pairs);
+  const int at_once = sm_count() / ctas;
+  const int grid = ctas * static_cast<int>(units < at_once ? units : at_once);
   void (*kernel)(const GroupedParams) = fp8 ? k_grouped_scaled : grad ? k_grouped_pair<true> : k_grouped_pair<false>;
   const int smem = fp8 ? S_SMEM_BYTES : SMEM_BYTES;
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), fp8 ? 0 : grad ? 1 : 2, smem);

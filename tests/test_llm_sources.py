@@ -1,0 +1,27 @@
+"""What the kernels' sources may not contain. The library also serves the loops with one rank per device, whose
+operands can lie in another GPU's memory, and TMA loads with cluster multicast are fit for a GPU's own memory only."""
+
+import glob
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "collective_fusedallreduce_gb300", "csrc")
+
+
+def statements():
+    """Every asm statement of the sources, its string literals joined."""
+    for path in sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.h"))):
+        with open(path) as f:
+            for m in re.finditer(r"asm(?: volatile)?\s*\(((?:\s*\"(?:[^\"\\]|\\.)*\")+)", f.read()):
+                yield os.path.basename(path), "".join(re.findall(r"\"((?:[^\"\\]|\\.)*)\"", m.group(1)))
+
+
+def test_statements_are_found():
+    text = [s for _, s in statements()]
+    assert any("cp.async.bulk.tensor.3d.shared::cluster" in s for s in text)
+    assert any("tcgen05.commit" in s and "multicast::cluster" in s for s in text)
+
+
+def test_no_bulk_copy_is_multicast():
+    for name, s in statements():
+        assert not ("cp.async.bulk" in s and "multicast" in s), (name, s)
