@@ -478,6 +478,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           else if (rank == 0) wait_bar_warp(full_bar(s), (parity >> s) & 1u, never);
         }
       }
+      // (CTA 0's MMA warp hands the stages of both CTAs back)
+      await_hand_back(empty_bar(0), STAGES, issued, parity, never);
     } else if (warp == 1) {
       // ------------------------------------------------------- MMA issuer
       if (rank == 0) {
@@ -1115,6 +1117,7 @@ __global__ void __launch_bounds__(FewCfg<SCALED, ROWS>::THREADS, 1)
     if (!ok)  // let copies in flight land
       for (int s = 0; s < STAGES_; ++s)
         if ((issued >> s) & 1u) wait_bar_warp(full_bar(s), (parity >> s) & 1u, never);
+    await_hand_back(empty_bar(0), STAGES_, issued, parity, never);
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
     const bool leader = elect_one();

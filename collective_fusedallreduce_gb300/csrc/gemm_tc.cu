@@ -348,6 +348,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<MODE, TWO_SM>::T
         for (int s = 0; s < STAGES; ++s)
           if ((issued >> s) & 1u) wait(full_bar(s), (issued_parity >> s) & 1u, never);
       }
+      // Every stage is handed back before the CTA may leave: no commit (the pair's come from CTA 0) still arrives on
+      // its barriers then. After a failure the first wait that runs out is time enough for all that was issued.
+      int dummy = 0;
+      volatile int* never = &dummy;
+      for (int s = 0; s < STAGES; ++s)
+        if (((issued >> s) & 1u) && !wait(empty_bar(s), (issued_parity >> s) & 1u, never)) break;
     }
   } else if (warp == 1) {
     // ------------------------------------------------------- MMA issuer
@@ -847,6 +853,14 @@ __global__ void __launch_bounds__(BsCfg::THREADS, 1) k_gemm_tc_bs(const __grid_c
         for (int s = 0; s < BS_A_STAGES; ++s)
           if ((issued >> s) & 1u) mbar_wait(afull(s), (issued_parity >> s) & 1u, never);
       }
+      // every buffer is handed back before the CTA may leave: no commit still arrives on its barriers then
+      int dummy = 0;
+      volatile int* never = &dummy;
+      bool back = true;
+      for (int s = 0; back && s < BS_A_STAGES; ++s)
+        if ((issued >> s) & 1u) back = mbar_wait(aempty(s), (issued_parity >> s) & 1u, never);
+      for (int b = 0; back && b < BS_B_BUFS; ++b)
+        if ((b_issued >> b) & 1u) back = mbar_wait(bempty(b), (b_parity >> b) & 1u, never);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer

@@ -25,3 +25,25 @@ def test_statements_are_found():
 def test_no_bulk_copy_is_multicast():
     for name, s in statements():
         assert not ("cp.async.bulk" in s and "multicast" in s), (name, s)
+
+
+def kernels():
+    """(file, name, text) of every __global__ function."""
+    for path in sorted(glob.glob(os.path.join(CSRC, "*.cu"))):
+        with open(path) as f:
+            parts = f.read().split("__global__")[1:]
+        for part in parts:
+            body = part[:part.index("\n}\n")]
+            yield os.path.basename(path), re.search(r"k_\w+", body).group(0), body
+
+
+def test_no_cta_leaves_before_its_stages_are_handed_back():
+    """A commit arrives on a barrier some time after it was issued: the producer waits for the last ones, or they may
+    reach shared memory that the CTA has given up (of its own, or of the other CTA of a pair)."""
+    seen = 0
+    for name, kernel, body in kernels():
+        if "umma_commit" not in body:
+            continue
+        seen += 1
+        assert "await_hand_back(empty_bar(0)" in body or re.search(r"wait\(a?empty(_bar)?\(s\), .*, never\)", body), kernel
+    assert seen >= 5
