@@ -26,7 +26,7 @@
 // (64 rows an expert: 97 us); one expert of 16384 rows 145 and 154 us.
 //   warp 0        TMA producer: k-blocks 128 bytes deep into a ring of 6 stages of 32 KB.
 //   warp 1        issues the MMAs (CTA 0 of the pair) and owns TMEM.
-//   warps 2, 3    in weight gradients: clear what a k-block holds of the next expert's rows.
+//   warps 2, 3    in weight gradients: have zeros loaded over what a k-block holds of the next expert's rows.
 //   warps 4..11   two per TMEM lane quarter, 128 columns each: conversion and stores.
 // Every mbarrier wait is bounded by %globaltimer as in the other tensor-core
 // kernels: on expiry COCO_ERR_TIMEOUT is recorded, the roles drain and return.
@@ -53,15 +53,18 @@ constexpr int THREADS = 32 * (FIRST_EPI_WARP + EPI_WARPS);
 constexpr int STRIP = 32 * 128;  // an epilogue warp's staging: 32 rows x 128 bytes
 constexpr int STRIP_OFF = STAGES * STAGE_BYTES;
 constexpr int BAR_OFF = STRIP_OFF + EPI_WARPS * STRIP;
-// full, empty and cleared per stage, accumulator full x2, empty x2, drain
+// full, empty and loaded (before zeros) per stage, accumulator full x2, empty x2, drain
 constexpr int NUM_BARS = 3 * STAGES + 5;
 constexpr int SMEM_BYTES = BAR_OFF + 8 * NUM_BARS + 16 + 1024;  // + alignment slack
 static_assert(SMEM_BYTES <= 232448, "shared memory over the per-CTA limit");
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int GROUP_MT = 8;  // rasterisation: m-tiles per group, n-major inside a group
 
+constexpr int kZeroMaps = 6;
+
 struct GroupedParams {
   CUtensorMap a[COCO_MAX_PTRS], b[COCO_MAX_PTRS];
+  CUtensorMap zero[kZeroMaps];  // weight gradients: boxes of 2^i rows of 128 bytes, unswizzled, read out of range
   void* out[COCO_MAX_PTRS];
   const float* sa[COCO_MAX_PTRS];
   const float* sb[COCO_MAX_PTRS];
@@ -236,17 +239,6 @@ __device__ __forceinline__ void add_scaled(uint64_t& sum, uint32_t lo, uint32_t 
   asm volatile("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(sum) : "l"(pack2(lo, hi)), "l"(scale));
 }
 
-// Arrivals that publish a warp's shared-memory writes to its own SM's tensor core: the writes are fenced to the
-// async proxy first (fence.proxy.async), and the only reader of a CTA's operands is that CTA's half of the pair's
-// MMA, which reads its own SM's shared memory. CTA scope is therefore enough for the remote arrival too; a release
-// at cluster scope costs some 2000 cycles per call (it made the ragged weight gradient 30 % slower).
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
-}
-
 // ---------------------------------------------------------------- epilogue
 
 // Values that a k loop does not need, kept in the warp's (then idle) staging strip across it: its 128 sums and
@@ -354,7 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const uint32_t bar0 = sbase + BAR_OFF;
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
-  auto clear_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };  // weight gradients: an expert's last block
+  auto loaded_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };  // weight gradients: an expert's last block
   auto tfull_bar = [&](int a) { return bar0 + 8u * (3 * STAGES + a); };
   auto tempty_bar = [&](int a) { return bar0 + 8u * (3 * STAGES + 2 + a); };
   const uint32_t drain_bar = bar0 + 8u * (3 * STAGES + 4);
@@ -368,11 +360,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      // CTA 0's is the pair's: its own producer's arrival, and in weight gradients two of each CTA (the producer's,
-      // or for an expert's last block those of the warps that cleared it)
-      mbar_init(full_bar(s), GRAD ? 4 : 1);
+      mbar_init(full_bar(s), 1);  // CTA 0's is the pair's
       mbar_init(empty_bar(s), 1);
-      mbar_init(clear_bar(s), 1);
+      mbar_init(loaded_bar(s), 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
@@ -404,7 +394,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       Tile t;
       int stage = 0;
       uint32_t phase = 0;
-      uint32_t issued = 0, parity = 0, own = 0, clear_parity = 0;  // per stage; own: the copies complete clear_bar
+      uint32_t issued = 0, parity = 0, own = 0, own_parity = 0;  // per stage; own: the copies complete loaded_bar
       bool ok = true;
       for (int u = cluster_id; ok && walk_find<GRAD>(P, w, u, t, TILE_M, TILE_N); u += nclusters) {
         const CUtensorMap *ma = &P.a[t.p], *mb = &P.b[t.p];
@@ -420,32 +410,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             break;
           }
           const uint32_t sa = sbase + stage * STAGE_BYTES, sb = sa + A_BYTES;
-          const bool to_clear = ragged && kb == kblocks - 1;
+          const bool partly = ragged && kb == kblocks - 1;
           if (leader) {
             if constexpr (GRAD) {
               // both operands' rows run along the contraction: 64 rows x 64 columns a box
               const int r = t.r0 + kb * P.bk;
-              if (to_clear) {
-                mbar_expect_tx(clear_bar(stage), STAGE_BYTES);
+              if (partly) {  // (then warps 2 and 3 have the rest of its rows zeroed, counted on CTA 0's barrier)
+                mbar_expect_tx(loaded_bar(stage), STAGE_BYTES);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                  tma_load_3d(sa + j * (A_BYTES / 2), ma, clear_bar(stage), acol + 64 * j, r, 0);
-                  tma_load_3d(sb + j * (B_BYTES / 2), mb, clear_bar(stage), bcol + 64 * j, r, 0);
+                  tma_load_3d(sa + j * (A_BYTES / 2), ma, loaded_bar(stage), acol + 64 * j, r, 0);
+                  tma_load_3d(sb + j * (B_BYTES / 2), mb, loaded_bar(stage), bcol + 64 * j, r, 0);
                 }
+                if (rank == 0) mbar_expect_tx(full_bar(stage), 2 * 4 * 128 * (P.bk - (t.r1 - r)));
               } else {
                 const uint32_t fb = mapa_rank0(full_bar(stage));
-                if (rank == 0) {
-                  mbar_expect_tx(full_bar(stage), 2 * STAGE_BYTES);
-                  mbar_arrive_relaxed(full_bar(stage));
-                }
+                if (rank == 0) mbar_expect_tx(full_bar(stage), 2 * STAGE_BYTES);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                   tma_load_3d_pair(sa + j * (A_BYTES / 2), ma, fb, acol + 64 * j, r, 0);
                   tma_load_3d_pair(sb + j * (B_BYTES / 2), mb, fb, bcol + 64 * j, r, 0);
-                }
-                if (rank != 0) {  // (relaxed: these publish nothing of this thread's)
-                  mbar_arrive_cluster_relaxed(fb);
-                  mbar_arrive_cluster_relaxed(fb);
                 }
               }
             } else {
@@ -466,16 +450,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           const uint32_t bit = 1u << stage;
           issued |= bit;
           parity = (parity & ~bit) | (phase << stage);
-          own = to_clear ? own | bit : own & ~bit;
-          if (to_clear) clear_parity ^= bit;  // (starts at 0: after the first use, its phase 0 is the one in flight)
+          own = partly ? own | bit : own & ~bit;
+          if (partly) own_parity ^= bit;  // (starts at 0: after the first use, its phase 0 is the one in flight)
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }
       if (!ok) {  // let copies in flight land (CTA 0's barriers count both CTAs')
         for (int s = 0; s < STAGES; ++s) {
           if (!((issued >> s) & 1u)) continue;
-          if ((own >> s) & 1u) wait_bar_warp(clear_bar(s), ((clear_parity >> s) & 1u) ^ 1u, never);
-          else if (rank == 0) wait_bar_warp(full_bar(s), (parity >> s) & 1u, never);
+          if ((own >> s) & 1u) wait_bar_warp(loaded_bar(s), ((own_parity >> s) & 1u) ^ 1u, never);
+          if (rank == 0) wait_bar_warp(full_bar(s), (parity >> s) & 1u, never);
         }
       }
       // (CTA 0's MMA warp hands the stages of both CTAs back)
@@ -540,14 +524,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
       }
     } else if (GRAD && warp >= 2) {
-      // ------------------------------------- clearing of the next expert's rows
-      // An expert's last k-block holds rows past its end. Both operands' are cleared (one alone would leave
-      // 0 * infinity), in each CTA's own shared memory, before the pair's MMA may read the stage.
+      // --------------------------------------- zeros over the next expert's rows
+      // An expert's last k-block holds rows past its end. Zeros go over them in both operands (in one alone they would
+      // leave 0 * infinity). They come by copies like any others, from rows out of range: counted on CTA 0's barrier,
+      // they need no ordering of this CTA's own writes before the pair's MMA. Clearing with stores and an arrival that
+      // releases them to CTA 0 (cluster scope) took 232 us where this takes 206 (16384 rows, 32 uneven experts, k 4096,
+      // n 2048). Warp 2 has A's two boxes of rows of 128 bytes done, warp 3 B's.
+      const bool leader = elect_one();
       Walk w;
       walk_load<GRAD>(P, w, 0, 0, TILE_M, TILE_N);
       Tile t;
       int stage = 0;
-      uint32_t clear_phase = 0;  // per stage: parity of its next use
+      uint32_t loaded_phase = 0;  // per stage: parity of its next use
       bool ok = true;
       for (int u = cluster_id; ok && walk_find<GRAD>(P, w, u, t, TILE_M, TILE_N); u += nclusters) {
         const int rows = t.r1 - t.r0, kblocks = (rows + P.bk - 1) / P.bk;
@@ -555,22 +543,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         stage = (stage + kblocks) % STAGES;
         const int valid = rows % P.bk;
         if (valid == 0) continue;
-        if (!wait_bar_warp(clear_bar(last), (clear_phase >> last) & 1u, abort_flag)) {
-          if (lane == 0) fail();
+        if (!wait_bar_warp(loaded_bar(last), (loaded_phase >> last) & 1u, abort_flag)) {
+          if (leader) fail();
           ok = false;
           break;
         }
-        clear_phase ^= 1u << last;
-        const uint32_t base = sbase + last * STAGE_BYTES;
-        // rows of 128 bytes, 64 to a box (the swizzle stays within a row): A's two boxes by one warp, B's by the other
-        for (int box = 0; box < 2; ++box)
-          for (int b = valid * 128 + lane * 16; b < 64 * 128; b += 32 * 16)
-            st_shared_v4(base + (warp - 2) * A_BYTES + box * (A_BYTES / 2) + b, 0u, 0u, 0u, 0u);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (rank == 0) mbar_arrive(full_bar(last));
-          else mbar_arrive_cluster(mapa_rank0(full_bar(last)));
+        loaded_phase ^= 1u << last;
+        if (leader) {
+          const uint32_t fb = mapa_rank0(full_bar(last));
+          uint32_t to = sbase + last * STAGE_BYTES + (warp - 2) * A_BYTES + valid * 128;
+#pragma unroll
+          for (int i = 0; i < kZeroMaps; ++i)  // (64 - valid rows: a box for every binary digit)
+            if (((64 - valid) >> i) & 1) {
+              tma_load_3d_pair(to, &P.zero[i], fb, 0, P.rows, 0);
+              tma_load_3d_pair(to + A_BYTES / 2, &P.zero[i], fb, 0, P.rows, 0);
+              to += 128u << i;
+            }
         }
         __syncwarp();
       }
@@ -1271,8 +1259,9 @@ __global__ void __launch_bounds__(FewCfg<SCALED, ROWS>::THREADS, 1)
 
 // ------------------------------------------------------------------- host
 
-// A dense [d2][d1][d0] array of 1- or 2-byte elements in boxes of box0 x box1, 128-byte swizzle, zeros outside.
-bool encode(CUtensorMap* map, const void* ptr, int dtype, int64_t d0, int64_t d1, int64_t d2, int box0, int box1) {
+// A dense [d2][d1][d0] array of 1- or 2-byte elements in boxes of box0 x box1, zeros outside.
+bool encode(CUtensorMap* map, const void* ptr, int dtype, int64_t d0, int64_t d1, int64_t d2, int box0, int box1,
+            CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   const int es = dtype_size(dtype);
@@ -1284,7 +1273,7 @@ bool encode(CUtensorMap* map, const void* ptr, int dtype, int64_t d0, int64_t d1
                                  : dtype == COCO_F16  ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   return enc(map, dt, 3, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1426,6 +1415,9 @@ cudaError_t launch_grouped(const GroupedLaunch& L, cudaStream_t s, unsigned int*
                                : encode(&P.b[p], L.rhs[p], L.in_dtype, L.n, L.k, L.experts, bk, bk));
     if (!good) return cudaErrorNotSupported;
   }
+  for (int i = 0; grad && i < kZeroMaps; ++i)
+    if (!encode(&P.zero[i], L.lhs[0], L.in_dtype, L.k, L.rows, 1, 64, 1 << i, CU_TENSOR_MAP_SWIZZLE_NONE))
+      return cudaErrorNotSupported;
   if (few.rows) {
     cudaError_t e;
     if (few.rows == 16) e = fp8 ? launch_few<true, 16>(P, few, 3, s) : launch_few<false, 16>(P, few, 4, s);

@@ -47,3 +47,8 @@ def test_no_cta_leaves_before_its_stages_are_handed_back():
         seen += 1
         assert "await_hand_back(empty_bar(0)" in body or re.search(r"wait\(a?empty(_bar)?\(s\), .*, never\)", body), kernel
     assert seen >= 5
+
+
+def test_releases_to_another_cta_have_its_scope():
+    for name, s in statements():
+        assert not ("mbarrier.arrive.release.cta" in s and "shared::cluster" in s), (name, s)
