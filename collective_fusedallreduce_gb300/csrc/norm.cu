@@ -668,7 +668,7 @@ cudaError_t bwd_go(const NormBwdArgs& a, int groups, int* parts, cudaStream_t s)
   const int64_t want = (a.rows + rpb - 1) / rpb;
   const dim3 grid(static_cast<unsigned>(want < most ? want : most), groups);
   const int smem = S::WIDE ? a.nchunks * kChunk * 4 : 0;
-  if (smem > 48 * 1024) {
+  if (S::WIDE) {  // (whatever the row's size: with the kernel's own arrays, rows just under 48 KB pass what needs no leave)
     const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&k_rmsnorm_backward<T, NR, VPT, THREADS>),
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
