@@ -19,6 +19,7 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "internal.h"
@@ -668,10 +669,20 @@ cudaError_t bwd_go(const NormBwdArgs& a, int groups, int* parts, cudaStream_t s)
   const int64_t want = (a.rows + rpb - 1) / rpb;
   const dim3 grid(static_cast<unsigned>(want < most ? want : most), groups);
   const int smem = S::WIDE ? a.nchunks * kChunk * 4 : 0;
-  if (S::WIDE) {  // (whatever the row's size: with the kernel's own arrays, rows just under 48 KB pass what needs no leave)
-    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&k_rmsnorm_backward<T, NR, VPT, THREADS>),
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if constexpr (S::WIDE) {
+    // The leave for dynamic shared memory is the process's: once per device, for the widest row that comes here, so
+    // that no call can take another's. (Any size needs it: with the kernel's own arrays, rows just under 48 KB pass
+    // what needs none.)
+    static std::atomic<bool> leave[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !leave[dev].load(std::memory_order_acquire)) {
+      e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&k_rmsnorm_backward<T, NR, VPT, THREADS>),
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, VPT * THREADS * kChunk * 4);
+      if (e != cudaSuccess) return e;
+      if (dev >= 0 && dev < 64) leave[dev].store(true, std::memory_order_release);
+    }
   }
   *parts = static_cast<int>(grid.x) * groups;
   k_rmsnorm_backward<T, NR, VPT, THREADS><<<grid, THREADS, smem, s>>>(a);

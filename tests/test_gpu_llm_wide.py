@@ -7,6 +7,7 @@ Tolerances as in test_gpu_llm_norm: (ranks + 160) 2^-24 of the terms' magnitudes
 import os
 import subprocess
 import sys
+import threading
 
 import pytest
 import torch
@@ -60,6 +61,32 @@ def test_first_call_of_a_process(cols):
            f"import test_gpu_llm_wide as t; t.first_calls({cols})"
     p = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert p.returncode == 0, p.stdout + p.stderr
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_calls_of_two_threads_do_not_take_each_others_shared_memory(dtype):
+    failed = []
+
+    def work(cols):
+        try:
+            torch.cuda.set_device(DEV)
+            s = torch.cuda.Stream()
+            args, check = calls[cols]
+            for _ in range(2000):
+                coco.coco_allreduce_rmsnorm_backward(*args, stream=s)
+            s.synchronize()
+            check()
+        except Exception as e:  # noqa: BLE001 (reported by the main thread)
+            failed.append((cols, e))
+
+    calls = {cols: gradient(2, 1, cols, dtype) for cols in (32768, 16400)}
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(cols,)) for cols in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
