@@ -38,6 +38,37 @@ bool any_overlap(const std::vector<Range>& a, const std::vector<Range>& b) {
   return false;
 }
 
+// Memory of one group's rows. Groups run at the same time, and what orders a write after a read (an output in an
+// input's place) or makes equal writes harmless (one buffer for several replicas) holds within a group only.
+struct GroupRange {
+  Range r;
+  int group;
+  bool same_place(const GroupRange& o) const { return group == o.group && r.lo == o.r.lo && r.hi == o.r.hi; }
+};
+
+void group_ranges(const TInfo& a, std::vector<GroupRange>* v, bool first_only = false) {
+  if (a.bytes == 0) return;
+  for (int g = 0; g < a.ngroups; ++g)
+    for (int r = 0; r < (first_only ? 1 : a.nranks); ++r) v->push_back({range_of(a.ptr(g, r), a.bytes), g});
+}
+
+// check_alias for outputs that belong to groups.
+coco_status check_group_alias(const std::vector<GroupRange>& outs, const std::vector<GroupRange>& ins, bool exact_ok) {
+  for (size_t i = 0; i < outs.size(); ++i) {
+    for (size_t j = i + 1; j < outs.size(); ++j)
+      if (overlap(outs[i].r, outs[j].r) && !outs[i].same_place(outs[j])) return COCO_ERR_ALIAS;
+    for (const GroupRange& in : ins)
+      if (overlap(outs[i].r, in.r) && !(exact_ok && outs[i].same_place(in))) return COCO_ERR_ALIAS;
+  }
+  return COCO_OK;
+}
+
+std::vector<Range> plain(const std::vector<GroupRange>& v) {
+  std::vector<Range> out;
+  for (const GroupRange& x : v) out.push_back(x.r);
+  return out;
+}
+
 // No C++ exception leaves an entry point: running out of host memory is reported as the CUDA error of that name.
 template <typename F>
 coco_status guarded(F&& f) {
@@ -98,18 +129,21 @@ static coco_status allreduce_rmsnorm_impl(const coco_tensor* partials, const coc
   if ((st = check_ptr(weight, 16)) != COCO_OK) return st;
   if (rstd && (st = check_ptr(rstd, 4)) != COCO_OK) return st;
 
-  std::vector<Range> ins, hid_r, nrm_r, aux_r;
-  tensor_ranges(in, &ins);
-  if (residual) tensor_ranges(res, &ins, true);
-  if (hidden) tensor_ranges(hid, &hid_r);
-  tensor_ranges(nrm, &nrm_r);
+  std::vector<GroupRange> ins_g, hid_g, nrm_g, aux_g;
+  group_ranges(in, &ins_g);
+  if (residual) group_ranges(res, &ins_g, true);
+  if (hidden) group_ranges(hid, &hid_g);
+  group_ranges(nrm, &nrm_g);
+  std::vector<Range> aux_r;
   if (fp8 && (st = check_scales(scales, nrm, rows * blocks128(cols) * 4, false, &aux_r)) != COCO_OK) return st;
-  if ((st = check_alias(aux_r, ins, false)) != COCO_OK) return st;  // (equal scale pointers: written alike)
+  for (size_t i = 0; i < aux_r.size(); ++i) aux_g.push_back({aux_r[i], static_cast<int>(i) / nrm.nranks});
+  if ((st = check_group_alias(aux_g, ins_g, false)) != COCO_OK) return st;
   std::vector<Range> rstd_r;
   if (rstd) rstd_r.push_back(range_of(rstd, rows * in.ngroups * 4));
   // an element-wise output may take an input's place exactly; e4m3 values are smaller than what they come from
-  if ((st = check_alias(hid_r, ins, true)) != COCO_OK) return st;
-  if ((st = check_alias(nrm_r, ins, !fp8)) != COCO_OK) return st;
+  if ((st = check_group_alias(hid_g, ins_g, true)) != COCO_OK) return st;
+  if ((st = check_group_alias(nrm_g, ins_g, !fp8)) != COCO_OK) return st;
+  const std::vector<Range> ins = plain(ins_g), hid_r = plain(hid_g), nrm_r = plain(nrm_g);
   const std::vector<Range> w{range_of(weight, cols * dtype_size(in.dtype))};
   if (any_overlap(hid_r, nrm_r) || any_overlap(hid_r, aux_r) || any_overlap(nrm_r, aux_r) ||
       any_overlap(rstd_r, hid_r) || any_overlap(rstd_r, nrm_r) || any_overlap(rstd_r, aux_r) ||
@@ -208,12 +242,13 @@ static coco_status allreduce_rmsnorm_backward_impl(const coco_tensor* dnormed, c
   const size_t need = coco_allreduce_rmsnorm_backward_bytes(rows * in.ngroups, cols);
   if (workspace_bytes < need) return COCO_ERR_SHAPE;
 
-  std::vector<Range> ins, outs;
-  tensor_ranges(in, &ins);
-  tensor_ranges(hid, &ins, true);
-  if (dhidden) tensor_ranges(dh, &ins, true);
-  tensor_ranges(o, &outs);
-  if ((st = check_alias(outs, ins, true)) != COCO_OK) return st;
+  std::vector<GroupRange> ins_g, outs_g;
+  group_ranges(in, &ins_g);
+  group_ranges(hid, &ins_g, true);
+  if (dhidden) group_ranges(dh, &ins_g, true);
+  group_ranges(o, &outs_g);
+  if ((st = check_group_alias(outs_g, ins_g, true)) != COCO_OK) return st;
+  const std::vector<Range> ins = plain(ins_g), outs = plain(outs_g);
   const std::vector<Range> small_in{range_of(weight, cols * dtype_size(in.dtype)),
                                     range_of(rstd, rows * in.ngroups * 4)};
   const std::vector<Range> dw{range_of(dweight, cols * 4)};

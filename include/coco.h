@@ -460,7 +460,8 @@ coco_status coco_loop_profitable(double orig_comp, double orig_comm, double ring
  *             replica at the same place.
  *   rstd      device pointer to [ngroups, rows] fp32: receives 1 / sqrt(mean(h^2) + eps), or NULL.
  *
- * hidden, and normed of type T, may take an input's place exactly. Other overlaps are COCO_ERR_ALIAS.
+ * hidden, and normed of type T, may take the place of an input of their own group exactly, and replicas (and scales) of
+ * one group may be one buffer. Other overlaps, those across groups among them, are COCO_ERR_ALIAS.
  */
 coco_status coco_allreduce_rmsnorm(const coco_tensor* partials, const coco_tensor* residual, const void* weight,
                                    float eps, const coco_tensor* hidden, const coco_tensor* normed,
@@ -479,7 +480,8 @@ coco_status coco_allreduce_rmsnorm(const coco_tensor* partials, const coco_tenso
  * A norm stored in 8 bits passes its gradient through unchanged.
  *   dnormed   LOCAL, T.            dhidden  REPLICATED, T (the residual stream's gradient), or NULL.
  *   hidden    REPLICATED, T, as the forward wrote it.   rstd  [ngroups, rows] fp32, as the forward wrote it.
- *   dx        REPLICATED, T; may take the place of dnormed_r, dhidden or hidden exactly.
+ *   dx        REPLICATED, T; may take the place of dnormed_r, dhidden or hidden of its own group exactly, and one
+ *             buffer may stand for a group's replicas. Other overlaps are COCO_ERR_ALIAS.
  *   dweight   device pointer to one row of fp32.
  *   workspace device memory of at least coco_allreduce_rmsnorm_backward_bytes(ngroups * rows, cols) bytes
  *             (fewer: COCO_ERR_SHAPE), 16-byte aligned; its contents before and after do not matter.
