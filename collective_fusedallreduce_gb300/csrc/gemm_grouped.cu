@@ -12,7 +12,8 @@
 // Work units are numbered expert by expert, and every warp finds its unit by
 // itself: 32 lanes read 32 experts' offsets, a prefix sum over their tile counts
 // and a ballot give the expert, so neither a table nor a launch per expert is
-// needed and empty experts cost one lane of one read.
+// needed and empty experts cost one lane of one read. Offsets that descend can number any amount of units: counts stop
+// at what ascending ones can have, in every warp alike, so they neither pass 32 bits nor keep the kernel longer.
 //
 // k_grouped_pair (16-bit operands): CTA pairs, persistent, one tile of up to
 // 256 x 256 per pair and step (tcgen05 cta_group::2: M = 256, N up to 256; each
@@ -80,6 +81,7 @@ struct GroupedParams {
   uint32_t bstep;      // the rhs tile's descriptor advance per MMA, in 16-byte units
   uint32_t blead;      // its leading byte offset >> 4
   int32_t split;       // few-row kernel: CTAs of a cluster that share a tile's k range
+  int32_t units;       // as many as ascending offsets can have (less than 2^30); later ones are left out
 };
 static_assert(sizeof(GroupedParams) <= 32000, "kernel parameter block too large");
 
@@ -119,9 +121,9 @@ __device__ __forceinline__ void walk_load(const GroupedParams& P, Walk& w, int b
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int v = __shfl_up_sync(0xffffffffu, s, d);
-    if (lane >= d) s += v;
+    if (lane >= d) s = min(s + v, P.units);
   }
-  w.upto = before + s;
+  w.upto = min(before + s, P.units);
 }
 
 // The tile of unit u (ascending from call to call), or false past the last one. The whole warp calls it.
@@ -1031,9 +1033,6 @@ __global__ void __launch_bounds__(FewCfg<SCALED, ROWS>::THREADS, 1)
   const int split = P.split;
   const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int cluster_id = blockIdx.x / split, nclusters = gridDim.x / split;
-  // A cluster that shares a tile's k range has one tile at most (the launch has as many clusters as there can be
-  // tiles); offsets that descend could number more, which are left out rather than mixed into the first one's sums.
-  const int u_end = split > 1 ? nclusters : INT32_MAX;
   // this CTA's part of every tile's k range
   const int kb0 = static_cast<int>(static_cast<int64_t>(P.kblocks) * rank / split);
   const int kb1 = static_cast<int>(static_cast<int64_t>(P.kblocks) * (rank + 1) / split);
@@ -1049,7 +1048,8 @@ __global__ void __launch_bounds__(FewCfg<SCALED, ROWS>::THREADS, 1)
     }
     mbar_init(drain_bar, 1);
     mbar_init(red_bar, 1);
-    if (split > 1) mbar_expect_tx(red_bar, C::RED_BYTES);  // (a cluster has at most one tile then)
+    // (a cluster has at most one tile then: the launch has one for each of P.units)
+    if (split > 1) mbar_expect_tx(red_bar, C::RED_BYTES);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -1076,7 +1076,7 @@ __global__ void __launch_bounds__(FewCfg<SCALED, ROWS>::THREADS, 1)
     int stage = 0;
     uint32_t phase = 0, issued = 0, parity = 0;
     bool ok = true;
-    for (int u = cluster_id; ok && u < u_end && walk_find<false>(P, w, u, t, ROWS, FEW_N); u += nclusters) {
+    for (int u = cluster_id; ok && walk_find<false>(P, w, u, t, ROWS, FEW_N); u += nclusters) {
       const CUtensorMap *mx = &P.a[t.p], *mw = &P.b[t.p];
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!wait_bar_warp(empty_bar(stage), phase ^ 1u, abort_flag)) {
@@ -1111,7 +1111,7 @@ __global__ void __launch_bounds__(FewCfg<SCALED, ROWS>::THREADS, 1)
     const bool leader = elect_one();
     const uint32_t idesc = P.idesc, wstep = P.bstep;
     const uint64_t wd0 = tile_desc(sbase, P.blead), xd0 = tile_desc(sbase + C::W_BYTES, 1);
-    const int total = min(walk_total<false>(P, ROWS, FEW_N), u_end);
+    const int total = walk_total<false>(P, ROWS, FEW_N);
     int stage = 0, acc = 0;
     uint32_t phase = 0, accph = 0;
     bool ok = true, any_mma = false;
@@ -1177,7 +1177,7 @@ __global__ void __launch_bounds__(FewCfg<SCALED, ROWS>::THREADS, 1)
       if (lane == 0) mbar_arrive_relaxed(tempty_bar(acc));
       if (++acc == ACCS) { acc = 0; accph ^= 1u; }
     };
-    for (int u = cluster_id; ok && u < u_end && walk_find<false>(P, w, u, t, ROWS, FEW_N); u += nclusters) {
+    for (int u = cluster_id; ok && walk_find<false>(P, w, u, t, ROWS, FEW_N); u += nclusters) {
       float sum[PW];
       uint32_t r[PW];
       if constexpr (SCALED) {
@@ -1390,8 +1390,12 @@ cudaError_t launch_grouped(const GroupedLaunch& L, cudaStream_t s, unsigned int*
   P.nscales = (L.n + 127) / 128;
   P.sb_k = L.form == GRP_NK ? 1 : P.nscales;
   P.sb_n = L.form == GRP_NK ? P.kscales : 1;
-  const Choice few = grad ? Choice{0, 1, 0} : choose(L, P.kblocks);
+  const int64_t grad_units = static_cast<int64_t>(L.nprob) * L.experts * ((L.k + TILE_M - 1) / TILE_M) *
+                             ((L.n + TILE_N - 1) / TILE_N);
+  const Choice few = grad ? Choice{0, 1, grad_units} : choose(L, P.kblocks);
+  if (few.units > (1 << 30) - 1) return cudaErrorNotSupported;  // (twice as many are counted in 32 bits)
   P.split = few.split;
+  P.units = static_cast<int32_t>(few.units);
   // few rows, and pairs: the rhs is the M side and the lhs the N side
   P.idesc = few.rows ? instruction(L.in_dtype, L.form != GRP_NK, false, FEW_N, few.rows)
             : fp8    ? instruction(L.in_dtype, false, L.form != GRP_NK, 128, TILE_N)
@@ -1426,13 +1430,9 @@ cudaError_t launch_grouped(const GroupedLaunch& L, cudaStream_t s, unsigned int*
     count_launch();
     return cudaGetLastError();
   }
-  // at most one partly filled tile per expert beyond the full ones
-  const int tm = fp8 ? S_TILE_M : TILE_M, ctas = fp8 ? 1 : 2;  // (a tile's CTAs)
-  const int64_t mts = grad ? static_cast<int64_t>(L.experts) * ((L.k + tm - 1) / tm)
-                           : static_cast<int64_t>(L.rows / tm) + L.experts;
-  const int64_t units = L.nprob * mts * ((L.n + TILE_N - 1) / TILE_N);
+  const int ctas = fp8 ? 1 : 2;  // (of a tile)
   const int at_once = sm_count() / ctas;
-  const int grid = ctas * static_cast<int>(units < at_once ? units : at_once);
+  const int grid = ctas * (P.units < at_once ? P.units : at_once);
   void (*kernel)(const GroupedParams) = fp8 ? k_grouped_scaled : grad ? k_grouped_pair<true> : k_grouped_pair<false>;
   const int smem = fp8 ? S_SMEM_BYTES : SMEM_BYTES;
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), fp8 ? 0 : grad ? 1 : 2, smem);
