@@ -15,6 +15,7 @@ there is no fallback.
 
 import ctypes
 import functools
+import operator
 import os
 import struct
 
@@ -162,7 +163,7 @@ class Dist:
     def __init__(self, layout, tensors, shape, slice_dim=-1, ngroups=1, dtype=None):
         self.layout = layout
         self.tensors = list(tensors)
-        self.shape = tuple(map(int, shape))
+        self.shape = tuple(shape) if type(shape) is torch.Size else tuple(map(int, shape))
         self.slice_dim = slice_dim
         self.ngroups = ngroups
         self.nranks = len(self.tensors) // ngroups
@@ -182,12 +183,31 @@ class Dist:
             t.ptr[i] = x.data_ptr() if x is not None else None
         return t
 
-    def packed(self):
+    def packed(self, what):
         """The coco_tensor as bytes: one struct.pack instead of a field at a time, which is most of what a call
-        on small tensors costs."""
+        on small tensors costs. The library sees addresses only: that every tensor is dense, and as large as the
+        others, is checked here (which costs as much again as taking an address, so once for one that is repeated)."""
+        ts, times = self.tensors, 1
+        if self.layout == REPLICATED:
+            first = ts[0]
+            for t in ts:
+                if t is not first:
+                    break
+            else:
+                ts, times = [first], len(ts)
+        try:
+            addresses = list(map(torch.Tensor.data_ptr, ts))
+        except TypeError:  # a None stands for a null pointer
+            addresses = [0 if x is None else x.data_ptr() for x in ts]
+            ts = [x for x in ts if x is not None]
+        if not all(map(torch.Tensor.is_contiguous, ts)) or (len(ts) > 1 and len(set(map(_nbytes, ts))) > 1):
+            raise CocoError(2, what)
         return _tensor_struct(len(self.tensors)).pack(
             self.dtype, self.layout, len(self.shape), self.slice_dim, *(self.shape + (0, 0, 0))[:3], self.nranks,
-            self.ngroups, *_addresses(self.tensors))
+            self.ngroups, *addresses * times)
+
+
+_nbytes = operator.attrgetter("nbytes")
 
 
 @functools.lru_cache(maxsize=None)
@@ -198,13 +218,6 @@ def _tensor_struct(n):
 @functools.lru_cache(maxsize=None)
 def _pointer_struct(n):
     return struct.Struct(f"={n}Q")
-
-
-def _addresses(tensors):
-    try:
-        return list(map(torch.Tensor.data_ptr, tensors))
-    except TypeError:  # a None stands for a null pointer
-        return [0 if x is None else x.data_ptr() for x in tensors]
 
 
 def local(tensors, ngroups=1):
@@ -321,8 +334,8 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _packed(d):
-    return None if d is None else d.packed()
+def _packed(d, what):
+    return None if d is None else d.packed(what)
 
 
 def _blocks(n):
@@ -360,6 +373,15 @@ def _scales(tensors, d, blocks, what):
     return _pointer_struct(len(ptrs)).pack(*ptrs)
 
 
+def _check_device(what, *tensors):
+    """Refuses host memory. Of a list of ranks' tensors or scales the first stands for all (a look at each costs as
+    much as taking its address)."""
+    for t in tensors:
+        t = t.tensors[0] if type(t) is Dist else t[0] if type(t) is list and t else t
+        if isinstance(t, torch.Tensor) and not t.is_cuda:
+            raise CocoError(7, f"{what}: a tensor that is not in device memory")
+
+
 def coco_allreduce_rmsnorm(partials, residual, weight, eps, hidden, normed, scales, rstd, stream=None):
     """h = sum of the ranks' partials + residual; normed = h / sqrt(mean(h^2) + eps) * weight over the last
     dimension. ``hidden`` (the stored h), ``residual`` and ``rstd`` ([groups, rows] fp32) may be None;
@@ -369,8 +391,10 @@ def coco_allreduce_rmsnorm(partials, residual, weight, eps, hidden, normed, scal
     rows, cols = _rows_cols(partials)
     w = _vector(weight, partials.tensors[0].dtype, cols, what)
     r = None if rstd is None else _vector(rstd, torch.float32, rows * partials.ngroups, what)
-    _check(_lib.coco_allreduce_rmsnorm(partials.packed(), _packed(residual), w, eps, _packed(hidden), normed.packed(),
-                                       _scales(scales, normed, rows * _blocks(cols), what), r, _stream(stream)), what)
+    sc = _scales(scales, normed, rows * _blocks(cols), what)
+    p, res, hid, nrm = partials.packed(what), _packed(residual, what), _packed(hidden, what), normed.packed(what)
+    _check_device(what, partials, residual, hidden, normed, weight, rstd, scales)
+    _check(_lib.coco_allreduce_rmsnorm(p, res, w, eps, hid, nrm, sc, r, _stream(stream)), what)
 
 
 def coco_allreduce_rmsnorm_backward_bytes(rows, cols):
@@ -389,8 +413,10 @@ def coco_allreduce_rmsnorm_backward(dnormed, dhidden, hidden, weight, rstd, dx, 
     dw = _vector(dweight, torch.float32, cols, what)
     if not workspace.is_contiguous():
         raise CocoError(2, what)
-    _check(_lib.coco_allreduce_rmsnorm_backward(dnormed.packed(), _packed(dhidden), hidden.packed(), w, r, dx.packed(),
-                                                dw, workspace.data_ptr(), workspace.nbytes, _stream(stream)), what)
+    dn, dh, hid, o = dnormed.packed(what), _packed(dhidden, what), hidden.packed(what), dx.packed(what)
+    _check_device(what, dnormed, dhidden, hidden, dx, weight, rstd, dweight, workspace)
+    _check(_lib.coco_allreduce_rmsnorm_backward(dn, dh, hid, w, r, o, dw, workspace.data_ptr(), workspace.nbytes,
+                                                _stream(stream)), what)
 
 
 def coco_quantize_fp8(x, block_rows, q, scales, stream=None):
@@ -403,8 +429,10 @@ def coco_quantize_fp8(x, block_rows, q, scales, stream=None):
         blocks = mats * _blocks(rows // mats if mats else 0) * _blocks(cols)
     else:
         blocks = rows * _blocks(cols)
-    _check(_lib.coco_quantize_fp8(x.packed(), block_rows, q.packed(), _scales(scales, q, blocks, what),
-                                  _stream(stream)), what)
+    sc = _scales(scales, q, blocks, what)
+    xp, qp = x.packed(what), q.packed(what)
+    _check_device(what, x, q, scales)
+    _check(_lib.coco_quantize_fp8(xp, block_rows, qp, sc, _stream(stream)), what)
 
 
 def _operand_scales(lhs, lhs_scales, rhs, rhs_scales, what):
@@ -422,7 +450,9 @@ def coco_einsum_fp8(spec, lhs, lhs_scales, rhs, rhs_scales, out, stream=None):
     block; ``spec`` "mk,kn->mn" or "mk,nk->mn". Scale tensors: one per pointer of the operand."""
     what = "coco_einsum_fp8"
     sa, sb = _operand_scales(lhs, lhs_scales, rhs, rhs_scales, what)
-    _check(_lib.coco_einsum_fp8(spec.encode(), lhs.packed(), sa, rhs.packed(), sb, out.packed(), _stream(stream)), what)
+    a, b, o = lhs.packed(what), rhs.packed(what), out.packed(what)
+    _check_device(what, lhs, rhs, out, lhs_scales, rhs_scales)
+    _check(_lib.coco_einsum_fp8(spec.encode(), a, sa, b, sb, o, _stream(stream)), what)
 
 
 def coco_grouped_einsum(spec, lhs, lhs_scales, rhs, rhs_scales, offsets, out, stream=None):
@@ -433,8 +463,9 @@ def coco_grouped_einsum(spec, lhs, lhs_scales, rhs, rhs_scales, offsets, out, st
     sa, sb = _operand_scales(lhs, lhs_scales, rhs, rhs_scales, what)
     experts = (rhs if len(rhs.shape) == 3 else out).shape[0]
     off = None if offsets is None else _vector(offsets, torch.int32, len(lhs.tensors) * (experts + 1), what)
-    _check(_lib.coco_grouped_einsum(spec.encode(), lhs.packed(), sa, rhs.packed(), sb, off, out.packed(),
-                                    _stream(stream)), what)
+    a, b, o = lhs.packed(what), rhs.packed(what), out.packed(what)
+    _check_device(what, lhs, rhs, out, offsets, lhs_scales, rhs_scales)
+    _check(_lib.coco_grouped_einsum(spec.encode(), a, sa, b, sb, off, o, _stream(stream)), what)
 
 
 def coco_dropout_keep_mask(seed, dropout_p, first_index, count, mask, stream=None):
