@@ -330,10 +330,6 @@ def coco_looped_einsum_rs_sched(spec, lhs, rhs, out, schedule, stream=None):
 # -------------------------------------------- 8-bit and expert-grouped operators
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
 def _packed(d, what):
     return None if d is None else d.packed(what)
 

@@ -22,9 +22,9 @@
 // an MMA's N goes in steps of 32, so an expert's last tile costs what its rows
 // cost and not 256 (32 experts of 126 to 4000 rows: a quarter of the work). In
 // weight gradients A holds lhs columns, B rhs columns, and the rows are summed.
-// 16384 rows over 32 uneven experts, k 4096, n 2048 in bf16: 188 us (1.46
-// PFLOP/s), its weight gradient 205 us, of which storing 537 MB is a good part
-// (64 rows an expert: 97 us); one expert of 16384 rows 145 and 154 us.
+// 16384 rows over 32 uneven experts, k 4096, n 2048 in bf16: 187 us (1.47
+// PFLOP/s), its weight gradient 204 us, of which storing 537 MB is a good part
+// (64 rows an expert: 97 us); one expert of 16384 rows 145 and 155 us.
 //   warp 0        TMA producer: k-blocks 128 bytes deep into a ring of 6 stages of 32 KB.
 //   warp 1        issues the MMAs (CTA 0 of the pair) and owns TMEM.
 //   warps 2, 3    in weight gradients: have zeros loaded over what a k-block holds of the next expert's rows.
@@ -530,7 +530,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       // An expert's last k-block holds rows past its end. Zeros go over them in both operands (in one alone they would
       // leave 0 * infinity). They come by copies like any others, from rows out of range: counted on CTA 0's barrier,
       // they need no ordering of this CTA's own writes before the pair's MMA. Clearing with stores and an arrival that
-      // releases them to CTA 0 (cluster scope) took 232 us where this takes 206 (16384 rows, 32 uneven experts, k 4096,
+      // releases them to CTA 0 (cluster scope) took 232 us where this takes 204 (16384 rows, 32 uneven experts, k 4096,
       // n 2048). Warp 2 has A's two boxes of rows of 128 bytes done, warp 3 B's.
       const bool leader = elect_one();
       Walk w;
@@ -679,10 +679,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 // k_grouped_scaled (e4m3, many rows): one 128 x 256 tile per CTA and step (M = 128, N = 256), no CTA depending on
 // another. The block's product has to be added up and its TMEM buffer handed back every 128 k, and with one MMA over
 // two CTAs that hand-over crosses CTAs both ways (commit to the other's epilogue, arrivals back), some thousand cycles
-// of every two blocks' 1024. The price is that a CTA reads all 256 of its columns of rhs itself, 48 KB a block (L2 gives
-// them: 8192^3 takes 382 to 385 us, 2.87 PFLOP/s, from a graph, where two CTAs that each loaded half of the columns for
-// both took 388). Tiles of 128 rows also cost an expert's end half of what 256 would: 16384 rows over 32 uneven experts,
-// k 4096, n 2048: 131 to 142 us.
+// of every two blocks' 1024. The price is that a CTA reads all 256 of its columns of rhs itself, 48 KB a block, which
+// L2 gives: 8192^3 takes 383 to 395 us (2.87 PFLOP/s) from a graph, where two CTAs that each loaded half of the columns
+// for both took 388. Tiles of 128 rows also cost an expert's end half of what 256 would: 16384 rows over 32 uneven
+// experts, k 4096, n 2048: 124 to 127 us. What bounds it is the power cap in a long loop (433 us a call at 8192^3) and
+// the epilogue's loop: 8 TMEM loads, 64 packed multiply-adds and the hand-over a block.
 //   warp 0        TMA producer: 128 rows of lhs and 256 columns of rhs; 4 stages of 48 KB.
 //   warp 1        issues the MMAs and owns TMEM (two buffers of 256 columns).
 //   warps 4..11   two per TMEM lane quarter, 128 columns each: sums of the scaled blocks in registers, then stores.
@@ -938,8 +939,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_grouped_scaled(const __grid_cons
 // Where there are fewer tiles than SMs, a cluster of `split` CTAs shares a tile's k range: each sends its fp32
 // sums for another's rows straight into that CTA's shared memory (st.async, counted on an mbarrier), which
 // adds them in rank order. No atomics, no workspace: repeated calls give the same bits. One row, k = n = 4096 in
-// e4m3: 7.3 us (2.3 TB/s), most of it the launch, the ring's first fill and the clusters' exchange; 32 rows over 64
-// experts, k 4096, n 2048: 34 us (4.5 TB/s of the weights met), the last wave of tiles being partly filled.
+// e4m3: 8.6 us with cold weights, 7.3 with weights in L2, most of it the launch, the ring's first fill and the
+// clusters' exchange; 32 rows over 64 experts, k 4096, n 2048, cold: 32 us (4.8 TB/s of the weights met), the last wave
+// of tiles being partly filled.
 //   warp 0        TMA producer, a ring of 128-byte deep k-blocks: 16 KB of weights, ROWS x 128 bytes of lhs.
 //   warp 1        issues the MMAs and owns TMEM.
 //   warps 2..     epilogue, one per TMEM lane quarter (ROWS = 64: two, 32 rows each): a lane holds one column n.
@@ -1308,14 +1310,17 @@ struct Choice {
 };
 
 // The time of each kernel is the k-blocks that its busiest SM goes through, times what one takes there, and the
-// choice is the least product. Measured on a GB300, in ns a k-block (128 bytes of k): two CTAs on 256 rows 480 in
-// e4m3, 370 in 16 bits; few rows from the first figure on one SM to the second on all of them (then HBM counts):
-// 16 rows 250 to 360 in e4m3, 230 to 350 in 16 bits; 64 rows 360 to 500 and 260 to 390; e4m3 weights stored [k][n]
-// are the slow operand side of these MMAs: 330 to 510 and 460 to 700. A shared k range costs 1900 once.
-// Both sides, one call from a graph, e4m3 [n][k], k = n = 4096: 1 row 7.3 us (16 rows, four CTAs a tile) and 16.5
-// (256 rows); 64 rows 9.8 and 17.0; 128 rows 13.4 and 17.3; 256 rows 17.5 and 17.3; 512 rows 31.1 and 17.7. 64
-// experts, k 4096, n 2048: 32 rows 29.5 and 35.1 us, 256 rows 81 and 104, 1024 rows 118 and 108; stored [k][n] 32
-// rows 40.3 and 34.3, 256 rows 115 and 103.
+// choice is the least product. Measured on a GB300, in ns a k-block (128 bytes of k): a CTA on 128 rows 480 in e4m3,
+// two on 256 rows 370 in 16 bits; few rows from the first figure on one SM to the second on all of them (then HBM
+// counts): 16 rows 250 to 360 in e4m3, 230 to 350 in 16 bits; 64 rows 360 to 500 and 260 to 390; e4m3 weights stored
+// [k][n] are the slow operand side of these MMAs: 330 to 510 and 460 to 700. A shared k range costs 1900 once.
+// Both sides, from a graph with cold weights (input sets in turn that together pass L2), in us. e4m3 [n][k], k = n =
+// 4096: 1 row 8.6 (16 rows, four CTAs a tile) and 15.7 (tiles of 128 rows); 64 rows 11.2 and 16.4; 128 rows 13.9 and
+// 17.1; 256 rows 17.8 and 17.2; 512 rows 31.7 and 17.4. 64 experts, k 4096, n 2048: 8 rows 16.1 and 20.0; 32 rows 32.1
+// and 31.8; 128 rows 61.8 and 65.5; 256 rows 75.1 and 74.9; 1024 rows 110.8 and 91.3; stored [k][n] 32 rows 43.7 and
+// 31.4, 256 rows 106 and 73; in bf16 [n][k] 32 rows 53.2 and 54.5, 256 rows 135 and 142. (The rule takes clusters of
+// eight to find room while they number no more CTAs than SMs, and they do not always: 128 rows, k 8192, n 1024 take
+// 17.2 where four CTAs a tile take 12.6.)
 Choice choose(const GroupedLaunch& L, int kblocks) {
   const bool fp8 = L.in_dtype == COCO_F8E4M3, kn8 = fp8 && L.form == GRP_KN;
   const int64_t pair_ns = fp8 ? 480 : 370, split_ns = 1900;

@@ -134,9 +134,9 @@ __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
 // Eight values over a block's scale, in e4m3 (round to nearest even). The quotient is the value times the
 // scale's rounded reciprocal, corrected by its own residual (Markstein, "Computation of elementary functions on
 // the IBM RISC System/6000 processor", 1990), which makes it the rounded quotient: with the product alone, some
-// values fall on the other side of a rounding boundary (8192 x 4096 in fp16 differed from rows that were divided by
-// 1.2e-4 in norm, and by 3.3e-6 with the correction). An infinite scale keeps the
-// uncorrected product (0, or NaN for the infinity itself).
+// values fall on the other side of a rounding boundary. (With it some 30 of 33.5 million values still differ from the
+// rounding in 64 bits, as they do where rows are divided: what fp32 leaves.) An infinite scale keeps the uncorrected
+// product (0, or NaN for the infinity itself).
 __device__ __forceinline__ uint2 to_e4m3(const float (&f)[kChunk], float scale) {
   const float inv = __frcp_rn(scale);
   const float s = inv == 0.0f ? 0.0f : -scale;
@@ -228,8 +228,8 @@ struct NormArgs {
 
 // Grid x: rows (blockDim / tpr a block), grid y: groups. A row's loads, its barrier and its stores do not overlap,
 // so what keeps HBM busy is other blocks on the SM: four of 512 threads (16-bit types, the compiler held to 32
-// registers) took 8192 x 4096 fp16 on eight ranks, eight copies, from 233 to 213 us (6.64 TB/s); three had not
-// been enough.
+// registers, at the price of up to 40 bytes of local memory a thread in the 8-bit form) took 8192 x 4096 fp16 on eight
+// ranks, eight copies, from 233 to 213 us (6.67 TB/s); three had not been enough.
 template <typename T, int NR, int VPT, bool FP8>
 __global__ void __launch_bounds__(512, VPT == 1 && NR > 0 && sizeof(T) == 2 ? 4 : 1)
     k_allreduce_rmsnorm(const __grid_constant__ NormArgs a) {
@@ -341,9 +341,11 @@ struct NormBwdArgs {
 // THREADS and blocks an SM, by the registers (64 for 1024 threads an SM): 16-bit rows of up to 8192 columns have
 // two blocks of 512 threads, with two chunks a thread keeping the dw sums in shared memory (WIDE; each thread its own
 // columns') and reading dhidden only when it is added; wider ones 1024 threads a row of two or four chunks, the
-// latter reading hidden again (from L2) instead of keeping it. fp32 rows: 512 threads, WIDE from four chunks on.
-// Measured: 8192 x 4096 fp16 on eight ranks 119 us (6.2 TB/s), 16384 x 1024 on two 38 us, 777 x 8192 on two 24 us,
-// 4096 x 16384 bf16 on one 113 us, 2048 x 32768 141 us; HBM bounds the first, latency between a row's phases the rest.
+// latter reading hidden again (from L2) instead of keeping it. fp32 rows: 512 threads, WIDE from four chunks on. The
+// wide forms keep some values in local memory all the same (up to 88 bytes a thread in 16 bits, up to 328 in fp32).
+// Measured: 8192 x 4096 fp16 on eight ranks 119 us (6.2 TB/s), in fp32 233; 16384 x 1024 bf16 on two 40 us, 777 x 8192
+// on two 24 us, 4096 x 16384 on one 114 us (fp32 191), 2048 x 32768 141 us; HBM bounds the first two, latency between a
+// row's phases the rest.
 template <typename T, int VPT, int THREADS>
 struct BwdShape {
   static constexpr bool WIDE = VPT > (sizeof(T) == 2 ? 1 : 2);
@@ -565,8 +567,9 @@ __global__ void __launch_bounds__(256) k_quantize_rows(const __grid_constant__ Q
 }
 
 // One scale per 128 rows x 128 columns: a block holds the tile in registers (kTileThreads threads, kTileChunks
-// chunks each) between its maximum and its rounding. 8192 x 32768 in bf16: 136 us (5.94 TB/s), bound by HBM; four
-// blocks of 256 threads an SM (512 or 1024 threads a tile: 154 to 217 us). Grid x: tiles, row-major; grid y: tensors.
+// chunks each, those that 64 registers do not hold in local memory: 72 to 80 bytes, fp32 240) between its maximum and
+// its rounding. 8192 x 32768 in bf16: 135 us (5.96 TB/s), bound by HBM, in fp32 295; four blocks of 256 threads an SM
+// (512 or 1024 threads a tile: 154 to 217 us). Grid x: tiles, row-major; grid y: tensors.
 constexpr int kTileThreads = 256, kTileRows = kTileThreads / kBlockLanes, kTileChunks = 128 / kTileRows;
 
 template <typename T>

@@ -164,8 +164,8 @@ def mlp_2d(x_blocks, w1_blocks, w2_blocks, m_x, n_y, bufs=None, stream=None, sid
 
 
 def route(expert_of, experts):
-    """Rows sorted by expert for ``expert_of`` [tokens, choices] (int64, on the device; nothing comes back to the
-    host). Returns (token_of_row [rows], row_of_choice [tokens, choices], offsets [experts + 1] int32)."""
+    """Rows sorted by expert for ``expert_of`` [tokens, choices] (int64 in [0, experts), on the device; nothing comes
+    back to the host). Returns (token_of_row [rows], row_of_choice [tokens, choices], offsets [experts + 1] int32)."""
     flat = expert_of.reshape(-1)
     order = torch.argsort(flat, stable=True)
     row_of = torch.empty_like(order)

@@ -513,7 +513,9 @@ coco_status coco_quantize_fp8(const coco_tensor* x, int32_t block_rows, const co
  * [ceil(n/128), ceil(k/128)]: the product with the transpose, which is the first one's input gradient with the
  * same stored weight). lhs F8E4M3, scales [m, ceil(k/128)]; LOCAL, REPLICATED (read from rank 0's pointer) or
  * SLICED on k. rhs F8E4M3; LOCAL, REPLICATED or SLICED on k. out LOCAL in F32, F16 or BF16, rounded once from the fp32 sum of the
- * blocks. Scale pointers per rank as for the tensors. No output may overlap another array.
+ * blocks. The product of a block's two scales is formed first, in fp32: where it leaves the normal range (scales beyond
+ * 2^64, or below 2^-63, on both sides) the block's part is infinite, NaN, zero or short of bits. Scale pointers per
+ * rank as for the tensors. No output may overlap another array.
  */
 coco_status coco_einsum_fp8(const char* spec, const coco_tensor* lhs, const float* const* lhs_scales,
                             const coco_tensor* rhs, const float* const* rhs_scales, const coco_tensor* out,
