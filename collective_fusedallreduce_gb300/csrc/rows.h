@@ -1,0 +1,221 @@
+// Rows held in registers: the pieces that the norms' and the experts' kernels share.
+// A row belongs to `tpr` threads (a power of two, 32 to 1024), and a thread holds
+// its 8-element chunks t, t + tpr, ... in fp32.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <type_traits>
+
+#include "internal.h"
+
+namespace coco {
+namespace {
+
+constexpr int kChunk = 8;         // elements a thread holds per step
+constexpr int kBlockLanes = 16;   // lanes that hold the 128 columns of one scale
+constexpr float kE4m3Max = 448.0f;
+constexpr float kAmaxFloor = 0x1p-100f;  // smallest block maximum a scale is made from: all-zero blocks stay finite
+
+// ------------------------------------------------------------------ chunks
+
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
+
+// Eight consecutive elements as loaded, and their conversions from and to fp32. Stores are streaming ones,
+// which keeps outputs from displacing what is still to be read (the gradient, 8192 x 4096 fp16 on eight ranks: 118 to
+// 116 us; in the quantiser the same cost 15 %, and it stores plainly).
+template <typename T>
+struct Chunk {
+  uint4 v;
+  __device__ __forceinline__ void load(const void* base, int64_t c) {
+    v = ld_stream(static_cast<const uint4*>(base) + c);
+  }
+  __device__ __forceinline__ void load_cached(const void* base, int64_t c) {
+    v = static_cast<const uint4*>(base)[c];
+  }
+  __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void get(float (&f)[kChunk]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float2 p;
+      if constexpr (std::is_same<T, __half>::value) p = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      else p = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+      f[2 * i] = p.x;
+      f[2 * i + 1] = p.y;
+    }
+  }
+  __device__ __forceinline__ void put(const float (&f)[kChunk]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (std::is_same<T, __half>::value) {
+        const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ void store(void* base, int64_t c) const { __stcs(static_cast<uint4*>(base) + c, v); }
+};
+
+template <>
+struct Chunk<float> {
+  uint4 v, w;
+  __device__ __forceinline__ void load(const void* base, int64_t c) {
+    v = ld_stream(static_cast<const uint4*>(base) + 2 * c);
+    w = ld_stream(static_cast<const uint4*>(base) + 2 * c + 1);
+  }
+  __device__ __forceinline__ void load_cached(const void* base, int64_t c) {
+    v = static_cast<const uint4*>(base)[2 * c];
+    w = static_cast<const uint4*>(base)[2 * c + 1];
+  }
+  __device__ __forceinline__ void zero() { v = w = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void get(float (&f)[kChunk]) const {
+    f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y); f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
+    f[4] = __uint_as_float(w.x); f[5] = __uint_as_float(w.y); f[6] = __uint_as_float(w.z); f[7] = __uint_as_float(w.w);
+  }
+  __device__ __forceinline__ void put(const float (&f)[kChunk]) {
+    v = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    w = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
+  }
+  __device__ __forceinline__ void store(void* base, int64_t c) const {
+    __stcs(static_cast<uint4*>(base) + 2 * c, v);
+    __stcs(static_cast<uint4*>(base) + 2 * c + 1, w);
+  }
+};
+
+// The larger of two magnitudes; a NaN stays one, so that a block that holds one shows it in its scale.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ float chunk_amax(const float (&f)[kChunk]) {
+  float m = fabsf(f[0]);
+#pragma unroll
+  for (int j = 1; j < kChunk; ++j) m = max_nan(m, fabsf(f[j]));
+  return m;
+}
+
+// The scale of a block whose largest magnitude is `amax`: the largest e4m3 value stands for that magnitude.
+__device__ __forceinline__ float scale_of(float amax) { return __fdiv_rn(max_nan(amax, kAmaxFloor), kE4m3Max); }
+
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+
+// Eight values over a block's scale, in e4m3 (round to nearest even). The quotient is the value times the
+// scale's rounded reciprocal, corrected by its own residual (Markstein, "Computation of elementary functions on
+// the IBM RISC System/6000 processor", 1990), which makes it the rounded quotient: with the product alone, some
+// values fall on the other side of a rounding boundary. (With it some 30 of 33.5 million values still differ from the
+// rounding in 64 bits, as they do where rows are divided: what fp32 leaves.) An infinite scale keeps the uncorrected
+// product (0, or NaN for the infinity itself).
+__device__ __forceinline__ uint2 to_e4m3(const float (&f)[kChunk], float scale) {
+  const float inv = __frcp_rn(scale);
+  const float s = inv == 0.0f ? 0.0f : -scale;
+  const uint64_t inv2 = pack2(inv, inv), s2 = pack2(s, s);  // (two values an instruction)
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t f2 = pack2(f[2 * i], f[2 * i + 1]);
+    uint64_t q2, r2;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q2) : "l"(f2), "l"(inv2));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r2) : "l"(q2), "l"(s2), "l"(f2));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(q2) : "l"(r2), "l"(inv2));
+    float2 q;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(q.x), "=f"(q.y) : "l"(q2));
+    h[i] = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+  }
+  return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+}
+
+// The sum of `v` over the threads of a row (tpr of them, a power of two and at least a warp), the same
+// value in each: within warps by shuffles, across warps through shared memory in warp order. Consecutive
+// calls alternate between the two halves of `red` (`turn`), so one barrier a call is enough. OWN_BARRIERS: rows
+// that share a block have a barrier each (named ones, from 1 on), so that they do not wait for one another.
+template <bool OWN_BARRIERS>
+__device__ __forceinline__ float row_sum(float v, int tpr, int slot, float (*red)[32], int turn) {
+#pragma unroll
+  for (int m = 16; m; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  if (tpr == 32) return v;
+  const int warp = threadIdx.x >> 5, warps = tpr >> 5;
+  if ((threadIdx.x & 31) == 0) red[turn][warp] = v;
+  // (one row a block, or more rows than there are named barriers: all threads together)
+  if (!OWN_BARRIERS || blockDim.x == tpr || blockDim.x > 15 * tpr) __syncthreads();
+  else asm volatile("bar.sync %0, %1;" ::"r"(1 + slot), "r"(tpr) : "memory");
+  const int first = warp & ~(warps - 1);
+  float s = red[turn][first];
+  for (int i = 1; i < warps; ++i) s += red[turn][first + i];
+  return s;
+}
+
+// The sum over the ranks' chunk c in rank order (fp32). NR: compile-time rank count, or 0.
+template <typename T, int NR>
+__device__ __forceinline__ void sum_ranks(const void* const* in, int nranks, int64_t c, float (&acc)[kChunk]) {
+  if constexpr (NR > 0) {
+    Chunk<T> raw[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) raw[r].load(in[r], c);
+    raw[0].get(acc);
+#pragma unroll
+    for (int r = 1; r < NR; ++r) {
+      float f[kChunk];
+      raw[r].get(f);
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j) acc[j] += f[j];
+    }
+  } else {
+    Chunk<T> first;
+    first.load(in[0], c);
+    first.get(acc);
+    for (int r0 = 1; r0 < nranks; r0 += 4) {
+      Chunk<T> raw[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (r0 + r < nranks) raw[r].load(in[r0 + r], c);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (r0 + r < nranks) {
+          float f[kChunk];
+          raw[r].get(f);
+#pragma unroll
+          for (int j = 0; j < kChunk; ++j) acc[j] += f[j];
+        }
+      }
+    }
+  }
+}
+
+// Threads of a row: a power of two that covers its chunks, at most 512, each with up to eight chunks (rows of up to
+// 32768 columns).
+struct RowShape {
+  int tpr_log2, vpt, threads, rpb;
+};
+inline RowShape row_shape(int nchunks) {
+  RowShape s;
+  s.tpr_log2 = 5;
+  while (s.tpr_log2 < 9 && (1 << s.tpr_log2) < nchunks) ++s.tpr_log2;
+  const int tpr = 1 << s.tpr_log2;
+  s.vpt = 1;
+  while (s.vpt * tpr < nchunks) s.vpt *= 2;
+  s.threads = tpr < 256 ? 256 : tpr;
+  s.rpb = s.threads / tpr;
+  return s;
+}
+
+}  // namespace
+}  // namespace coco
