@@ -97,6 +97,20 @@ for _name, _args in {
     "coco_quantize_fp8": [_B, ctypes.c_int32, _B, _B, _S],
     "coco_einsum_fp8": [ctypes.c_char_p, _B, _B, _B, _B, _B, _S],
     "coco_grouped_einsum": [ctypes.c_char_p, _B, _B, _B, _B, ctypes.c_void_p, _B, _S],
+    "coco_expert_sort": [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                         ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, _S],
+    "coco_expert_dispatch": [_B, _B, ctypes.c_void_p, _B, _B, _S],
+    "coco_expert_combine": [_B, ctypes.c_void_p, ctypes.c_void_p, _B, _B, _S],
+    "coco_expert_combine_backward": [_B, _B, ctypes.c_void_p, ctypes.c_void_p, _B, ctypes.c_void_p, _S],
+    "coco_allreduce_layernorm": [_B, _B, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_float, _B, _B, _B,
+                                 ctypes.c_void_p, ctypes.c_void_p, _S],
+    "coco_allreduce_layernorm_backward": [_B, _B, _B, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, _B,
+                                          ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, _S],
+    "coco_scattered_clip": [ctypes.POINTER(CocoScatteredPlan), ctypes.c_int32, ctypes.c_float,
+                            ctypes.POINTER(CocoScatteredPlan), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, _S],
+    "coco_scattered_allreduce_clip": [ctypes.POINTER(CocoScatteredPlan), ctypes.c_float, ctypes.c_float,
+                                      ctypes.POINTER(CocoScatteredPlan), ctypes.c_void_p, ctypes.c_void_p,
+                                      ctypes.c_size_t, _S],
     "coco_device_status": [_S],
     "coco_wait_selftest": [ctypes.c_uint64, _S],
 }.items():
@@ -113,6 +127,10 @@ _lib.coco_scattered_allreduce.argtypes = [ctypes.POINTER(CocoScatteredPlan), cty
 _lib.coco_scattered_allreduce.restype = ctypes.c_int
 _lib.coco_allreduce_rmsnorm_backward_bytes.argtypes = [ctypes.c_int64, ctypes.c_int64]
 _lib.coco_allreduce_rmsnorm_backward_bytes.restype = ctypes.c_size_t
+_lib.coco_allreduce_layernorm_backward_bytes.argtypes = [ctypes.c_int64, ctypes.c_int64]
+_lib.coco_allreduce_layernorm_backward_bytes.restype = ctypes.c_size_t
+_lib.coco_scattered_clip_bytes.argtypes = []
+_lib.coco_scattered_clip_bytes.restype = ctypes.c_size_t
 _lib.coco_status_string.argtypes = [ctypes.c_int]
 _lib.coco_status_string.restype = ctypes.c_char_p
 _lib.coco_last_cuda_error.restype = ctypes.c_int
@@ -139,6 +157,9 @@ EXPORTED = [
     "coco_shard_order", "coco_loop_profitable", "coco_plan_cache_stats", "coco_plan_cache_clear",
     "coco_allreduce_rmsnorm", "coco_allreduce_rmsnorm_backward", "coco_allreduce_rmsnorm_backward_bytes",
     "coco_quantize_fp8", "coco_einsum_fp8", "coco_grouped_einsum",
+    "coco_expert_sort", "coco_expert_dispatch", "coco_expert_combine", "coco_expert_combine_backward",
+    "coco_allreduce_layernorm", "coco_allreduce_layernorm_backward", "coco_allreduce_layernorm_backward_bytes",
+    "coco_scattered_clip", "coco_scattered_allreduce_clip", "coco_scattered_clip_bytes",
 ]
 
 
@@ -462,6 +483,156 @@ def coco_grouped_einsum(spec, lhs, lhs_scales, rhs, rhs_scales, offsets, out, st
     a, b, o = lhs.packed(what), rhs.packed(what), out.packed(what)
     _check_device(what, lhs, rhs, out, offsets, lhs_scales, rhs_scales)
     _check(_lib.coco_grouped_einsum(spec.encode(), a, sa, b, sb, off, o, _stream(stream)), what)
+
+
+# --------------------------------- experts' rows, layer norm, gradient clipping
+
+
+def _check_here(what, *tensors):
+    """_check_device, and refuses another device than the current one, on which the call runs."""
+    _check_device(what, *tensors)
+    here = torch.cuda.current_device()
+    for t in tensors:
+        t = t.tensors[0] if type(t) is Dist else t[0] if type(t) is list and t else t
+        if t is not None and t.get_device() != here:
+            raise CocoError(7, f"{what}: a tensor of another device than the current one")
+
+
+def _pointer(t, dtype, numel, what):
+    """A plain tensor argument's address, or None."""
+    return None if t is None else _vector(t, dtype, numel, what)
+
+
+def coco_expert_sort(expert_of, experts, row_of_choice, choice_of_row, offsets, stream=None):
+    """The rows of a mixture of experts, sorted by expert. ``expert_of`` [tokens, choices] or [groups, tokens, choices]
+    (int32 or int64; a number outside [0, experts) has no row) gives ``row_of_choice`` (int32, the same shape, -1 for
+    no row), ``choice_of_row`` (int32 [groups, tokens * choices] or None; -1 behind the last expert's rows) and
+    ``offsets`` (int32 [groups * ranks, experts + 1], a line per rank as coco_grouped_einsum reads them)."""
+    what = "coco_expert_sort"
+    shape = expert_of.shape
+    if not 2 <= len(shape) <= 3 or not expert_of.is_contiguous() or offsets.dim() != 2:
+        raise CocoError(2, what)
+    if expert_of.dtype not in (torch.int64, torch.int32):
+        raise CocoError(3, what)
+    groups = shape[0] if len(shape) == 3 else 1
+    lines = offsets.shape[0]
+    if groups < 1 or lines % groups:
+        raise CocoError(2, what)
+    n = expert_of.numel()
+    row = _vector(row_of_choice, torch.int32, n, what)
+    choice = _pointer(choice_of_row, torch.int32, n, what)
+    off = _vector(offsets, torch.int32, lines * (experts + 1), what)
+    _check_here(what, expert_of, row_of_choice, choice_of_row, offsets)
+    _check(_lib.coco_expert_sort(expert_of.data_ptr(), expert_of.element_size(), shape[-2], shape[-1], experts, groups,
+                                 lines // groups, row, choice, off, _stream(stream)), what)
+
+
+def _row_scales(tensors, d, what):
+    if tensors is None:
+        return None
+    rows, cols = _rows_cols(d)
+    return _scales(tensors, d, rows * _blocks(cols), what)
+
+
+def coco_expert_dispatch(x, x_scales, row_of_choice, rows, row_scales, stream=None):
+    """rows[row_of_choice[t, k]] = x[t]: ``x`` REPLICATED [tokens, cols] to ``rows`` REPLICATED [tokens * choices,
+    cols], with a scale tensor per pointer where they are float8_e4m3fn (else None). Rows that no choice names are left
+    as they were."""
+    what = "coco_expert_dispatch"
+    sx, sr = _row_scales(x_scales, x, what), _row_scales(row_scales, rows, what)
+    row = _vector(row_of_choice, torch.int32, rows.shape[0] * rows.ngroups, what)
+    xp, rp = x.packed(what), rows.packed(what)
+    _check_here(what, x, rows, row_of_choice, x_scales, row_scales)
+    _check(_lib.coco_expert_dispatch(xp, sx, row, rp, sr, _stream(stream)), what)
+
+
+def coco_expert_combine(rows, row_of_choice, gates, residual, out, stream=None):
+    """out[t] = sum over k of gates[t, k] * rows[row_of_choice[t, k]]: every rank's own sum (``out`` LOCAL, ``residual``
+    None), or their AllReduce with the residual (``out`` REPLICATED). ``gates``: fp32, the shape of ``row_of_choice``, or
+    None for ones, which is the dispatch's gradient."""
+    what = "coco_expert_combine"
+    n = rows.shape[0] * rows.ngroups
+    row, w = _vector(row_of_choice, torch.int32, n, what), _pointer(gates, torch.float32, n, what)
+    rp, res, o = rows.packed(what), _packed(residual, what), out.packed(what)
+    _check_here(what, rows, residual, out, row_of_choice, gates)
+    _check(_lib.coco_expert_combine(rp, row, w, res, o, _stream(stream)), what)
+
+
+def coco_expert_combine_backward(dout, rows, row_of_choice, gates, drows, dgates, stream=None):
+    """The gradient of coco_expert_combine: ``drows`` (REPLICATED: every rank's is the same) and ``dgates`` (fp32, the
+    shape of ``row_of_choice``; None with ``rows`` None) for ``dout``, the gradient of the summed output."""
+    what = "coco_expert_combine_backward"
+    n = drows.shape[0] * drows.ngroups
+    row, w = _vector(row_of_choice, torch.int32, n, what), _pointer(gates, torch.float32, n, what)
+    dw = _pointer(dgates, torch.float32, n, what)
+    d, rp, o = dout.packed(what), _packed(rows, what), drows.packed(what)
+    _check_here(what, dout, rows, drows, row_of_choice, gates, dgates)
+    _check(_lib.coco_expert_combine_backward(d, rp, row, w, o, dw, _stream(stream)), what)
+
+
+def coco_allreduce_layernorm(partials, residual, weight, bias, eps, hidden, normed, scales, mean, rstd, stream=None):
+    """h = sum of the ranks' partials + residual; normed = (h - mean) / sqrt(variance + eps) * weight + bias over the
+    last dimension. ``bias``, ``residual``, ``hidden`` (the stored h), ``mean`` and ``rstd`` ([groups, rows] fp32) may be
+    None; ``normed`` and ``scales`` as coco_allreduce_rmsnorm's."""
+    what = "coco_allreduce_layernorm"
+    rows, cols = _rows_cols(partials)
+    dtype, n = partials.tensors[0].dtype, rows * partials.ngroups
+    w, b = _vector(weight, dtype, cols, what), _pointer(bias, dtype, cols, what)
+    m, r = _pointer(mean, torch.float32, n, what), _pointer(rstd, torch.float32, n, what)
+    sc = _scales(scales, normed, rows * _blocks(cols), what)
+    p, res, hid, nrm = partials.packed(what), _packed(residual, what), _packed(hidden, what), normed.packed(what)
+    _check_here(what, partials, residual, hidden, normed, weight, bias, mean, rstd, scales)
+    _check(_lib.coco_allreduce_layernorm(p, res, w, b, eps, hid, nrm, sc, m, r, _stream(stream)), what)
+
+
+def coco_allreduce_layernorm_backward_bytes(rows, cols):
+    """Workspace bytes of coco_allreduce_layernorm_backward for ``rows`` rows (all groups together)."""
+    return int(_lib.coco_allreduce_layernorm_backward_bytes(int(rows), int(cols)))
+
+
+def coco_allreduce_layernorm_backward(dnormed, dhidden, hidden, weight, mean, rstd, dx, dweight, dbias, workspace,
+                                      stream=None):
+    """The gradient of coco_allreduce_layernorm: ``dnormed`` LOCAL (summed over the ranks here), ``dhidden`` the
+    residual stream's gradient or None; writes ``dx`` (of each partial and of the residual), ``dweight`` and ``dbias``
+    (fp32; the latter may be None). ``workspace``: coco_allreduce_layernorm_backward_bytes() bytes."""
+    what = "coco_allreduce_layernorm_backward"
+    rows, cols = _rows_cols(dnormed)
+    w = _vector(weight, dnormed.tensors[0].dtype, cols, what)
+    m = _vector(mean, torch.float32, rows * dnormed.ngroups, what)
+    r = _vector(rstd, torch.float32, rows * dnormed.ngroups, what)
+    dw, db = _vector(dweight, torch.float32, cols, what), _pointer(dbias, torch.float32, cols, what)
+    if not workspace.is_contiguous():
+        raise CocoError(2, what)
+    dn, dh, hid, o = dnormed.packed(what), _packed(dhidden, what), hidden.packed(what), dx.packed(what)
+    _check_here(what, dnormed, dhidden, hidden, dx, weight, mean, rstd, dweight, dbias, workspace)
+    _check(_lib.coco_allreduce_layernorm_backward(dn, dh, hid, w, m, r, o, dw, db, workspace.data_ptr(),
+                                                  workspace.nbytes, _stream(stream)), what)
+
+
+def coco_scattered_clip_bytes():
+    """Workspace bytes of coco_scattered_clip and coco_scattered_allreduce_clip."""
+    return int(_lib.coco_scattered_clip_bytes())
+
+
+def _clip(name, plan, second, max_norm, out, norm, workspace, stream):
+    n = _vector(norm, torch.float32, 1, name)
+    if not workspace.is_contiguous():
+        raise CocoError(2, name)
+    _check_here(name, norm, workspace)
+    _check(getattr(_lib, name)(ctypes.byref(plan), second, max_norm, None if out is None else ctypes.byref(out), n,
+                               workspace.data_ptr(), workspace.nbytes, _stream(stream)), name)
+
+
+def coco_scattered_clip(plan, layout, max_norm, out, norm, workspace, stream=None):
+    """Scales the plan's tensors so that their norm is at most ``max_norm`` (inf: only the norm), into the tensors of
+    the plan ``out`` (None: in place); ``norm`` (one fp32) receives the norm before. ``layout`` LOCAL: the ranks'
+    tensors are parts of one gradient; REPLICATED: copies of it. ``workspace``: coco_scattered_clip_bytes() bytes."""
+    _clip("coco_scattered_clip", plan, layout, max_norm, out, norm, workspace, stream)
+
+
+def coco_scattered_allreduce_clip(plan, alpha, max_norm, out, norm, workspace, stream=None):
+    """coco_scattered_allreduce (alpha times the sum over the ranks) with the sum's norm and clipping fused in."""
+    _clip("coco_scattered_allreduce_clip", plan, alpha, max_norm, out, norm, workspace, stream)
 
 
 def coco_dropout_keep_mask(seed, dropout_p, first_index, count, mask, stream=None):

@@ -1,0 +1,476 @@
+// Tokens to their experts and back. A routing names `choices` experts for every
+// token; choice i = t * choices + k of it has the row
+//
+//   row(i) = #{j: e(j) < e(i)} + #{j < i: e(j) = e(i)}
+//
+// of the experts' operands (sorted by expert, within one in the choices' order),
+// or none where e(i) is not an expert. Then
+//
+//   dispatch          rows[row(t, k)] = x[t]
+//   combine           out[t] = sum_k gate[t, k] * rows[row(t, k)]   (+ over ranks, + residual)
+//   combine backward  drows[row(t, k)] = gate[t, k] * dout[t]
+//                     dgate[t, k] = sum over ranks and columns of dout[t] * rows[row(t, k)]
+//
+// and the dispatch's gradient is a combine without gates. All of them walk tokens
+// (never rows), so a token's row is read once however many experts it goes to, and
+// rows that no choice names are not touched. Bound by HBM but for the sort, which
+// is bound by latency.
+
+#include <atomic>
+
+#include "internal.h"
+#include "rows.h"
+#include "tc_ptx.h"
+
+namespace coco {
+namespace {
+
+// -------------------------------------------------------------------- sort
+
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+constexpr int kSortSmem = 200 * 1024;
+constexpr int kSortTile = 8192;  // experts that a pass over the choices counts (more of them: more passes)
+
+struct SortArgs {
+  const void* expert_of;  // [groups][n]
+  int32_t* row_of;        // [groups][n]
+  int32_t* choice_of;     // [groups][n], or null
+  int32_t* offsets;       // [groups * nranks][experts + 1]
+  int64_t n, seg;         // choices, and those of one warp (a multiple of 32)
+  int32_t experts, tile, warps, nranks;
+};
+
+// The expert of choice i, or -1 where it is none.
+template <typename I>
+__device__ __forceinline__ int expert_at(const I* e, int64_t i, int experts) {
+  const I v = e[i];
+  return v >= 0 && v < static_cast<I>(experts) ? static_cast<int>(v) : -1;
+}
+
+__device__ __forceinline__ uint32_t cluster_nctarank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ int32_t ld_peer(const int32_t* p, int cta) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(cta));
+  int32_t v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// A stable counting sort by one cluster of CTAs for each group. Every warp owns a run of the choices and counts its
+// experts in shared memory; a column's counts become the warps' starts in order, the CTAs' sums are exchanged through
+// distributed shared memory, and a scan over the experts gives the offsets. Each warp then walks its run again, 32
+// choices at a time: a choice's row is its expert's start, plus what the warp has placed there, plus the earlier lanes
+// with the same expert.
+template <typename I>
+__global__ void __launch_bounds__(kSortThreads) k_expert_sort(const __grid_constant__ SortArgs a) {
+  extern __shared__ int32_t sort_smem[];
+  __shared__ int32_t scan[2][kSortWarps];
+  int32_t* hist = sort_smem;                // [warps][tile]
+  int32_t* sums = hist + a.warps * a.tile;  // [tile]: this CTA's choices of every expert
+  int32_t* start = sums + a.tile;           // [tile]: the first row of this CTA's
+  const int ctas = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
+  const int g = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const I* expert_of = static_cast<const I*>(a.expert_of) + g * a.n;
+  int32_t* row_of = a.row_of + g * a.n;
+  int32_t* choice_of = a.choice_of ? a.choice_of + g * a.n : nullptr;
+  const int64_t at = static_cast<int64_t>(rank * a.warps + warp) * a.seg;
+  const int64_t first = warp < a.warps ? (at < a.n ? at : a.n) : a.n;
+  const int64_t last = first + a.seg < a.n ? first + a.seg : a.n;
+  int32_t base = 0;  // rows of the experts before this tile's
+  for (int e0 = 0; e0 < a.experts || e0 == 0; e0 += a.tile) {
+    const int ne = a.experts - e0 < a.tile ? a.experts - e0 : a.tile;
+    for (int i = threadIdx.x; i < a.warps * a.tile; i += kSortThreads) hist[i] = 0;
+    __syncthreads();
+    for (int64_t i = first + lane; i < last; i += 32) {
+      const int e = expert_at(expert_of, i, a.experts) - e0;
+      if (e >= 0 && e < ne) atomicAdd(&hist[warp * a.tile + e], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < ne; e += kSortThreads) {
+      int32_t s = 0;
+      for (int w = 0; w < a.warps; ++w) {
+        const int32_t c = hist[w * a.tile + e];
+        hist[w * a.tile + e] = s;
+        s += c;
+      }
+      sums[e] = s;
+    }
+    cluster_sync();
+    int turn = 0;
+    for (int b = 0; b < ne; b += kSortThreads, turn ^= 1) {
+      const int e = b + threadIdx.x;
+      int32_t before = 0, all = 0;
+      if (e < ne)
+        for (int c = 0; c < ctas; ++c) {
+          const int32_t s = ld_peer(sums + e, c);
+          all += s;
+          if (c < rank) before += s;
+        }
+      int32_t incl = all;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int32_t v = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += v;
+      }
+      if (lane == 31) scan[turn][warp] = incl;
+      __syncthreads();
+      int32_t here = base, total = 0;
+      for (int w = 0; w < kSortWarps; ++w) {
+        const int32_t v = scan[turn][w];
+        if (w < warp) here += v;
+        total += v;
+      }
+      here += incl - all;
+      if (e < ne) {
+        start[e] = here + before;
+        if (rank == 0)
+          for (int r = 0; r < a.nranks; ++r)
+            a.offsets[static_cast<int64_t>(g * a.nranks + r) * (a.experts + 1) + e0 + e] = here;
+      }
+      base += total;
+    }
+    __syncthreads();
+    for (int64_t i0 = first; i0 < last; i0 += 32) {
+      const int64_t i = i0 + lane;
+      const int all_e = i < last ? expert_at(expert_of, i, a.experts) : -1;
+      const int e = all_e >= e0 && all_e < e0 + ne ? all_e - e0 : -1;
+      const unsigned peers = __match_any_sync(0xffffffffu, e);
+      int32_t pos = -1;
+      if (e >= 0) pos = start[e] + hist[warp * a.tile + e] + __popc(peers & ((1u << lane) - 1));
+      __syncwarp();
+      if (e >= 0 && (peers >> lane) == 1u) hist[warp * a.tile + e] += __popc(peers);  // (the last lane of them)
+      __syncwarp();
+      if (i < last) {
+        if (e >= 0) {
+          row_of[i] = pos;
+          if (choice_of) choice_of[pos] = static_cast<int32_t>(i);
+        } else if (all_e < 0 && e0 == 0) {
+          row_of[i] = -1;
+        }
+      }
+    }
+    cluster_sync();  // (nobody's sums are read any more)
+  }
+  if (rank == 0 && threadIdx.x < a.nranks)
+    a.offsets[static_cast<int64_t>(g * a.nranks + threadIdx.x) * (a.experts + 1) + a.experts] = base;
+  if (choice_of)
+    for (int64_t p = static_cast<int64_t>(base) + rank * kSortThreads + threadIdx.x; p < a.n; p += ctas * kSortThreads)
+      choice_of[p] = -1;
+}
+
+// ---------------------------------------------------------------- dispatch
+
+constexpr int kThreads = 256;
+
+struct DispatchArgs {
+  ExpertTables t;
+  const int32_t* row_of;  // [groups][tokens][choices]
+  int64_t tokens, rows;
+  int32_t choices, nranks;
+  int32_t nvec, nscales;  // 16-byte vectors of a row, scales of a row
+};
+
+// Grid x: a token's vectors and then its scales, token after token; grid y: groups.
+__global__ void __launch_bounds__(kThreads) k_expert_dispatch(const __grid_constant__ DispatchArgs a) {
+  const int g = blockIdx.y;
+  const char* x = static_cast<const char*>(a.t.in[g]);
+  const float* scales = a.t.in_scales[g];
+  const int32_t* row_of = a.row_of + g * a.tokens * a.choices;
+  const int per = a.nvec + a.nscales, nout = a.t.nout[g], slot0 = g * a.nranks;
+  const int64_t total = a.tokens * per, step = static_cast<int64_t>(gridDim.x) * kThreads;
+  for (int64_t p = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; p < total; p += step) {
+    const int64_t t = total <= 0x7fffffff ? static_cast<uint32_t>(p) / static_cast<uint32_t>(per) : p / per;
+    const int c = static_cast<int>(p - t * per);
+    if (c < a.nvec) {
+      const uint4 v = ld_stream(x + (t * a.nvec + c) * 16);
+      for (int k = 0; k < a.choices; ++k) {
+        const int64_t row = row_of[t * a.choices + k];
+        if (row >= 0 && row < a.rows)
+          for (int q = 0; q < nout; ++q) __stcs(static_cast<uint4*>(a.t.out[slot0 + q]) + row * a.nvec + c, v);
+      }
+    } else {
+      const float v = scales[t * a.nscales + (c - a.nvec)];
+      for (int k = 0; k < a.choices; ++k) {
+        const int64_t row = row_of[t * a.choices + k];
+        if (row >= 0 && row < a.rows)
+          for (int q = 0; q < nout; ++q) a.t.out_scales[slot0 + q][row * a.nscales + (c - a.nvec)] = v;
+      }
+    }
+  }
+}
+
+// ----------------------------------------------------------------- combine
+
+struct CombineArgs {
+  ExpertTables t;
+  const int32_t* row_of;  // [groups][tokens][choices]
+  const float* gates;     // the same shape, or null (ones)
+  int64_t tokens, rows;
+  int32_t choices, nranks, nchunks;
+};
+
+// SUMMED: grid y counts groups, whose ranks' rows are added up, with the residual, for every distinct output. Otherwise
+// it counts ranks, each with an output of its own (NR is 1). Grid x: chunks of 8 columns, token after token. A choice's
+// rows are added over the ranks first (in order), then weighted; product and sum are rounded one by one.
+template <typename T, int NR, bool SUMMED>
+__global__ void __launch_bounds__(kThreads) k_expert_combine(const __grid_constant__ CombineArgs a) {
+  const int g = SUMMED ? blockIdx.y : blockIdx.y / a.nranks;
+  const int slot0 = SUMMED ? g * a.nranks : blockIdx.y;
+  const void* const* in = a.t.in + slot0;
+  const void* residual = SUMMED ? a.t.residual[g] : nullptr;
+  const int nout = SUMMED ? a.t.nout[g] : 1;
+  const int32_t* row_of = a.row_of + g * a.tokens * a.choices;
+  const float* gates = a.gates ? a.gates + g * a.tokens * a.choices : nullptr;
+  const int64_t total = a.tokens * a.nchunks, step = static_cast<int64_t>(gridDim.x) * kThreads;
+  for (int64_t p = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; p < total; p += step) {
+    const int64_t t = total <= 0x7fffffff ? static_cast<uint32_t>(p) / static_cast<uint32_t>(a.nchunks) : p / a.nchunks;
+    const int c = static_cast<int>(p - t * a.nchunks);
+    Chunk<T> res;
+    if (residual) res.load(residual, p);
+    float acc[kChunk];
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j) acc[j] = 0.0f;
+    for (int k = 0; k < a.choices; ++k) {
+      const int64_t row = row_of[t * a.choices + k];
+      if (row < 0 || row >= a.rows) continue;
+      float f[kChunk];
+      sum_ranks<T, NR>(in, a.nranks, row * a.nchunks + c, f);
+      if (gates) {
+        const float w = gates[t * a.choices + k];
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j) f[j] = __fmul_rn(f[j], w);
+      }
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j) acc[j] = __fadd_rn(acc[j], f[j]);
+    }
+    if (residual) {
+      float f[kChunk];
+      res.get(f);
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j) acc[j] += f[j];
+    }
+    Chunk<T> o;
+    o.put(acc);
+    for (int q = 0; q < nout; ++q) o.store(a.t.out[slot0 + q], p);
+  }
+}
+
+// -------------------------------------------------------- combine backward
+
+struct CombineBwdArgs {
+  ExpertTables t;         // in: every rank's rows (all null without dgates); residual: dout of every group
+  const int32_t* row_of;  // [groups][tokens][choices]
+  const float* gates;     // or null (ones)
+  float* dgates;          // or null
+  int64_t tokens, rows;
+  int32_t choices, nranks, nchunks;
+  int32_t tpr_log2;
+};
+
+// A token belongs to `tpr` threads, which keep its gradient in registers; grid y: groups.
+template <typename T, int NR, int VPT>
+__global__ void __launch_bounds__(512) k_expert_combine_backward(const __grid_constant__ CombineBwdArgs a) {
+  __shared__ float red[2][32];
+  const int g = blockIdx.y;
+  const int tpr = 1 << a.tpr_log2;
+  const int tt = threadIdx.x & (tpr - 1), slot = threadIdx.x >> a.tpr_log2, rpb = blockDim.x >> a.tpr_log2;
+  const void* const* in = a.t.in + g * a.nranks;
+  const int slot0 = g * a.nranks, nout = a.t.nout[g];
+  int turn = 0;
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * rpb; base < a.tokens;
+       base += static_cast<int64_t>(gridDim.x) * rpb) {
+    const int64_t t = base + slot;
+    const bool live = t < a.tokens;
+    Chunk<T> d[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = tt + i * tpr;
+      if (live && c < a.nchunks) d[i].load(a.t.residual[g], t * a.nchunks + c);
+    }
+    for (int k = 0; k < a.choices; ++k) {
+      const int64_t at = (g * a.tokens + t) * a.choices + k;
+      int64_t row = live ? a.row_of[at] : -1;
+      if (row >= a.rows) row = -1;
+      const float w = row >= 0 && a.gates ? a.gates[at] : 1.0f;
+      float dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int c = tt + i * tpr;
+        if (row >= 0 && c < a.nchunks) {
+          float f[kChunk], o[kChunk];
+          d[i].get(o);
+          if (a.dgates) {
+            sum_ranks<T, NR>(in, a.nranks, row * a.nchunks + c, f);
+#pragma unroll
+            for (int j = 0; j < kChunk; ++j) dot = fmaf(f[j], o[j], dot);
+          }
+#pragma unroll
+          for (int j = 0; j < kChunk; ++j) o[j] *= w;
+          Chunk<T> ov;
+          ov.put(o);
+          for (int q = 0; q < nout; ++q) ov.store(a.t.out[slot0 + q], row * a.nchunks + c);
+        }
+      }
+      if (a.dgates) {
+        dot = row_sum<false>(dot, tpr, slot, red, turn);
+        turn ^= 1;
+        if (live && tt == 0) a.dgates[at] = dot;
+      }
+    }
+  }
+}
+
+// --------------------------------------------------------------- launchers
+
+int blocks_for(int64_t items) {
+  const int64_t want = (items + kThreads - 1) / kThreads, most = 1 << 30;
+  return static_cast<int>(want < most ? want : most);
+}
+
+template <typename T, int NR, bool SUMMED>
+cudaError_t combine_go(const CombineArgs& a, int ngroups, cudaStream_t s) {
+  const dim3 grid(blocks_for(a.tokens * a.nchunks), SUMMED ? ngroups : ngroups * a.nranks);
+  k_expert_combine<T, NR, SUMMED><<<grid, kThreads, 0, s>>>(a);
+  count_launch();
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t combine_ranks(const CombineArgs& a, bool summed, int ngroups, cudaStream_t s) {
+  if (!summed) return combine_go<T, 1, false>(a, ngroups, s);
+  switch (a.nranks) {
+    case 1: return combine_go<T, 1, true>(a, ngroups, s);
+    case 8: return combine_go<T, 8, true>(a, ngroups, s);
+    default: return combine_go<T, 0, true>(a, ngroups, s);
+  }
+}
+
+template <typename T, int NR>
+cudaError_t combine_bwd_vpt(const CombineBwdArgs& a, const RowShape& r, dim3 grid, cudaStream_t s) {
+  switch (r.vpt) {
+    case 1: k_expert_combine_backward<T, NR, 1><<<grid, r.threads, 0, s>>>(a); break;
+    case 2: k_expert_combine_backward<T, NR, 2><<<grid, r.threads, 0, s>>>(a); break;
+    case 4: k_expert_combine_backward<T, NR, 4><<<grid, r.threads, 0, s>>>(a); break;
+    default: k_expert_combine_backward<T, NR, 8><<<grid, r.threads, 0, s>>>(a); break;
+  }
+  count_launch();
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t combine_bwd_ranks(const CombineBwdArgs& a, const RowShape& r, dim3 grid, cudaStream_t s) {
+  switch (a.nranks) {
+    case 1: return combine_bwd_vpt<T, 1>(a, r, grid, s);
+    case 8: return combine_bwd_vpt<T, 8>(a, r, grid, s);
+    default: return combine_bwd_vpt<T, 0>(a, r, grid, s);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_expert_sort(const ExpertSortLaunch& L, cudaStream_t s) {
+  SortArgs a;
+  a.expert_of = L.expert_of;
+  a.row_of = L.row_of;
+  a.choice_of = L.choice_of;
+  a.offsets = L.offsets;
+  a.n = L.n;
+  a.experts = L.experts;
+  a.nranks = L.nranks;
+  a.tile = L.experts < kSortTile ? (L.experts > 0 ? L.experts : 1) : kSortTile;
+  const int most = kSortSmem / (4 * a.tile) - 2;
+  a.warps = most < kSortWarps ? most : kSortWarps;
+  const int ctas = L.n <= 4 * kSortThreads ? 1 : 8;
+  a.seg = (L.n + ctas * a.warps - 1) / (ctas * a.warps);
+  a.seg = (a.seg + 31) / 32 * 32;
+  const void* fn = L.index64 ? reinterpret_cast<const void*>(&k_expert_sort<int64_t>)
+                             : reinterpret_cast<const void*>(&k_expert_sort<int32_t>);
+  // (the leave for dynamic shared memory is the process's: once per device and kernel, for the most that comes here)
+  static std::atomic<bool> leave[2][64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool kept = dev >= 0 && dev < 64;
+  if (!kept || !leave[L.index64][dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
+    if (e != cudaSuccess) return e;
+    if (kept) leave[L.index64][dev].store(true, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, L.ngroups);
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(a.warps + 2) * a.tile * 4;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = L.index64 ? cudaLaunchKernelEx(&cfg, k_expert_sort<int64_t>, a) : cudaLaunchKernelEx(&cfg, k_expert_sort<int32_t>, a);
+  count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_expert_dispatch(const ExpertRowsLaunch& L, cudaStream_t s) {
+  DispatchArgs a;
+  a.t = L.t;
+  a.row_of = L.row_of;
+  a.tokens = L.tokens;
+  a.rows = L.rows;
+  a.choices = L.choices;
+  a.nranks = L.nranks;
+  a.nvec = static_cast<int32_t>(static_cast<int64_t>(L.cols) * dtype_size(L.dtype) / 16);
+  a.nscales = L.dtype == COCO_F8E4M3 ? static_cast<int32_t>((static_cast<int64_t>(L.cols) + 127) / 128) : 0;
+  const dim3 grid(blocks_for(a.tokens * (static_cast<int64_t>(a.nvec) + a.nscales)), L.ngroups);
+  k_expert_dispatch<<<grid, kThreads, 0, s>>>(a);
+  count_launch();
+  return cudaGetLastError();
+}
+
+cudaError_t launch_expert_combine(const ExpertRowsLaunch& L, cudaStream_t s) {
+  CombineArgs a;
+  a.t = L.t;
+  a.row_of = L.row_of;
+  a.gates = L.gates;
+  a.tokens = L.tokens;
+  a.rows = L.rows;
+  a.choices = L.choices;
+  a.nranks = L.nranks;
+  a.nchunks = L.cols / kChunk;
+  switch (L.dtype) {
+    case COCO_F32: return combine_ranks<float>(a, L.summed, L.ngroups, s);
+    case COCO_F16: return combine_ranks<__half>(a, L.summed, L.ngroups, s);
+    default: return combine_ranks<__nv_bfloat16>(a, L.summed, L.ngroups, s);
+  }
+}
+
+cudaError_t launch_expert_combine_backward(const ExpertRowsLaunch& L, cudaStream_t s) {
+  CombineBwdArgs a;
+  a.t = L.t;
+  a.row_of = L.row_of;
+  a.gates = L.gates;
+  a.dgates = L.dgates;
+  a.tokens = L.tokens;
+  a.rows = L.rows;
+  a.choices = L.choices;
+  a.nranks = L.nranks;
+  a.nchunks = L.cols / kChunk;
+  const RowShape r = row_shape(a.nchunks);
+  a.tpr_log2 = r.tpr_log2;
+  const int64_t blocks = (L.tokens + r.rpb - 1) / r.rpb;
+  const dim3 grid(static_cast<unsigned>(blocks < (1 << 30) ? blocks : (1 << 30)), L.ngroups);
+  switch (L.dtype) {
+    case COCO_F32: return combine_bwd_ranks<float>(a, r, grid, s);
+    case COCO_F16: return combine_bwd_ranks<__half>(a, r, grid, s);
+    default: return combine_bwd_ranks<__nv_bfloat16>(a, r, grid, s);
+  }
+}
+
+}  // namespace coco

@@ -122,6 +122,87 @@ struct QuantLaunch {
 };
 cudaError_t launch_quantize_fp8(const QuantLaunch& L, cudaStream_t s);
 
+// ------------------------------------------- layer norm and its gradient
+
+struct LayerNormLaunch {
+  NormTables t;
+  int dtype;
+  bool fp8;  // normed is e4m3 with scales
+  int nranks, ngroups;
+  int64_t rows;
+  int32_t cols;
+  float eps;
+  const void* weight;
+  const void* bias;  // or nullptr
+  float* mean;       // [ngroups][rows], or nullptr
+  float* rstd;       // [ngroups][rows], or nullptr
+};
+cudaError_t launch_allreduce_layernorm(const LayerNormLaunch& L, cudaStream_t s);
+
+struct LayerNormBwdLaunch {
+  NormBwdLaunch n;    // n.partial: norm_backward_parts(ngroups * rows) times two rows of cols
+  const float* mean;  // [ngroups][rows]
+  float* dbias;       // or nullptr
+};
+cudaError_t launch_layernorm_backward(const LayerNormBwdLaunch& L, cudaStream_t s);
+
+// --------------------------------------------- tokens to their experts and back
+
+struct ExpertSortLaunch {
+  const void* expert_of;  // [ngroups][n]
+  bool index64;
+  int64_t n;  // choices of a group
+  int experts, nranks, ngroups;
+  int32_t* row_of;     // [ngroups][n]
+  int32_t* choice_of;  // [ngroups][n], or nullptr
+  int32_t* offsets;    // [ngroups * nranks][experts + 1]
+};
+cudaError_t launch_expert_sort(const ExpertSortLaunch& L, cudaStream_t s);
+
+// Pointer tables of one launch, group-major like ReduceTables. Operands that ranks share have one pointer per group at
+// [g], the others one per rank; group g's distinct outputs are out[g*nranks + j], j < nout[g] (or one per rank).
+struct ExpertTables {
+  const void* in[COCO_MAX_PTRS];
+  const float* in_scales[COCO_MAX_PTRS];
+  const void* residual[COCO_MAX_PTRS];  // per group
+  void* out[COCO_MAX_PTRS];
+  float* out_scales[COCO_MAX_PTRS];
+  int32_t nout[COCO_MAX_PTRS];
+};
+
+struct ExpertRowsLaunch {
+  ExpertTables t;
+  int dtype;
+  bool summed;  // combine: over the ranks
+  int nranks, ngroups;
+  int64_t tokens, rows;
+  int32_t choices, cols;
+  const int32_t* row_of;  // [ngroups][tokens][choices]
+  const float* gates;     // the same shape, or nullptr (ones)
+  float* dgates;          // combine backward: the same shape, or nullptr
+};
+cudaError_t launch_expert_dispatch(const ExpertRowsLaunch& L, cudaStream_t s);  // in, in_scales: per group
+cudaError_t launch_expert_combine(const ExpertRowsLaunch& L, cudaStream_t s);   // in: per rank
+cudaError_t launch_expert_combine_backward(const ExpertRowsLaunch& L, cudaStream_t s);  // residual: dout
+
+// ------------------------------------------------ clipping scattered gradients
+
+// CLIP_LOCAL: the ranks' tensors are parts of one gradient; CLIP_REPLICATED: copies of it; CLIP_SUM: its summands.
+enum ClipMode { CLIP_LOCAL = 0, CLIP_REPLICATED = 1, CLIP_SUM = 2 };
+
+struct ClipLaunch {
+  const void* table;
+  const void* out_table;  // the same pointer in place
+  int64_t nbuckets;
+  int mode, nranks, out_nranks;
+  int dtype, out_dtype;
+  float alpha, max_norm;
+  float* norm;
+  double* parts;  // kClipMaxParts
+};
+constexpr int kClipMaxParts = 1024;
+cudaError_t launch_scattered_clip(const ClipLaunch& L, cudaStream_t s);
+
 // ---------------------------------------------------------------- GEMM plans
 
 // A dense row-major [nb][rows][cols] operand (elements).

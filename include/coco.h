@@ -89,8 +89,8 @@ typedef enum {
 } coco_status;
 
 /* COCO_F8E4M3 (4 exponent bits, 3 fraction bits, largest value 448, no infinity) is taken by the entry points
- * of the section on 8-bit and expert-grouped operators only; its innermost per-rank dimension is a multiple
- * of 16 elements. Elsewhere it is COCO_ERR_DTYPE. */
+ * of the section on 8-bit and expert-grouped operators and by coco_expert_dispatch and coco_allreduce_layernorm
+ * only; its innermost per-rank dimension is a multiple of 16 elements. Elsewhere it is COCO_ERR_DTYPE. */
 typedef enum { COCO_F32 = 0, COCO_F16 = 1, COCO_BF16 = 2, COCO_F8E4M3 = 3 } coco_dtype;
 
 typedef enum { COCO_LOCAL = 0, COCO_SLICED = 1, COCO_REPLICATED = 2 } coco_layout;
@@ -539,6 +539,153 @@ coco_status coco_einsum_fp8(const char* spec, const coco_tensor* lhs, const floa
 coco_status coco_grouped_einsum(const char* spec, const coco_tensor* lhs, const float* const* lhs_scales,
                                 const coco_tensor* rhs, const float* const* rhs_scales, const int32_t* offsets,
                                 const coco_tensor* out, void* stream);
+
+/* ------------------------- experts' rows, layer norm, gradient clipping */
+
+/*
+ * Rows sorted by expert, as coco_grouped_einsum takes them. A routing is one per group (the ranks of a group hold the
+ * same tokens): expert_of[g][t][k] is the expert of token t's k-th choice. Choice i = t * choices + k has the row
+ *
+ *   row_of_choice[g][i] = #{j : expert_of[j] < expert_of[i]} + #{j < i : expert_of[j] == expert_of[i]}
+ *
+ * (counting choices of experts only), so an expert's rows keep the choices' order. A choice whose number is outside
+ * [0, experts) has no row (a dropped or padding token): its entry is -1. A token may name an expert twice.
+ *
+ *   expert_of      device pointer to [ngroups, tokens, choices] int32 (index_bytes 4) or int64 (8), aligned to its elements.
+ *   row_of_choice  device pointer to [ngroups, tokens, choices] int32.
+ *   choice_of_row  device pointer to [ngroups, tokens * choices] int32, or NULL: the choice of every row (its token is
+ *                  choice_of_row / choices), -1 behind the last expert's rows.
+ *   offsets        device pointer to [ngroups * nranks, experts + 1] int32: a line per rank, those of a group alike.
+ * tokens * choices < 2^31 and experts <= 65536, else COCO_ERR_UNSUPPORTED; index_bytes other than 4 and 8: COCO_ERR_DTYPE.
+ * No output may overlap another array. Without tokens or choices the offsets are zeros.
+ */
+coco_status coco_expert_sort(const void* expert_of, int32_t index_bytes, int64_t tokens, int32_t choices,
+                             int32_t experts, int32_t ngroups, int32_t nranks, int32_t* row_of_choice,
+                             int32_t* choice_of_row, int32_t* offsets, void* stream);
+
+/*
+ * Tokens to their experts' rows: rows[row_of_choice[t][k]] = x[t], bit for bit.
+ *   x              REPLICATED [tokens, cols] in F32, F16, BF16, or F8E4M3 with x_scales [tokens, ceil(cols/128)] (one
+ *                  device pointer per rank, of which a group's first is read; else NULL).
+ *   row_of_choice  as coco_expert_sort writes it; choices = (rows of `rows`) / tokens, which has to divide. A value outside
+ *                  [0, rows) is a choice without a row. No two choices of a group may name one row.
+ *   rows           REPLICATED [tokens * choices, cols], x's type, with row_scales (one pointer per rank) where it has
+ *                  scales; replicas (and scales) of one group may be one buffer.
+ * Rows (and scales) that no choice names are left as they were; the grouped products do not read them. The gradient
+ * with respect to x is coco_expert_combine without gates.
+ */
+coco_status coco_expert_dispatch(const coco_tensor* x, const float* const* x_scales, const int32_t* row_of_choice,
+                                 const coco_tensor* rows, float* const* row_scales, void* stream);
+
+/*
+ * The experts' rows back to their tokens. With out LOCAL (every rank's own sum; residual NULL) and with out REPLICATED
+ * (the AllReduce of those sums, never written, and the residual):
+ *
+ *   out_r[t] = sum_k gates[t][k] * rows_r[row_of_choice[t][k]]
+ *   out[t]   = sum_k gates[t][k] * (sum_r rows_r[row_of_choice[t][k]]) + residual[t]
+ *
+ * in fp32 (ranks in order, then choices in order, then the residual) with one rounding. A choice without a row adds
+ * nothing, whatever its gate is.
+ *   rows           LOCAL [tokens * choices, cols], T in {F32, F16, BF16}.
+ *   row_of_choice  [ngroups, tokens, choices] as above (several choices may name one row here).
+ *   gates          device pointer to [ngroups, tokens, choices] fp32, or NULL (ones).
+ *   residual       REPLICATED [tokens, cols], T, or NULL.
+ *   out            LOCAL or REPLICATED [tokens, cols], T. A REPLICATED one may take the residual's place in its own group
+ *                  exactly, and replicas of one group may be one buffer; other overlaps are COCO_ERR_ALIAS.
+ */
+coco_status coco_expert_combine(const coco_tensor* rows, const int32_t* row_of_choice, const float* gates,
+                                const coco_tensor* residual, const coco_tensor* out, void* stream);
+
+/*
+ * The gradient of coco_expert_combine for the gradient `dout` of its (summed) output:
+ *
+ *   drows[row_of_choice[t][k]] = gates[t][k] * dout[t]
+ *   dgates[t][k]               = sum over ranks r and columns of dout[t] * rows_r[row_of_choice[t][k]]
+ *
+ * The first is the same for every rank; the residual's gradient is dout itself. The products' sum is fp32 in a fixed
+ * order; dgates is 0 for a choice without a row, and rows that no choice names are left as they were. No two choices of a
+ * group may name one row.
+ *   dout   REPLICATED [tokens, cols], T; cols at most 32768, else COCO_ERR_UNSUPPORTED.
+ *   rows   LOCAL [tokens * choices, cols], T, as the forward read them, or NULL with dgates NULL (gates without a gradient).
+ *   gates  as the forward's, or NULL (ones).    drows  REPLICATED [tokens * choices, cols], T.
+ *   dgates device pointer to [ngroups, tokens, choices] fp32, or NULL with rows NULL.
+ * No output may overlap another array; replicas of one group may be one buffer.
+ */
+coco_status coco_expert_combine_backward(const coco_tensor* dout, const coco_tensor* rows, const int32_t* row_of_choice,
+                                         const float* gates, const coco_tensor* drows, float* dgates, void* stream);
+
+/*
+ * AllReduce, the residual's addition and the layer norm (Ba, Kiros and Hinton 2016) in one pass:
+ *
+ *   h = sum_{r=0}^{N-1} partials_r + residual,  m = mean(h),  v = mean((h - m)^2)
+ *   y = (h - m) / sqrt(v + eps) * weight + bias
+ *
+ * over the last dimension. Arguments, limits and aliases as coco_allreduce_rmsnorm's; besides them
+ *   bias  device pointer to one row of T, or NULL.
+ *   mean  device pointer to [ngroups, rows] fp32: receives m, or NULL; rstd receives 1 / sqrt(v + eps), or NULL.
+ * The variance is summed about the mean, from the unrounded h: a mean far from zero costs it nothing.
+ */
+coco_status coco_allreduce_layernorm(const coco_tensor* partials, const coco_tensor* residual, const void* weight,
+                                     const void* bias, float eps, const coco_tensor* hidden, const coco_tensor* normed,
+                                     float* const* scales, float* mean, float* rstd, void* stream);
+
+/*
+ * The gradient of coco_allreduce_layernorm, in the manner of coco_allreduce_rmsnorm_backward:
+ *
+ *   dy = sum_r dnormed_r,  xhat = (hidden - mean) * rstd,  g = dy * weight
+ *   dx = rstd * (g - mean(g) - xhat * mean(g * xhat)) + dhidden
+ *   dweight = sum over all rows (of all groups) of dy * xhat,   dbias = sum over all rows of dy
+ *
+ *   mean, rstd  [ngroups, rows] fp32, as the forward wrote them.    dbias  device pointer to one row of fp32, or NULL.
+ *   workspace   at least coco_allreduce_layernorm_backward_bytes(ngroups * rows, cols) bytes.
+ * All sums are fp32 in a fixed order: repeated calls on one device give the same bits.
+ */
+coco_status coco_allreduce_layernorm_backward(const coco_tensor* dnormed, const coco_tensor* dhidden,
+                                              const coco_tensor* hidden, const void* weight, const float* mean,
+                                              const float* rstd, const coco_tensor* dx, float* dweight, float* dbias,
+                                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace for `rows` rows in all groups together (0 for sizes out of range). Host only. */
+size_t coco_allreduce_layernorm_backward_bytes(int64_t rows, int64_t cols);
+
+/*
+ * Clipping by the global norm, over the tensors of a scattered plan (a model's gradients):
+ *
+ *   norm = sqrt(sum of x^2 over all tensors),   out = x * (norm <= max_norm ? 1 : max_norm / norm)
+ *
+ *   plan      the tensors' plan. layout COCO_LOCAL: the ranks' tensors are parts of one gradient (a tensor-parallel
+ *             model's slices), all of them enter the norm and each is scaled; COCO_REPLICATED: they are copies of one, of
+ *             which rank 0's is read. Other layouts: COCO_ERR_LAYOUT.
+ *   max_norm  >= 0, else COCO_ERR_VALUE; INFINITY only takes the norm (in place, nothing is written).
+ *   out       the plan of the tensors that receive the result, of the same sizes in the same order, in any type (fp32
+ *             gradients for the optimizer from 16-bit ones), or NULL: in place. COCO_LOCAL: as many ranks as `plan`;
+ *             COCO_REPLICATED: each of its ranks receives a copy. `out` may be `plan` itself; its tensors may otherwise
+ *             not overlap plan's (the library does not see them: only the tables do). Where the two tables hold
+ *             tensors of other sizes, buckets that differ are left alone and the norm is NaN.
+ *   norm      device pointer to one fp32: receives the norm before clipping.
+ *   workspace coco_scattered_clip_bytes() bytes of device memory (fewer: COCO_ERR_SHAPE), 16-byte aligned; its contents
+ *             before and after do not matter. Calls that may run at the same time need one each.
+ * Squares are summed in fp32 per lane and bucket (fp64 where they leave its range), beyond that in fp64, in a fixed order:
+ * repeated calls on one device give the same bits. The product is rounded once to out's type. In place with a factor of
+ * 1, nothing is written. A norm that is NaN makes every value NaN; an infinite one makes finite values zero and
+ * infinities NaN.
+ */
+coco_status coco_scattered_clip(const coco_scattered_plan* plan, int32_t layout, float max_norm,
+                                const coco_scattered_plan* out, float* norm, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/*
+ * coco_scattered_allreduce with the clipping fused in: x = alpha * sum_q tensor_q (fp32, rank order 0..N-1, rounded to
+ * out's type), whose norm and clipped values are taken as above; the sum's pass over memory gives its norm. `out` (NULL: in
+ * place on every rank of `plan`) may have any number of ranks, each of which receives a copy. Everything else as
+ * coco_scattered_clip; with max_norm INFINITY and out NULL the tensors receive what coco_scattered_allreduce writes.
+ */
+coco_status coco_scattered_allreduce_clip(const coco_scattered_plan* plan, float alpha, float max_norm,
+                                          const coco_scattered_plan* out, float* norm, void* workspace,
+                                          size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that clipping takes, whatever the plan. Host only. */
+size_t coco_scattered_clip_bytes(void);
 
 /* ------------------------------------------------------------- utilities */
 
