@@ -26,7 +26,8 @@ Every function states the passage it follows. Where the pages are silent the
 docstring says which reading was taken and why.
 
 Pins: each public function is checked in ``tests/test_oracle_pins.py`` (the
-8-bit and expert-grouped ones in ``tests/test_oracle_llm_pins.py``) against
+language-model layers' in ``tests/test_oracle_llm_pins.py`` and
+``tests/test_oracle_layers_pins.py``) against
 facts the pages or mathematics fix (brute force, closed forms, identities the
 pages state, published hash test vectors). No function here is unpinned.
 """
@@ -70,6 +71,13 @@ from .llm import (
     grouped_einsum,
     moe_layer,
     moe_layer_backward,
+    expert_sort,
+    expert_dispatch,
+    expert_combine,
+    expert_combine_backward,
+    allreduce_layernorm,
+    allreduce_layernorm_backward,
+    clip,
 )
 from .scattered import (
     buckets as scattered_buckets,
@@ -102,4 +110,6 @@ __all__ = [
     "e4m3_table", "to_e4m3", "block_amax", "scales_of", "spread", "quantize", "dequantize",
     "allreduce_rmsnorm", "allreduce_rmsnorm_backward", "grouped_einsum",
     "moe_layer", "moe_layer_backward",
+    "expert_sort", "expert_dispatch", "expert_combine", "expert_combine_backward",
+    "allreduce_layernorm", "allreduce_layernorm_backward", "clip",
 ]

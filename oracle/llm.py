@@ -1,8 +1,10 @@
-"""8-bit and expert-grouped operators, in float64 NumPy (test infrastructure only).
+"""Operators of a language model's layers, in float64 NumPy (test infrastructure only).
 
 The pages have none of these; the definitions are the published ones: the
 root-mean-square norm of Zhang and Sennrich ("Root Mean Square Layer
-Normalization", 2019), the e4m3 format of the OCP "8-bit Floating Point
+Normalization", 2019), the layer norm of Ba, Kiros and Hinton ("Layer
+Normalization", 2016), clipping by the global norm of Pascanu, Mikolov and Bengio
+("On the difficulty of training recurrent neural networks", 2013), the e4m3 format of the OCP "8-bit Floating Point
 Specification" (four exponent bits of bias 7, three fraction bits, largest value
 448, no infinity, code 0x7f for NaN), and products of block-scaled values and
 of expert-sorted rows written out as sums.
@@ -134,3 +136,73 @@ def moe_layer_backward(partials, residual, weight, eps, expert_of, up, down, dou
                 dx[t] += u[e] @ dmid
     dh, dw = allreduce_rmsnorm_backward([dx], dout, h, rstd, weight)
     return dh, dw, dup, ddown
+
+
+def expert_sort(expert_of, experts):
+    """(row of every choice, choice of every row, offsets) of a routing [tokens, choices]: choice by choice, a loop."""
+    flat = [int(e) for e in np.asarray(expert_of).reshape(-1)]
+    offsets = np.zeros(experts + 1, np.int64)
+    for e in flat:
+        if 0 <= e < experts:
+            offsets[e + 1:] += 1
+    placed = np.zeros(experts, np.int64)
+    row_of, choice_of = np.full(len(flat), -1), np.full(len(flat), -1)
+    for i, e in enumerate(flat):
+        if 0 <= e < experts:
+            row_of[i] = offsets[e] + placed[e]
+            choice_of[row_of[i]] = i
+            placed[e] += 1
+    return row_of.reshape(np.shape(expert_of)), choice_of, offsets
+
+
+def expert_dispatch(x, row_of, rows):
+    """`rows` with x[t] written to the row of every choice of token t."""
+    out = np.array(rows)
+    for t, k in np.argwhere((row_of >= 0) & (row_of < len(out))):
+        out[row_of[t, k]] = x[t]
+    return out
+
+
+def expert_combine(rows, row_of, gates, residual):
+    """Sum over a token's choices of gate * row, rows summed over the ranks (a list); gates None for ones."""
+    total = sum(rows)
+    out = np.zeros((row_of.shape[0], total.shape[1])) + (0.0 if residual is None else residual)
+    for t, k in np.argwhere((row_of >= 0) & (row_of < len(total))):
+        out[t] += (1.0 if gates is None else gates[t, k]) * total[row_of[t, k]]
+    return out
+
+
+def expert_combine_backward(dout, rows, row_of, gates, drows):
+    """(`drows` with the rows' gradients written, the gates' gradients)."""
+    total, drows, dgates = sum(rows), np.array(drows), np.zeros(row_of.shape)
+    for t, k in np.argwhere((row_of >= 0) & (row_of < len(total))):
+        drows[row_of[t, k]] = (1.0 if gates is None else gates[t, k]) * dout[t]
+        dgates[t, k] = np.dot(dout[t], total[row_of[t, k]])
+    return drows, dgates
+
+
+def allreduce_layernorm(partials, residual, weight, bias, eps):
+    """(h, y, mean, 1 / standard deviation) over the last dimension."""
+    h = sum(partials) + (0.0 if residual is None else residual)
+    mean = np.mean(h, -1)
+    centred = h - mean[..., None]
+    rstd = 1.0 / np.sqrt(np.mean(centred * centred, -1) + eps)
+    return h, centred * rstd[..., None] * weight + (0.0 if bias is None else bias), mean, rstd
+
+
+def allreduce_layernorm_backward(dnormed, dhidden, h, mean, rstd, weight):
+    """(gradient of h, of the weight, of the bias) for sum(y * sum(dnormed)) + sum(h * dhidden)."""
+    dy = sum(dnormed)
+    xhat = (h - mean[..., None]) * rstd[..., None]
+    g = dy * weight
+    dh = rstd[..., None] * (g - np.mean(g, -1, keepdims=True) - xhat * np.mean(g * xhat, -1, keepdims=True))
+    cols = h.shape[-1]
+    return (dh + (0.0 if dhidden is None else dhidden), (dy * xhat).reshape(-1, cols).sum(0),
+            dy.reshape(-1, cols).sum(0))
+
+
+def clip(tensors, max_norm):
+    """(the tensors scaled so that their norm is at most max_norm, the norm before)."""
+    norm = np.sqrt(sum(np.sum(np.square(t)) for t in tensors))
+    factor = 1.0 if norm <= max_norm else max_norm / norm
+    return [t * factor for t in tensors], norm
