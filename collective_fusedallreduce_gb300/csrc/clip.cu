@@ -36,71 +36,73 @@ struct ClipArgs {
   int32_t nparts;
 };
 
-// One rank's part of a bucket.
+// The entries of ranks r0 .. r0 + n - 1 (three words each, n at most 10) of bucket b, a word a lane: one load brings all.
+__device__ __forceinline__ uint32_t entry_words(const uint32_t* table, int64_t b, int nranks, int r0, int n) {
+  const int lane = threadIdx.x & 31;
+  return lane < 3 * n ? __ldg(table + kHeaderWords + (b * nranks + r0) * 3 + lane) : 0u;
+}
+
+// A rank's part of a bucket: the j-th entry of a warp's words.
 struct Bucket {
   char* base;  // its first element
   int32_t len;
-  uint32_t code;
 };
 
+__device__ __forceinline__ uint32_t code_of(uint32_t words) { return __shfl_sync(0xffffffffu, words, 2); }
+
 template <typename T>
-__device__ __forceinline__ Bucket bucket_at(const uint32_t* table, int64_t b, int nranks, int rank) {
-  const uint32_t* e = table + kHeaderWords + (b * nranks + rank) * 3;
+__device__ __forceinline__ Bucket bucket_of(uint32_t words, int j) {
+  const uint32_t lo = __shfl_sync(0xffffffffu, words, 3 * j), hi = __shfl_sync(0xffffffffu, words, 3 * j + 1);
+  const uint32_t code = code_of(words);  // the same bucket and length for every rank
   Bucket r;
-  r.code = e[2];
-  r.len = static_cast<int>(r.code & 1023u) + 1;
-  r.base = reinterpret_cast<char*>((static_cast<uint64_t>(e[1]) << 32) | e[0]) +
-           static_cast<int64_t>(r.code >> 10) * 1024 * sizeof(T);
+  r.base = reinterpret_cast<char*>((static_cast<uint64_t>(hi) << 32) | lo) +
+           static_cast<int64_t>(code >> 10) * 1024 * sizeof(T);
+  r.len = static_cast<int>(code & 1023u) + 1;
   return r;
 }
 
-// The elements of a lane's chunk c of a bucket; past its end zeros.
+// A lane's chunk c of a bucket that ends inside it or before it: its elements, and zeros past them. (Plain loads: it may
+// have been written by this thread.)
 template <typename T>
-__device__ __forceinline__ void load_part(const Bucket& b, int c, float (&f)[kChunk]) {
-  if ((c + 1) * kChunk <= b.len) {
-    Chunk<T> v;
-    v.load(b.base, c);
-    v.get(f);
-  } else {
+__device__ __forceinline__ void load_end(const Bucket& b, int c, float (&f)[kChunk]) {
 #pragma unroll
-    for (int j = 0; j < kChunk; ++j)
-      f[j] = c * kChunk + j < b.len ? static_cast<float>(reinterpret_cast<const T*>(b.base)[c * kChunk + j]) : 0.0f;
-  }
+  for (int j = 0; j < kChunk; ++j)
+    f[j] = c * kChunk + j < b.len ? static_cast<float>(reinterpret_cast<const T*>(b.base)[c * kChunk + j]) : 0.0f;
 }
 
 template <typename T>
-__device__ __forceinline__ void store_part(const Bucket& b, int c, const float (&f)[kChunk]) {
-  if ((c + 1) * kChunk <= b.len) {
-    Chunk<T> v;
-    v.put(f);
-    *reinterpret_cast<Chunk<T>*>(b.base + c * kChunk * sizeof(T)) = v;  // (not a streaming store: it is read again)
-  } else {
+__device__ __forceinline__ void store_end(const Bucket& b, int c, const float (&f)[kChunk]) {
 #pragma unroll
-    for (int j = 0; j < kChunk; ++j)
-      if (c * kChunk + j < b.len) reinterpret_cast<T*>(b.base)[c * kChunk + j] = static_cast<T>(f[j]);
-  }
+  for (int j = 0; j < kChunk; ++j)
+    if (c * kChunk + j < b.len) reinterpret_cast<T*>(b.base)[c * kChunk + j] = static_cast<T>(f[j]);
 }
 
-// The squares' sum of a lane's part of a bucket: in fp32, and again in fp64 where that has left fp32's range (past its
-// largest number, or so low that squares were lost).
-__device__ __forceinline__ double squares(const float (&f)[kBucketChunks][kChunk]) {
-  float s = 0.0f;
+template <typename T>
+__device__ __forceinline__ void store_full(const Bucket& b, int c, const float (&f)[kChunk]) {
+  Chunk<T> v;
+  v.put(f);
+  *reinterpret_cast<Chunk<T>*>(b.base + c * kChunk * sizeof(T)) = v;  // (not a streaming store: it is read again)
+}
+
+__device__ __forceinline__ float add_squares(const float (&f)[kChunk], float s) {
 #pragma unroll
-  for (int i = 0; i < kBucketChunks; ++i)
-#pragma unroll
-    for (int j = 0; j < kChunk; ++j) s = fmaf(f[i][j], f[i][j], s);
+  for (int j = 0; j < kChunk; ++j) s = fmaf(f[j], f[j], s);
+  return s;
+}
+
+// The squares' sum of a lane's part of a bucket, s in fp32; taken again in fp64 where that has left fp32's range (past
+// its largest number, or so low that squares were lost).
+template <typename T>
+__device__ __forceinline__ double squares(const Bucket& b, float s) {
   if (s >= 0x1p-80f && s <= FLT_MAX) return s;
-  bool any = s != 0.0f;
-#pragma unroll
-  for (int i = 0; i < kBucketChunks; ++i)
-#pragma unroll
-    for (int j = 0; j < kChunk; ++j) any |= f[i][j] != 0.0f;
   double d = 0.0;
-  if (any) {
+#pragma unroll 1
+  for (int c = threadIdx.x & 31; c * kChunk < b.len; c += 32) {
+    float f[kChunk];
+    load_end<T>(b, c, f);
 #pragma unroll
-    for (int i = 0; i < kBucketChunks; ++i)
-#pragma unroll
-      for (int j = 0; j < kChunk; ++j) d = fma(static_cast<double>(f[i][j]), static_cast<double>(f[i][j]), d);
+    for (int j = 0; j < kChunk; ++j)
+      if (f[j] != 0.0f) d = fma(static_cast<double>(f[j]), static_cast<double>(f[j]), d);
   }
   return d;
 }
@@ -116,67 +118,176 @@ __device__ __forceinline__ double block_sum(double v, double* red) {
   return v;
 }
 
-// Whether the tensors of the two tables have bucket b in common. Where they do not, nothing is written and the norm is NaN.
-template <typename T, typename U>
-__device__ __forceinline__ bool same_bucket(const ClipArgs& a, int64_t b) {
-  return a.table == a.out_table ||
-         bucket_at<T>(a.table, b, a.nranks, 0).code == bucket_at<U>(a.out_table, b, a.out_nranks, 0).code;
-}
-
-// Warps take buckets round-robin (those of every rank with CLIP_LOCAL). With CLIP_SUM the ranks' tensors are added in
-// rank order, scaled by alpha, rounded to U and stored to out's rank 0, and it is those values' norm.
-template <typename T, typename U, int MODE>
-__global__ void __launch_bounds__(kThreads) k_clip_squares(const __grid_constant__ ClipArgs a) {
-  __shared__ double red[kWarps];
+// A whole bucket's squares. With CLIP_SUM a chunk is the sum over the ranks (NR of them, or any number four at a time).
+template <typename T, typename U, int MODE, int NR>
+__device__ __forceinline__ double squares_full(const ClipArgs& a, int64_t b, uint32_t words, uint32_t out_words) {
   const int lane = threadIdx.x & 31;
-  const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
-  const int64_t nwarps = static_cast<int64_t>(gridDim.x) * kWarps;
-  const int64_t items = MODE == CLIP_LOCAL ? a.nbuckets * a.nranks : a.nbuckets;
-  double sum = 0.0;
-  for (int64_t it = warp; it < items; it += nwarps) {
-    const int64_t b = MODE == CLIP_LOCAL ? it / a.nranks : it;
-    if (!same_bucket<T, U>(a, b)) {
-      sum = __longlong_as_double(0x7ff8000000000000ll);
-      continue;
+  float s = 0.0f;
+  if constexpr (MODE != CLIP_SUM) {
+    const Bucket k = bucket_of<T>(words, 0);
+    Chunk<T> v[kBucketChunks];
+#pragma unroll
+    for (int i = 0; i < kBucketChunks; ++i) v[i].load(k.base, lane + 32 * i);
+#pragma unroll
+    for (int i = 0; i < kBucketChunks; ++i) {
+      float f[kChunk];
+      v[i].get(f);
+      s = add_squares(f, s);
     }
-    float f[kBucketChunks][kChunk];
-    if constexpr (MODE != CLIP_SUM) {
-      const Bucket k = bucket_at<T>(a.table, b, a.nranks, MODE == CLIP_LOCAL ? static_cast<int>(it - b * a.nranks) : 0);
+    return squares<T>(k, s);
+  } else {
+    const Bucket to = bucket_of<U>(out_words, 0);
+    const void* in[NR ? NR : 1];
+    if constexpr (NR > 0) {
 #pragma unroll
-      for (int i = 0; i < kBucketChunks; ++i) load_part<T>(k, lane + 32 * i, f[i]);
-    } else {
-      const Bucket to = bucket_at<U>(a.out_table, b, a.out_nranks, 0);
-      for (int r = 0; r < a.nranks; ++r) {
-        const Bucket k = bucket_at<T>(a.table, b, a.nranks, r);
+      for (int r = 0; r < NR; ++r) in[r] = bucket_of<T>(words, r).base;
+    }
 #pragma unroll
-        for (int i = 0; i < kBucketChunks; ++i) {
-          float v[kChunk];
-          load_part<T>(k, lane + 32 * i, v);
+    for (int i = 0; i < kBucketChunks; ++i) {
+      float f[kChunk];
+      if constexpr (NR > 0) {
+        sum_ranks<T, NR>(in, NR, lane + 32 * i, f);
+      } else {
 #pragma unroll
-          for (int j = 0; j < kChunk; ++j) f[i][j] = r ? f[i][j] + v[j] : v[j];
+        for (int j = 0; j < kChunk; ++j) f[j] = -0.0f;  // (added to anything, it leaves that as it is)
+        for (int r0 = 0; r0 < a.nranks; r0 += 4) {
+          const int n = a.nranks - r0 < 4 ? a.nranks - r0 : 4;
+          const uint32_t w = entry_words(a.table, b, a.nranks, r0, n);
+          Chunk<T> raw[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (r < n) raw[r].load(bucket_of<T>(w, r).base, lane + 32 * i);
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (r < n) {
+              float g[kChunk];
+              raw[r].get(g);
+#pragma unroll
+              for (int j = 0; j < kChunk; ++j) f[j] += g[j];
+            }
         }
       }
 #pragma unroll
-      for (int i = 0; i < kBucketChunks; ++i) {
-#pragma unroll
-        for (int j = 0; j < kChunk; ++j) f[i][j] = static_cast<float>(static_cast<U>(f[i][j] * a.alpha));
-        store_part<U>(to, lane + 32 * i, f[i]);
-      }
+      for (int j = 0; j < kChunk; ++j) f[j] = static_cast<float>(static_cast<U>(f[j] * a.alpha));
+      store_full<U>(to, lane + 32 * i, f);
+      s = add_squares(f, s);
     }
-    sum += squares(f);
+    return squares<U>(to, s);
+  }
+}
+
+// The same for the last bucket of a tensor, a chunk and a rank at a time.
+template <typename T, typename U, int MODE>
+__device__ __forceinline__ double squares_end(const ClipArgs& a, int64_t b, uint32_t words, uint32_t out_words) {
+  const Bucket k = bucket_of<T>(words, 0), to = bucket_of<U>(out_words, 0);
+  const int rounds = (k.len + 32 * kChunk - 1) / (32 * kChunk);
+  float s = 0.0f;
+#pragma unroll 1
+  for (int i = 0; i < rounds; ++i) {
+    const int c = (threadIdx.x & 31) + 32 * i;
+    float f[kChunk];
+    load_end<T>(k, c, f);
+    if constexpr (MODE == CLIP_SUM) {
+#pragma unroll 1
+      for (int r = 1; r < a.nranks; ++r) {
+        const Bucket kr = bucket_of<T>(entry_words(a.table, b, a.nranks, r, 1), 0);
+        float g[kChunk];
+        load_end<T>(kr, c, g);
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j) f[j] += g[j];
+      }
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j) f[j] = static_cast<float>(static_cast<U>(f[j] * a.alpha));
+      store_end<U>(to, c, f);
+    }
+    s = add_squares(f, s);
+  }
+  if constexpr (MODE == CLIP_SUM) return squares<U>(to, s);
+  else return squares<T>(k, s);
+}
+
+// Warps take buckets round-robin (those of every rank with CLIP_LOCAL), the next one's entries under way. With CLIP_SUM
+// the ranks' tensors are added in rank order, scaled by alpha, rounded to U and stored to out's rank 0, and it is those
+// values' norm. Where the two tables' tensors do not have a bucket in common, nothing is written and the norm is NaN.
+template <typename T, typename U, int MODE, int NR>
+__global__ void __launch_bounds__(kThreads, MODE == CLIP_SUM && NR == 8 ? 3 : 4)
+    k_clip_squares(const __grid_constant__ ClipArgs a) {
+  __shared__ double red[kWarps];
+  const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
+  const int64_t nwarps = static_cast<int64_t>(gridDim.x) * kWarps;
+  const int64_t items = MODE == CLIP_LOCAL ? a.nbuckets * a.nranks : a.nbuckets;
+  const bool two = a.table != a.out_table;
+  const int n = MODE == CLIP_SUM && NR > 0 ? NR : 1;
+  uint32_t words = 0, out_words = 0;
+  auto fetch = [&](int64_t it) {  // (CLIP_LOCAL counts the entries themselves)
+    words = MODE == CLIP_LOCAL ? entry_words(a.table, it, 1, 0, 1) : entry_words(a.table, it, a.nranks, 0, n);
+    if (two) out_words = MODE == CLIP_LOCAL ? entry_words(a.out_table, it, 1, 0, 1)
+                                            : entry_words(a.out_table, it, a.out_nranks, 0, 1);
+    else out_words = words;
+  };
+  double sum = 0.0;
+  if (warp < items) fetch(warp);
+  for (int64_t it = warp; it < items; it += nwarps) {
+    const uint32_t w = words, ow = out_words;
+    if (it + nwarps < items) fetch(it + nwarps);
+    const uint32_t code = code_of(w);
+    if (code != code_of(ow)) sum = __longlong_as_double(0x7ff8000000000000ll);
+    else if ((code & 1023u) == 1023u) sum += squares_full<T, U, MODE, NR>(a, it, w, ow);
+    else sum += squares_end<T, U, MODE>(a, it, w, ow);
   }
   sum = block_sum(sum, red);
   if (threadIdx.x == 0) a.parts[blockIdx.x] = sum;
+}
+
+template <typename X, typename U>
+__device__ __forceinline__ void scale_full(const ClipArgs& a, int64_t b, uint32_t words, uint32_t out_words, int first,
+                                           int last, float factor) {
+  const int lane = threadIdx.x & 31;
+  const Bucket from = bucket_of<X>(words, 0);
+  Chunk<X> v[kBucketChunks];
+#pragma unroll
+  for (int i = 0; i < kBucketChunks; ++i) v[i].load(from.base, lane + 32 * i);
+#pragma unroll 1
+  for (int r = first; r < last; ++r) {
+    const Bucket to = bucket_of<U>(r ? entry_words(a.out_table, b, a.out_nranks, r, 1) : out_words, 0);
+#pragma unroll
+    for (int i = 0; i < kBucketChunks; ++i) {
+      float f[kChunk];
+      v[i].get(f);
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j) f[j] *= factor;
+      Chunk<U> o;
+      o.put(f);
+      o.store(to.base, lane + 32 * i);
+    }
+  }
+}
+
+template <typename X, typename U>
+__device__ __forceinline__ void scale_end(const ClipArgs& a, int64_t b, uint32_t words, uint32_t out_words, int first,
+                                          int last, float factor) {
+  const Bucket from = bucket_of<X>(words, 0);
+  const int rounds = (from.len + 32 * kChunk - 1) / (32 * kChunk);
+#pragma unroll 1
+  for (int i = 0; i < rounds; ++i) {
+    const int c = (threadIdx.x & 31) + 32 * i;
+    float f[kChunk];
+    load_end<X>(from, c, f);
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j) f[j] *= factor;
+#pragma unroll 1
+    for (int r = first; r < last; ++r)
+      store_end<U>(bucket_of<U>(r ? entry_words(a.out_table, b, a.out_nranks, r, 1) : out_words, 0), c, f);
+  }
 }
 
 // Every block joins the sums of squares; block 0 writes the norm. Then out = x * factor, last buckets first; x is the
 // ranks' own tensor (CLIP_LOCAL), rank 0's (CLIP_REPLICATED), or out's rank 0 (CLIP_SUM). `in_place`: where the factor is
 // 1, the tensors that hold x already are left as they are.
 template <typename T, typename U, int MODE>
-__global__ void __launch_bounds__(kThreads) k_clip_scale(const __grid_constant__ ClipArgs a, bool in_place) {
+__global__ void __launch_bounds__(kThreads, 4) k_clip_scale(const __grid_constant__ ClipArgs a, bool in_place) {
   __shared__ double red[kWarps];
   __shared__ float shared_factor;
-  const int lane = threadIdx.x & 31;
   double total = 0.0;
   for (int i = threadIdx.x; i < a.nparts; i += kThreads) total += a.parts[i];
   total = block_sum(total, red);
@@ -193,26 +304,25 @@ __global__ void __launch_bounds__(kThreads) k_clip_scale(const __grid_constant__
   const int64_t nwarps = static_cast<int64_t>(gridDim.x) * kWarps;
   const int64_t items = MODE == CLIP_LOCAL ? a.nbuckets * a.nranks : a.nbuckets;
   using X = typename std::conditional<MODE == CLIP_SUM, U, T>::type;
-  for (int64_t it = items - 1 - warp; it >= 0; it -= nwarps) {
-    const int64_t b = MODE == CLIP_LOCAL ? it / a.nranks : it;
-    if (!same_bucket<T, U>(a, b)) continue;
-    const int r0 = MODE == CLIP_LOCAL ? static_cast<int>(it - b * a.nranks) : 0;
-    const Bucket from = MODE == CLIP_SUM ? bucket_at<X>(a.out_table, b, a.out_nranks, 0)
-                                         : bucket_at<X>(a.table, b, a.nranks, r0);
-    const int first = MODE == CLIP_LOCAL ? r0 : MODE == CLIP_SUM && keep ? 1 : 0;
-    const int last = MODE == CLIP_LOCAL ? r0 + 1 : a.out_nranks;
-    float f[kBucketChunks][kChunk];
-#pragma unroll
-    for (int i = 0; i < kBucketChunks; ++i) {
-      load_part<X>(from, lane + 32 * i, f[i]);
-#pragma unroll
-      for (int j = 0; j < kChunk; ++j) f[i][j] *= factor;
-    }
-    for (int r = first; r < last; ++r) {
-      const Bucket to = bucket_at<U>(a.out_table, b, a.out_nranks, r);
-#pragma unroll
-      for (int i = 0; i < kBucketChunks; ++i) store_part<U>(to, lane + 32 * i, f[i]);
-    }
+  const bool two = a.table != a.out_table;
+  const int first = MODE == CLIP_SUM && keep ? 1 : 0, last = MODE == CLIP_LOCAL ? 1 : a.out_nranks;
+  uint32_t words = 0, out_words = 0;
+  auto fetch = [&](int64_t it) {
+    words = MODE == CLIP_LOCAL ? entry_words(a.table, it, 1, 0, 1) : entry_words(a.table, it, a.nranks, 0, 1);
+    if (two) out_words = MODE == CLIP_LOCAL ? entry_words(a.out_table, it, 1, 0, 1)
+                                            : entry_words(a.out_table, it, a.out_nranks, 0, 1);
+    else out_words = words;
+  };
+  int64_t it = items - 1 - warp;
+  if (it >= 0) fetch(it);
+  for (; it >= 0; it -= nwarps) {
+    const uint32_t w = words, ow = out_words;
+    if (it >= nwarps) fetch(it - nwarps);
+    const uint32_t code = code_of(w);
+    if (code != code_of(ow)) continue;
+    const uint32_t src = MODE == CLIP_SUM ? ow : w;
+    if ((code & 1023u) == 1023u) scale_full<X, U>(a, it, src, ow, first, last, factor);
+    else scale_end<X, U>(a, it, src, ow, first, last, factor);
   }
 }
 
@@ -233,10 +343,18 @@ cudaError_t clip_go(const ClipLaunch& L, cudaStream_t s) {
   int64_t most = static_cast<int64_t>(sm_count()) * 4;
   most = most < kClipMaxParts ? most : kClipMaxParts;
   a.nparts = static_cast<int32_t>(want < most ? want : most);
-  k_clip_squares<T, U, MODE><<<a.nparts, kThreads, 0, s>>>(a);
+  if constexpr (MODE == CLIP_SUM) {
+    cudaError_t e = with_ranks<2, 4, 8>(L.nranks, [&](auto n) {
+      k_clip_squares<T, U, MODE, n.value><<<a.nparts, kThreads, 0, s>>>(a);
+      return cudaGetLastError();
+    });
+    if (e != cudaSuccess) return e;
+  } else {
+    k_clip_squares<T, U, MODE, 1><<<a.nparts, kThreads, 0, s>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   count_launch();
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   k_clip_scale<T, U, MODE><<<a.nparts, kThreads, 0, s>>>(a, L.table == L.out_table);
   count_launch();
   return cudaGetLastError();

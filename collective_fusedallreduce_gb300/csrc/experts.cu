@@ -61,6 +61,19 @@ __device__ __forceinline__ int32_t ld_peer(const int32_t* p, int cta) {
   return v;
 }
 
+constexpr int kSortBatch = 8;  // choices a lane loads at a time
+
+// The experts of a lane's choices i0 + lane, i0 + 32 + lane, ..., -1 where there is none.
+template <typename I>
+__device__ __forceinline__ void load_experts(const I* e, int64_t i0, int64_t last, int experts, int (&out)[kSortBatch]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < kSortBatch; ++j) {
+    const int64_t i = i0 + 32 * j + lane;
+    out[j] = i < last ? expert_at(e, i, experts) : -1;
+  }
+}
+
 // A stable counting sort by one cluster of CTAs for each group. Every warp owns a run of the choices and counts its
 // experts in shared memory; a column's counts become the warps' starts in order, the CTAs' sums are exchanged through
 // distributed shared memory, and a scan over the experts gives the offsets. Each warp then walks its run again, 32
@@ -73,6 +86,7 @@ __global__ void __launch_bounds__(kSortThreads) k_expert_sort(const __grid_const
   int32_t* hist = sort_smem;                // [warps][tile]
   int32_t* sums = hist + a.warps * a.tile;  // [tile]: this CTA's choices of every expert
   int32_t* start = sums + a.tile;           // [tile]: the first row of this CTA's
+  const int threads = blockDim.x;
   const int ctas = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
   const int g = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -82,28 +96,37 @@ __global__ void __launch_bounds__(kSortThreads) k_expert_sort(const __grid_const
   const int64_t at = static_cast<int64_t>(rank * a.warps + warp) * a.seg;
   const int64_t first = warp < a.warps ? (at < a.n ? at : a.n) : a.n;
   const int64_t last = first + a.seg < a.n ? first + a.seg : a.n;
+  int32_t* mine = hist + (warp < a.warps ? warp : 0) * a.tile;
   int32_t base = 0;  // rows of the experts before this tile's
   for (int e0 = 0; e0 < a.experts || e0 == 0; e0 += a.tile) {
     const int ne = a.experts - e0 < a.tile ? a.experts - e0 : a.tile;
-    for (int i = threadIdx.x; i < a.warps * a.tile; i += kSortThreads) hist[i] = 0;
+    for (int i = threadIdx.x; i < a.warps * a.tile; i += threads) hist[i] = 0;
     __syncthreads();
-    for (int64_t i = first + lane; i < last; i += 32) {
-      const int e = expert_at(expert_of, i, a.experts) - e0;
-      if (e >= 0 && e < ne) atomicAdd(&hist[warp * a.tile + e], 1);
+    for (int64_t i0 = first; i0 < last; i0 += 32 * kSortBatch) {
+      int e[kSortBatch];
+      load_experts(expert_of, i0, last, a.experts, e);
+#pragma unroll
+      for (int j = 0; j < kSortBatch; ++j)
+        if (e[j] >= e0 && e[j] < e0 + ne) atomicAdd(mine + e[j] - e0, 1);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < ne; e += kSortThreads) {
+    for (int e = threadIdx.x; e < ne; e += threads) {
       int32_t s = 0;
-      for (int w = 0; w < a.warps; ++w) {
-        const int32_t c = hist[w * a.tile + e];
-        hist[w * a.tile + e] = s;
-        s += c;
+      for (int w0 = 0; w0 < a.warps; w0 += 8) {  // (eight at a time: their loads do not wait for one another)
+        int32_t c[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) c[j] = w0 + j < a.warps ? hist[(w0 + j) * a.tile + e] : 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (w0 + j < a.warps) hist[(w0 + j) * a.tile + e] = s;
+          s += c[j];
+        }
       }
       sums[e] = s;
     }
     cluster_sync();
     int turn = 0;
-    for (int b = 0; b < ne; b += kSortThreads, turn ^= 1) {
+    for (int b = 0; b < ne; b += threads, turn ^= 1) {
       const int e = b + threadIdx.x;
       int32_t before = 0, all = 0;
       if (e < ne)
@@ -121,7 +144,7 @@ __global__ void __launch_bounds__(kSortThreads) k_expert_sort(const __grid_const
       if (lane == 31) scan[turn][warp] = incl;
       __syncthreads();
       int32_t here = base, total = 0;
-      for (int w = 0; w < kSortWarps; ++w) {
+      for (int w = 0; w < threads >> 5; ++w) {
         const int32_t v = scan[turn][w];
         if (w < warp) here += v;
         total += v;
@@ -136,22 +159,27 @@ __global__ void __launch_bounds__(kSortThreads) k_expert_sort(const __grid_const
       base += total;
     }
     __syncthreads();
-    for (int64_t i0 = first; i0 < last; i0 += 32) {
-      const int64_t i = i0 + lane;
-      const int all_e = i < last ? expert_at(expert_of, i, a.experts) : -1;
-      const int e = all_e >= e0 && all_e < e0 + ne ? all_e - e0 : -1;
-      const unsigned peers = __match_any_sync(0xffffffffu, e);
-      int32_t pos = -1;
-      if (e >= 0) pos = start[e] + hist[warp * a.tile + e] + __popc(peers & ((1u << lane) - 1));
-      __syncwarp();
-      if (e >= 0 && (peers >> lane) == 1u) hist[warp * a.tile + e] += __popc(peers);  // (the last lane of them)
-      __syncwarp();
-      if (i < last) {
-        if (e >= 0) {
-          row_of[i] = pos;
-          if (choice_of) choice_of[pos] = static_cast<int32_t>(i);
-        } else if (all_e < 0 && e0 == 0) {
-          row_of[i] = -1;
+    for (int64_t i0 = first; i0 < last; i0 += 32 * kSortBatch) {
+      int all_e[kSortBatch];
+      load_experts(expert_of, i0, last, a.experts, all_e);
+#pragma unroll
+      for (int j = 0; j < kSortBatch; ++j) {
+        const int64_t i = i0 + 32 * j + lane;
+        if (i0 + 32 * j >= last) break;  // (the whole warp)
+        const int e = all_e[j] >= e0 && all_e[j] < e0 + ne ? all_e[j] - e0 : -1;
+        const unsigned peers = __match_any_sync(0xffffffffu, e);
+        int32_t pos = -1;
+        if (e >= 0) pos = start[e] + mine[e] + __popc(peers & ((1u << lane) - 1));
+        __syncwarp();
+        if (e >= 0 && (peers >> lane) == 1u) mine[e] += __popc(peers);  // (the last lane of them)
+        __syncwarp();
+        if (i < last) {
+          if (e >= 0) {
+            row_of[i] = pos;
+            if (choice_of) choice_of[pos] = static_cast<int32_t>(i);
+          } else if (all_e[j] < 0 && e0 == 0) {
+            row_of[i] = -1;
+          }
         }
       }
     }
@@ -160,7 +188,7 @@ __global__ void __launch_bounds__(kSortThreads) k_expert_sort(const __grid_const
   if (rank == 0 && threadIdx.x < a.nranks)
     a.offsets[static_cast<int64_t>(g * a.nranks + threadIdx.x) * (a.experts + 1) + a.experts] = base;
   if (choice_of)
-    for (int64_t p = static_cast<int64_t>(base) + rank * kSortThreads + threadIdx.x; p < a.n; p += ctas * kSortThreads)
+    for (int64_t p = static_cast<int64_t>(base) + rank * threads + threadIdx.x; p < a.n; p += ctas * threads)
       choice_of[p] = -1;
 }
 
@@ -215,11 +243,19 @@ struct CombineArgs {
   int32_t choices, nranks, nchunks;
 };
 
+// How many positions a thread takes and how many choices at a time, so that some sixteen loads are under way.
+template <int NR>
+struct CombineShape {
+  static constexpr int ITEMS = NR == 1 || NR == 2 ? 2 : 1;
+  static constexpr int AHEAD = NR == 8 || NR == 0 ? 1 : 2;
+};
+
 // SUMMED: grid y counts groups, whose ranks' rows are added up, with the residual, for every distinct output. Otherwise
 // it counts ranks, each with an output of its own (NR is 1). Grid x: chunks of 8 columns, token after token. A choice's
 // rows are added over the ranks first (in order), then weighted; product and sum are rounded one by one.
 template <typename T, int NR, bool SUMMED>
 __global__ void __launch_bounds__(kThreads) k_expert_combine(const __grid_constant__ CombineArgs a) {
+  constexpr int ITEMS = CombineShape<NR>::ITEMS, AHEAD = CombineShape<NR>::AHEAD;
   const int g = SUMMED ? blockIdx.y : blockIdx.y / a.nranks;
   const int slot0 = SUMMED ? g * a.nranks : blockIdx.y;
   const void* const* in = a.t.in + slot0;
@@ -227,37 +263,80 @@ __global__ void __launch_bounds__(kThreads) k_expert_combine(const __grid_consta
   const int nout = SUMMED ? a.t.nout[g] : 1;
   const int32_t* row_of = a.row_of + g * a.tokens * a.choices;
   const float* gates = a.gates ? a.gates + g * a.tokens * a.choices : nullptr;
-  const int64_t total = a.tokens * a.nchunks, step = static_cast<int64_t>(gridDim.x) * kThreads;
-  for (int64_t p = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; p < total; p += step) {
-    const int64_t t = total <= 0x7fffffff ? static_cast<uint32_t>(p) / static_cast<uint32_t>(a.nchunks) : p / a.nchunks;
-    const int c = static_cast<int>(p - t * a.nchunks);
-    Chunk<T> res;
-    if (residual) res.load(residual, p);
-    float acc[kChunk];
+  const int64_t total = a.tokens * a.nchunks, step = static_cast<int64_t>(gridDim.x) * kThreads * ITEMS;
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * kThreads * ITEMS + threadIdx.x; base < total; base += step) {
+    int64_t first[ITEMS];  // a position's first choice, or -1
+    int32_t c[ITEMS];
+    Chunk<T> res[ITEMS];
+    float acc[ITEMS][kChunk];
 #pragma unroll
-    for (int j = 0; j < kChunk; ++j) acc[j] = 0.0f;
-    for (int k = 0; k < a.choices; ++k) {
-      const int64_t row = row_of[t * a.choices + k];
-      if (row < 0 || row >= a.rows) continue;
-      float f[kChunk];
-      sum_ranks<T, NR>(in, a.nranks, row * a.nchunks + c, f);
-      if (gates) {
-        const float w = gates[t * a.choices + k];
+    for (int u = 0; u < ITEMS; ++u) {
+      const int64_t p = base + u * kThreads;
+      const int64_t t = total <= 0x7fffffff ? static_cast<uint32_t>(p) / static_cast<uint32_t>(a.nchunks) : p / a.nchunks;
+      c[u] = static_cast<int32_t>(p - t * a.nchunks);
+      first[u] = p < total ? t * a.choices : -1;
+      if (p < total && residual) res[u].load(residual, p);
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j) f[j] = __fmul_rn(f[j], w);
+      for (int j = 0; j < kChunk; ++j) acc[u][j] = 0.0f;
+    }
+    for (int k0 = 0; k0 < a.choices; k0 += AHEAD) {
+      int32_t row[ITEMS][AHEAD];
+      float w[ITEMS][AHEAD];
+#pragma unroll
+      for (int u = 0; u < ITEMS; ++u)
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+          const bool has = first[u] >= 0 && k0 + k < a.choices;
+          row[u][k] = has ? row_of[first[u] + k0 + k] : -1;
+          if (row[u][k] >= a.rows) row[u][k] = -1;
+          w[u][k] = has && gates ? gates[first[u] + k0 + k] : 1.0f;
+        }
+      if constexpr (NR > 0) {
+        Chunk<T> raw[ITEMS][AHEAD][NR];
+#pragma unroll
+        for (int u = 0; u < ITEMS; ++u)
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k)
+            if (row[u][k] >= 0)
+#pragma unroll
+              for (int r = 0; r < NR; ++r) raw[u][k][r].load(in[r], static_cast<int64_t>(row[u][k]) * a.nchunks + c[u]);
+#pragma unroll
+        for (int u = 0; u < ITEMS; ++u)
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k)
+            if (row[u][k] >= 0) {
+              float s[kChunk], f[kChunk];
+              raw[u][k][0].get(s);
+#pragma unroll
+              for (int r = 1; r < NR; ++r) {
+                raw[u][k][r].get(f);
+#pragma unroll
+                for (int j = 0; j < kChunk; ++j) s[j] += f[j];
+              }
+#pragma unroll
+              for (int j = 0; j < kChunk; ++j) acc[u][j] = __fadd_rn(acc[u][j], __fmul_rn(s[j], w[u][k]));
+            }
+      } else if (row[0][0] >= 0) {
+        float s[kChunk];
+        sum_all<T, 0>(in, a.nranks, static_cast<int64_t>(row[0][0]) * a.nchunks + c[0], s);
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j) acc[0][j] = __fadd_rn(acc[0][j], __fmul_rn(s[j], w[0][0]));
       }
-#pragma unroll
-      for (int j = 0; j < kChunk; ++j) acc[j] = __fadd_rn(acc[j], f[j]);
     }
-    if (residual) {
-      float f[kChunk];
-      res.get(f);
 #pragma unroll
-      for (int j = 0; j < kChunk; ++j) acc[j] += f[j];
+    for (int u = 0; u < ITEMS; ++u) {
+      const int64_t p = base + u * kThreads;
+      if (p >= total) break;
+      if (residual) {
+        float f[kChunk];
+        res[u].get(f);
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j) acc[u][j] += f[j];
+      }
+      Chunk<T> o;
+      o.put(acc[u]);
+      for (int q = 0; q < nout; ++q) o.store(a.t.out[slot0 + q], p);
     }
-    Chunk<T> o;
-    o.put(acc);
-    for (int q = 0; q < nout; ++q) o.store(a.t.out[slot0 + q], p);
   }
 }
 
@@ -273,10 +352,32 @@ struct CombineBwdArgs {
   int32_t tpr_log2;
 };
 
+constexpr int kDots = 4;  // choices whose products are summed at a time
+
+// kDots sums over the threads of a token, as row_sum; tokens that share a block have a barrier each.
+__device__ __forceinline__ void token_sums(float (&v)[kDots], int tpr, int slot, float (*red)[kDots][32], int turn) {
+#pragma unroll
+  for (int i = 0; i < kDots; ++i) v[i] = warp_sum(v[i]);
+  if (tpr == 32) return;
+  const int warp = threadIdx.x >> 5, warps = tpr >> 5;
+  if ((threadIdx.x & 31) == 0)
+#pragma unroll
+    for (int i = 0; i < kDots; ++i) red[turn][i][warp] = v[i];
+  if (blockDim.x == tpr || blockDim.x > 15 * tpr) __syncthreads();
+  else asm volatile("bar.sync %0, %1;" ::"r"(1 + slot), "r"(tpr) : "memory");
+  const int first = warp & ~(warps - 1), t = threadIdx.x & (tpr - 1);
+  if (t < kDots) {  // (thread t has the t-th sum)
+    float s = red[turn][t][first];
+    for (int i = 1; i < warps; ++i) s += red[turn][t][first + i];
+    v[0] = s;
+  }
+}
+
 // A token belongs to `tpr` threads, which keep its gradient in registers; grid y: groups.
-template <typename T, int NR, int VPT>
-__global__ void __launch_bounds__(512) k_expert_combine_backward(const __grid_constant__ CombineBwdArgs a) {
-  __shared__ float red[2][32];
+template <typename T, int NR, int VPT, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 1024 ? 1 : 2)
+    k_expert_combine_backward(const __grid_constant__ CombineBwdArgs a) {
+  __shared__ float red[2][kDots][32];
   const int g = blockIdx.y;
   const int tpr = 1 << a.tpr_log2;
   const int tt = threadIdx.x & (tpr - 1), slot = threadIdx.x >> a.tpr_log2, rpb = blockDim.x >> a.tpr_log2;
@@ -287,40 +388,65 @@ __global__ void __launch_bounds__(512) k_expert_combine_backward(const __grid_co
        base += static_cast<int64_t>(gridDim.x) * rpb) {
     const int64_t t = base + slot;
     const bool live = t < a.tokens;
+    const int64_t at = (g * a.tokens + t) * a.choices;
     Chunk<T> d[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = tt + i * tpr;
       if (live && c < a.nchunks) d[i].load(a.t.residual[g], t * a.nchunks + c);
     }
-    for (int k = 0; k < a.choices; ++k) {
-      const int64_t at = (g * a.tokens + t) * a.choices + k;
-      int64_t row = live ? a.row_of[at] : -1;
-      if (row >= a.rows) row = -1;
-      const float w = row >= 0 && a.gates ? a.gates[at] : 1.0f;
-      float dot = 0.0f;
+    for (int k0 = 0; k0 < a.choices; k0 += kDots) {
+      int32_t row[kDots];
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int c = tt + i * tpr;
-        if (row >= 0 && c < a.nchunks) {
-          float f[kChunk], o[kChunk];
-          d[i].get(o);
-          if (a.dgates) {
-            sum_ranks<T, NR>(in, a.nranks, row * a.nchunks + c, f);
-#pragma unroll
-            for (int j = 0; j < kChunk; ++j) dot = fmaf(f[j], o[j], dot);
-          }
-#pragma unroll
-          for (int j = 0; j < kChunk; ++j) o[j] *= w;
-          Chunk<T> ov;
-          ov.put(o);
-          for (int q = 0; q < nout; ++q) ov.store(a.t.out[slot0 + q], row * a.nchunks + c);
-        }
+      for (int k = 0; k < kDots; ++k) {
+        row[k] = live && k0 + k < a.choices ? a.row_of[at + k0 + k] : -1;
+        if (row[k] >= a.rows) row[k] = -1;
       }
       if (a.dgates) {
-        dot = row_sum<false>(dot, tpr, slot, red, turn);
+        float dot[kDots];
+#pragma unroll
+        for (int k = 0; k < kDots; ++k) {
+          dot[k] = 0.0f;
+          if (row[k] < 0) continue;
+#pragma unroll
+          for (int i = 0; i < VPT; ++i) {
+            const int c = tt + i * tpr;
+            if (c < a.nchunks) {
+              float f[kChunk], o[kChunk];
+              sum_all<T, NR>(in, a.nranks, static_cast<int64_t>(row[k]) * a.nchunks + c, f);
+              d[i].get(o);
+#pragma unroll
+              for (int j = 0; j < kChunk; ++j) dot[k] = fmaf(f[j], o[j], dot[k]);
+            }
+          }
+        }
+        token_sums(dot, tpr, slot, red, turn);
         turn ^= 1;
-        if (live && tt == 0) a.dgates[at] = dot;
+        if (tpr == 32) {
+#pragma unroll
+          for (int k = 0; k < kDots; ++k)
+            if (live && tt == k && k0 + k < a.choices) a.dgates[at + k0 + k] = dot[k];
+        } else if (live && tt < kDots && k0 + tt < a.choices) {
+          a.dgates[at + k0 + tt] = dot[0];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kDots; ++k) {
+        if (row[k] < 0) continue;
+        const float w = a.gates ? a.gates[at + k0 + k] : 1.0f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+          const int c = tt + i * tpr;
+          if (c < a.nchunks) {
+            float o[kChunk];
+            d[i].get(o);
+#pragma unroll
+            for (int j = 0; j < kChunk; ++j) o[j] *= w;
+            Chunk<T> ov;
+            ov.put(o);
+            for (int q = 0; q < nout; ++q) ov.store(a.t.out[slot0 + q], static_cast<int64_t>(row[k]) * a.nchunks + c);
+          }
+        }
       }
     }
   }
@@ -335,7 +461,8 @@ int blocks_for(int64_t items) {
 
 template <typename T, int NR, bool SUMMED>
 cudaError_t combine_go(const CombineArgs& a, int ngroups, cudaStream_t s) {
-  const dim3 grid(blocks_for(a.tokens * a.nchunks), SUMMED ? ngroups : ngroups * a.nranks);
+  constexpr int ITEMS = CombineShape<NR>::ITEMS;
+  const dim3 grid(blocks_for((a.tokens * a.nchunks + ITEMS - 1) / ITEMS), SUMMED ? ngroups : ngroups * a.nranks);
   k_expert_combine<T, NR, SUMMED><<<grid, kThreads, 0, s>>>(a);
   count_launch();
   return cudaGetLastError();
@@ -344,32 +471,32 @@ cudaError_t combine_go(const CombineArgs& a, int ngroups, cudaStream_t s) {
 template <typename T>
 cudaError_t combine_ranks(const CombineArgs& a, bool summed, int ngroups, cudaStream_t s) {
   if (!summed) return combine_go<T, 1, false>(a, ngroups, s);
-  switch (a.nranks) {
-    case 1: return combine_go<T, 1, true>(a, ngroups, s);
-    case 8: return combine_go<T, 8, true>(a, ngroups, s);
-    default: return combine_go<T, 0, true>(a, ngroups, s);
-  }
+  return with_ranks<1, 2, 3, 4, 8>(a.nranks, [&](auto n) { return combine_go<T, n.value, true>(a, ngroups, s); });
 }
 
-template <typename T, int NR>
-cudaError_t combine_bwd_vpt(const CombineBwdArgs& a, const RowShape& r, dim3 grid, cudaStream_t s) {
-  switch (r.vpt) {
-    case 1: k_expert_combine_backward<T, NR, 1><<<grid, r.threads, 0, s>>>(a); break;
-    case 2: k_expert_combine_backward<T, NR, 2><<<grid, r.threads, 0, s>>>(a); break;
-    case 4: k_expert_combine_backward<T, NR, 4><<<grid, r.threads, 0, s>>>(a); break;
-    default: k_expert_combine_backward<T, NR, 8><<<grid, r.threads, 0, s>>>(a); break;
-  }
+template <typename T, int NR, int VPT, int THREADS>
+cudaError_t combine_bwd_go(const CombineBwdArgs& a, int ngroups, cudaStream_t s) {
+  const int tpr = 1 << a.tpr_log2;
+  const int threads = THREADS == 1024 ? 1024 : tpr < 256 ? 256 : tpr, rpb = threads / tpr;
+  const int64_t blocks = (a.tokens + rpb - 1) / rpb;
+  const dim3 grid(static_cast<unsigned>(blocks < (1 << 30) ? blocks : (1 << 30)), ngroups);
+  k_expert_combine_backward<T, NR, VPT, THREADS><<<grid, threads, 0, s>>>(a);
   count_launch();
   return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t combine_bwd_ranks(const CombineBwdArgs& a, const RowShape& r, dim3 grid, cudaStream_t s) {
-  switch (a.nranks) {
-    case 1: return combine_bwd_vpt<T, 1>(a, r, grid, s);
-    case 8: return combine_bwd_vpt<T, 8>(a, r, grid, s);
-    default: return combine_bwd_vpt<T, 0>(a, r, grid, s);
-  }
+cudaError_t combine_bwd_shape(CombineBwdArgs& a, int ngroups, cudaStream_t s) {
+  a.tpr_log2 = 5;
+  while (a.tpr_log2 < 9 && (1 << a.tpr_log2) < a.nchunks) ++a.tpr_log2;
+  if (a.nchunks <= 512)
+    return with_ranks<1, 2, 4, 8>(a.nranks, [&](auto n) { return combine_bwd_go<T, n.value, 1, 512>(a, ngroups, s); });
+  if (a.nchunks <= 1024)
+    return with_ranks<1, 2, 8>(a.nranks, [&](auto n) { return combine_bwd_go<T, n.value, 2, 512>(a, ngroups, s); });
+  a.tpr_log2 = 10;
+  if (a.nchunks <= 2048)
+    return with_ranks<1>(a.nranks, [&](auto n) { return combine_bwd_go<T, n.value, 2, 1024>(a, ngroups, s); });
+  return combine_bwd_go<T, 0, 4, 1024>(a, ngroups, s);
 }
 
 }  // namespace
@@ -384,9 +511,13 @@ cudaError_t launch_expert_sort(const ExpertSortLaunch& L, cudaStream_t s) {
   a.experts = L.experts;
   a.nranks = L.nranks;
   a.tile = L.experts < kSortTile ? (L.experts > 0 ? L.experts : 1) : kSortTile;
-  const int most = kSortSmem / (4 * a.tile) - 2;
-  a.warps = most < kSortWarps ? most : kSortWarps;
+  // One CTA, of as many threads as there are choices or experts, or eight.
   const int ctas = L.n <= 4 * kSortThreads ? 1 : 8;
+  const int64_t wide = L.n > L.experts ? L.n : L.experts;
+  const int threads = ctas > 1 || wide >= kSortThreads ? kSortThreads : wide <= 128 ? 128 : static_cast<int>((wide + 31) / 32 * 32);
+  const int most = kSortSmem / (4 * a.tile) - 2, filled = static_cast<int>(L.n < kSortThreads ? (L.n + 31) / 32 : kSortWarps);
+  a.warps = most < threads / 32 ? most : threads / 32;
+  if (a.warps > filled && ctas == 1) a.warps = filled > 0 ? filled : 1;
   a.seg = (L.n + ctas * a.warps - 1) / (ctas * a.warps);
   a.seg = (a.seg + 31) / 32 * 32;
   const void* fn = L.index64 ? reinterpret_cast<const void*>(&k_expert_sort<int64_t>)
@@ -404,7 +535,7 @@ cudaError_t launch_expert_sort(const ExpertSortLaunch& L, cudaStream_t s) {
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas, L.ngroups);
-  cfg.blockDim = dim3(kSortThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = static_cast<size_t>(a.warps + 2) * a.tile * 4;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -462,14 +593,10 @@ cudaError_t launch_expert_combine_backward(const ExpertRowsLaunch& L, cudaStream
   a.choices = L.choices;
   a.nranks = L.nranks;
   a.nchunks = L.cols / kChunk;
-  const RowShape r = row_shape(a.nchunks);
-  a.tpr_log2 = r.tpr_log2;
-  const int64_t blocks = (L.tokens + r.rpb - 1) / r.rpb;
-  const dim3 grid(static_cast<unsigned>(blocks < (1 << 30) ? blocks : (1 << 30)), L.ngroups);
   switch (L.dtype) {
-    case COCO_F32: return combine_bwd_ranks<float>(a, r, grid, s);
-    case COCO_F16: return combine_bwd_ranks<__half>(a, r, grid, s);
-    default: return combine_bwd_ranks<__nv_bfloat16>(a, r, grid, s);
+    case COCO_F32: return combine_bwd_shape<float>(a, L.ngroups, s);
+    case COCO_F16: return combine_bwd_shape<__half>(a, L.ngroups, s);
+    default: return combine_bwd_shape<__nv_bfloat16>(a, L.ngroups, s);
   }
 }
 
