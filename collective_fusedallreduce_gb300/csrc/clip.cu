@@ -210,7 +210,7 @@ __device__ __forceinline__ double squares_end(const ClipArgs& a, int64_t b, uint
 // the ranks' tensors are added in rank order, scaled by alpha, rounded to U and stored to out's rank 0, and it is those
 // values' norm. Where the two tables' tensors do not have a bucket in common, nothing is written and the norm is NaN.
 template <typename T, typename U, int MODE, int NR>
-__global__ void __launch_bounds__(kThreads, MODE == CLIP_SUM && NR == 8 ? 3 : 4)
+__global__ void __launch_bounds__(kThreads, MODE == CLIP_SUM ? (NR == 8 ? 3 : 4) : sizeof(T) == 2 ? 6 : 4)
     k_clip_squares(const __grid_constant__ ClipArgs a) {
   __shared__ double red[kWarps];
   const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
@@ -340,11 +340,11 @@ cudaError_t clip_go(const ClipLaunch& L, cudaStream_t s) {
   a.parts = L.parts;
   const int64_t items = MODE == CLIP_LOCAL ? L.nbuckets * L.nranks : L.nbuckets;
   const int64_t want = items ? (items + kWarps - 1) / kWarps : 1;
-  int64_t most = static_cast<int64_t>(sm_count()) * 4;
+  int64_t most = static_cast<int64_t>(sm_count()) * (MODE == CLIP_SUM ? 4 : 6);
   most = most < kClipMaxParts ? most : kClipMaxParts;
   a.nparts = static_cast<int32_t>(want < most ? want : most);
   if constexpr (MODE == CLIP_SUM) {
-    cudaError_t e = with_ranks<2, 4, 8>(L.nranks, [&](auto n) {
+    cudaError_t e = with_ranks<2, 3, 4, 8>(L.nranks, [&](auto n) {
       k_clip_squares<T, U, MODE, n.value><<<a.nparts, kThreads, 0, s>>>(a);
       return cudaGetLastError();
     });

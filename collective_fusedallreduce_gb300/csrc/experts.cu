@@ -53,6 +53,9 @@ __device__ __forceinline__ uint32_t cluster_nctarank() {
   return r;
 }
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 __device__ __forceinline__ int32_t ld_peer(const int32_t* p, int cta) {
   uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(cta));
@@ -97,14 +100,21 @@ __global__ void __launch_bounds__(kSortThreads) k_expert_sort(const __grid_const
   const int64_t first = warp < a.warps ? (at < a.n ? at : a.n) : a.n;
   const int64_t last = first + a.seg < a.n ? first + a.seg : a.n;
   int32_t* mine = hist + (warp < a.warps ? warp : 0) * a.tile;
+  const bool kept = a.seg <= 32 * kSortBatch;  // a lane's choices fit its registers
+  int kept_e[kSortBatch];
+  if (kept) load_experts(expert_of, first, last, a.experts, kept_e);
   int32_t base = 0;  // rows of the experts before this tile's
   for (int e0 = 0; e0 < a.experts || e0 == 0; e0 += a.tile) {
     const int ne = a.experts - e0 < a.tile ? a.experts - e0 : a.tile;
+    if (e0 > 0) __syncthreads();  // every warp has placed the last tile's
     for (int i = threadIdx.x; i < a.warps * a.tile; i += threads) hist[i] = 0;
     __syncthreads();
     for (int64_t i0 = first; i0 < last; i0 += 32 * kSortBatch) {
       int e[kSortBatch];
-      load_experts(expert_of, i0, last, a.experts, e);
+      if (!kept) load_experts(expert_of, i0, last, a.experts, e);
+#pragma unroll
+      for (int j = 0; j < kSortBatch; ++j)
+        if (kept) e[j] = kept_e[j];
 #pragma unroll
       for (int j = 0; j < kSortBatch; ++j)
         if (e[j] >= e0 && e[j] < e0 + ne) atomicAdd(mine + e[j] - e0, 1);
@@ -124,16 +134,21 @@ __global__ void __launch_bounds__(kSortThreads) k_expert_sort(const __grid_const
       }
       sums[e] = s;
     }
-    cluster_sync();
+    cluster_sync();  // every CTA's sums are there
     int turn = 0;
     for (int b = 0; b < ne; b += threads, turn ^= 1) {
       const int e = b + threadIdx.x;
       int32_t before = 0, all = 0;
       if (e < ne)
-        for (int c = 0; c < ctas; ++c) {
-          const int32_t s = ld_peer(sums + e, c);
-          all += s;
-          if (c < rank) before += s;
+        for (int c0 = 0; c0 < ctas; c0 += 8) {  // (eight at a time: their loads do not wait for one another)
+          int32_t s[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) s[c] = c0 + c < ctas ? ld_peer(sums + e, c0 + c) : 0;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            all += s[c];
+            if (c0 + c < rank) before += s[c];
+          }
         }
       int32_t incl = all;
 #pragma unroll
@@ -143,13 +158,15 @@ __global__ void __launch_bounds__(kSortThreads) k_expert_sort(const __grid_const
       }
       if (lane == 31) scan[turn][warp] = incl;
       __syncthreads();
-      int32_t here = base, total = 0;
-      for (int w = 0; w < threads >> 5; ++w) {
-        const int32_t v = scan[turn][w];
-        if (w < warp) here += v;
-        total += v;
+      int32_t sum = lane < threads >> 5 ? scan[turn][lane] : 0;  // the warps' sums, scanned by every warp
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int32_t v = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += v;
       }
-      here += incl - all;
+      const int32_t total = __shfl_sync(0xffffffffu, sum, 31);
+      const int32_t earlier = __shfl_sync(0xffffffffu, sum, warp > 0 ? warp - 1 : 0);
+      const int32_t here = base + (warp > 0 ? earlier : 0) + incl - all;
       if (e < ne) {
         start[e] = here + before;
         if (rank == 0)
@@ -158,10 +175,14 @@ __global__ void __launch_bounds__(kSortThreads) k_expert_sort(const __grid_const
       }
       base += total;
     }
+    cluster_arrive();  // this CTA reads no more of them
     __syncthreads();
     for (int64_t i0 = first; i0 < last; i0 += 32 * kSortBatch) {
       int all_e[kSortBatch];
-      load_experts(expert_of, i0, last, a.experts, all_e);
+      if (!kept) load_experts(expert_of, i0, last, a.experts, all_e);
+#pragma unroll
+      for (int j = 0; j < kSortBatch; ++j)
+        if (kept) all_e[j] = kept_e[j];
 #pragma unroll
       for (int j = 0; j < kSortBatch; ++j) {
         const int64_t i = i0 + 32 * j + lane;
@@ -183,7 +204,7 @@ __global__ void __launch_bounds__(kSortThreads) k_expert_sort(const __grid_const
         }
       }
     }
-    cluster_sync();  // (nobody's sums are read any more)
+    cluster_wait();  // nobody does: they may be written again, or the CTA leave
   }
   if (rank == 0 && threadIdx.x < a.nranks)
     a.offsets[static_cast<int64_t>(g * a.nranks + threadIdx.x) * (a.experts + 1) + a.experts] = base;
@@ -243,19 +264,22 @@ struct CombineArgs {
   int32_t choices, nranks, nchunks;
 };
 
-// How many positions a thread takes and how many choices at a time, so that some sixteen loads are under way.
-template <int NR>
+// How many positions a thread takes and how many choices at a time, so that some loads are under way. MANY: more than two
+// choices.
+template <int NR, bool MANY>
 struct CombineShape {
-  static constexpr int ITEMS = NR == 1 || NR == 2 ? 2 : 1;
-  static constexpr int AHEAD = NR == 8 || NR == 0 ? 1 : 2;
+  static constexpr int ITEMS = NR == 1 && !MANY ? 2 : 1;
+  static constexpr int AHEAD = NR == 1 && MANY ? 4 : NR == 8 || NR == 0 ? 1 : 2;
+  static constexpr int BLOCKS = NR == 1 && MANY ? 5 : 4;
 };
 
 // SUMMED: grid y counts groups, whose ranks' rows are added up, with the residual, for every distinct output. Otherwise
 // it counts ranks, each with an output of its own (NR is 1). Grid x: chunks of 8 columns, token after token. A choice's
 // rows are added over the ranks first (in order), then weighted; product and sum are rounded one by one.
-template <typename T, int NR, bool SUMMED>
-__global__ void __launch_bounds__(kThreads) k_expert_combine(const __grid_constant__ CombineArgs a) {
-  constexpr int ITEMS = CombineShape<NR>::ITEMS, AHEAD = CombineShape<NR>::AHEAD;
+template <typename T, int NR, bool SUMMED, bool MANY>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? CombineShape<NR, MANY>::BLOCKS : 2)
+    k_expert_combine(const __grid_constant__ CombineArgs a) {
+  constexpr int ITEMS = CombineShape<NR, MANY>::ITEMS, AHEAD = CombineShape<NR, MANY>::AHEAD;
   const int g = SUMMED ? blockIdx.y : blockIdx.y / a.nranks;
   const int slot0 = SUMMED ? g * a.nranks : blockIdx.y;
   const void* const* in = a.t.in + slot0;
@@ -365,17 +389,17 @@ __device__ __forceinline__ void token_sums(float (&v)[kDots], int tpr, int slot,
     for (int i = 0; i < kDots; ++i) red[turn][i][warp] = v[i];
   if (blockDim.x == tpr || blockDim.x > 15 * tpr) __syncthreads();
   else asm volatile("bar.sync %0, %1;" ::"r"(1 + slot), "r"(tpr) : "memory");
-  const int first = warp & ~(warps - 1), t = threadIdx.x & (tpr - 1);
-  if (t < kDots) {  // (thread t has the t-th sum)
-    float s = red[turn][t][first];
-    for (int i = 1; i < warps; ++i) s += red[turn][t][first + i];
+  const int first = warp & ~(warps - 1), i = threadIdx.x & (tpr - 1);
+  if (i < kDots) {  // (thread i has the i-th sum)
+    float s = red[turn][i][first];
+    for (int w = 1; w < warps; ++w) s += red[turn][i][first + w];
     v[0] = s;
   }
 }
 
 // A token belongs to `tpr` threads, which keep its gradient in registers; grid y: groups.
 template <typename T, int NR, int VPT, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS == 1024 ? 1 : 2)
+__global__ void __launch_bounds__(THREADS, THREADS == 1024 ? 1 : VPT == 1 && NR > 0 && NR <= 2 && sizeof(T) == 2 ? 3 : 2)
     k_expert_combine_backward(const __grid_constant__ CombineBwdArgs a) {
   __shared__ float red[2][kDots][32];
   const int g = blockIdx.y;
@@ -402,32 +426,21 @@ __global__ void __launch_bounds__(THREADS, THREADS == 1024 ? 1 : 2)
         row[k] = live && k0 + k < a.choices ? a.row_of[at + k0 + k] : -1;
         if (row[k] >= a.rows) row[k] = -1;
       }
-      if (a.dgates) {
-        float dot[kDots];
+      float dot[kDots];
 #pragma unroll
-        for (int k = 0; k < kDots; ++k) {
-          dot[k] = 0.0f;
-          if (row[k] < 0) continue;
+      for (int k = 0; k < kDots; ++k) {
+        dot[k] = 0.0f;
+        if (row[k] < 0 || !a.dgates) continue;
 #pragma unroll
-          for (int i = 0; i < VPT; ++i) {
-            const int c = tt + i * tpr;
-            if (c < a.nchunks) {
-              float f[kChunk], o[kChunk];
-              sum_all<T, NR>(in, a.nranks, static_cast<int64_t>(row[k]) * a.nchunks + c, f);
-              d[i].get(o);
+        for (int i = 0; i < VPT; ++i) {
+          const int c = tt + i * tpr;
+          if (c < a.nchunks) {
+            float f[kChunk], o[kChunk];
+            sum_all<T, NR>(in, a.nranks, static_cast<int64_t>(row[k]) * a.nchunks + c, f);
+            d[i].get(o);
 #pragma unroll
-              for (int j = 0; j < kChunk; ++j) dot[k] = fmaf(f[j], o[j], dot[k]);
-            }
+            for (int j = 0; j < kChunk; ++j) dot[k] = fmaf(f[j], o[j], dot[k]);
           }
-        }
-        token_sums(dot, tpr, slot, red, turn);
-        turn ^= 1;
-        if (tpr == 32) {
-#pragma unroll
-          for (int k = 0; k < kDots; ++k)
-            if (live && tt == k && k0 + k < a.choices) a.dgates[at + k0 + k] = dot[k];
-        } else if (live && tt < kDots && k0 + tt < a.choices) {
-          a.dgates[at + k0 + tt] = dot[0];
         }
       }
 #pragma unroll
@@ -448,6 +461,17 @@ __global__ void __launch_bounds__(THREADS, THREADS == 1024 ? 1 : 2)
           }
         }
       }
+      if (a.dgates) {
+        token_sums(dot, tpr, slot, red, turn);
+        turn ^= 1;
+        if (tpr == 32) {
+#pragma unroll
+          for (int k = 0; k < kDots; ++k)
+            if (live && tt == k && k0 + k < a.choices) a.dgates[at + k0 + k] = dot[k];
+        } else if (live && tt < kDots && k0 + tt < a.choices) {
+          a.dgates[at + k0 + tt] = dot[0];
+        }
+      }
     }
   }
 }
@@ -459,18 +483,20 @@ int blocks_for(int64_t items) {
   return static_cast<int>(want < most ? want : most);
 }
 
-template <typename T, int NR, bool SUMMED>
+template <typename T, int NR, bool SUMMED, bool MANY = false>
 cudaError_t combine_go(const CombineArgs& a, int ngroups, cudaStream_t s) {
-  constexpr int ITEMS = CombineShape<NR>::ITEMS;
+  constexpr int ITEMS = CombineShape<NR, MANY>::ITEMS;
   const dim3 grid(blocks_for((a.tokens * a.nchunks + ITEMS - 1) / ITEMS), SUMMED ? ngroups : ngroups * a.nranks);
-  k_expert_combine<T, NR, SUMMED><<<grid, kThreads, 0, s>>>(a);
+  k_expert_combine<T, NR, SUMMED, MANY><<<grid, kThreads, 0, s>>>(a);
   count_launch();
   return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t combine_ranks(const CombineArgs& a, bool summed, int ngroups, cudaStream_t s) {
-  if (!summed) return combine_go<T, 1, false>(a, ngroups, s);
+  const bool many = a.choices > 2;
+  if (!summed) return many ? combine_go<T, 1, false, true>(a, ngroups, s) : combine_go<T, 1, false>(a, ngroups, s);
+  if (a.nranks == 1 && many) return combine_go<T, 1, true, true>(a, ngroups, s);
   return with_ranks<1, 2, 3, 4, 8>(a.nranks, [&](auto n) { return combine_go<T, n.value, true>(a, ngroups, s); });
 }
 
@@ -512,7 +538,7 @@ cudaError_t launch_expert_sort(const ExpertSortLaunch& L, cudaStream_t s) {
   a.nranks = L.nranks;
   a.tile = L.experts < kSortTile ? (L.experts > 0 ? L.experts : 1) : kSortTile;
   // One CTA, of as many threads as there are choices or experts, or eight.
-  const int ctas = L.n <= 4 * kSortThreads ? 1 : 8;
+  const int ctas = L.n <= kSortThreads ? 1 : L.n <= 32 * kSortThreads ? 8 : 16;
   const int64_t wide = L.n > L.experts ? L.n : L.experts;
   const int threads = ctas > 1 || wide >= kSortThreads ? kSortThreads : wide <= 128 ? 128 : static_cast<int>((wide + 31) / 32 * 32);
   const int most = kSortSmem / (4 * a.tile) - 2, filled = static_cast<int>(L.n < kSortThreads ? (L.n + 31) / 32 : kSortWarps);
@@ -530,6 +556,8 @@ cudaError_t launch_expert_sort(const ExpertSortLaunch& L, cudaStream_t s) {
   const bool kept = dev >= 0 && dev < 64;
   if (!kept || !leave[L.index64][dev].load(std::memory_order_acquire)) {
     e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     if (kept) leave[L.index64][dev].store(true, std::memory_order_release);
   }

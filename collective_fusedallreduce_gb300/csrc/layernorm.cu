@@ -48,9 +48,29 @@ __device__ __forceinline__ int warp_columns(int w, int tpr, int nchunks, int vpt
 }
 
 // Rows of up to 4096 columns have one chunk a thread, up to 8192 two; wider ones have 1024 threads and two or four.
+// AHEAD: few ranks' rows are loaded a row ahead, by blocks that stay and walk the rows.
 template <typename T, int NR, int VPT, int THREADS>
 struct NormShape {
+  static constexpr bool AHEAD = NR > 0 && VPT * (NR + 1) * sizeof(T) <= 8;
   static constexpr int BLOCKS = THREADS == 1024 ? 1 : VPT == 1 && NR > 0 && sizeof(T) == 2 ? 3 : 2;
+};
+
+// A thread's part of the rows of NR ranks and the residual, as loaded.
+template <typename T, int NR, int VPT>
+struct RowPart {
+  Chunk<T> v[VPT][NR + 1];
+  __device__ __forceinline__ void load(const void* const* in, const void* residual, bool live, int64_t c0, int t, int tpr,
+                                       int nchunks) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = t + i * tpr;
+      if (live && c < nchunks) {
+#pragma unroll
+        for (int r = 0; r < NR; ++r) v[i][r].load(in[r], c0 + c);
+        if (residual) v[i][NR].load(residual, c0 + c);
+      }
+    }
+  }
 };
 
 // Grid x: rows (blockDim / tpr a block), grid y: groups.
@@ -62,7 +82,7 @@ __global__ void __launch_bounds__(THREADS, NormShape<T, NR, VPT, THREADS>::BLOCK
   const int g = blockIdx.y;
   const int tpr = 1 << a.tpr_log2;
   const int t = threadIdx.x & (tpr - 1), slot = threadIdx.x >> a.tpr_log2, rpb = blockDim.x >> a.tpr_log2;
-  const int warp = threadIdx.x >> 5, warps = tpr >> 5, first = warp & ~(warps - 1);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = tpr >> 5, first = warp & ~(warps - 1);
   const void* const* in = a.t.in + g * a.nranks;
   const void* residual = a.t.residual[g];
   const int nhidden = a.t.nhidden[g], nnormed = a.t.nnormed[g];
@@ -73,12 +93,18 @@ __global__ void __launch_bounds__(THREADS, NormShape<T, NR, VPT, THREADS>::BLOCK
   const float inv_n = mine_n ? 1.0f / static_cast<float>(mine_n) : 0.0f;
   if (t % 32 == 0 && slot == 0) counts[warp] = static_cast<float>(mine_n);  // (read behind a row's barrier)
   int turn = 0;
+  using S = NormShape<T, NR, VPT, THREADS>;
+  RowPart<T, S::AHEAD ? NR : 0, S::AHEAD ? VPT : 1> part;
+  if constexpr (S::AHEAD) {
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * rpb + slot;
+    part.load(in, residual, row < a.rows, row * a.nchunks, t, tpr, a.nchunks);
+  }
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * rpb; base < a.rows;
        base += static_cast<int64_t>(gridDim.x) * rpb, turn ^= 1) {
     const int64_t row = base + slot;
     const bool live = row < a.rows;
     const int64_t c0 = row * a.nchunks;
-    if constexpr (VPT > 1) {
+    if constexpr (VPT > 1 && !S::AHEAD) {
       // A row that a later block will take is brought to L2 meanwhile: a row's loads, its barrier and its stores do not
       // overlap, and there are few rows on an SM.
       const int64_t ahead = row + a.ahead;
@@ -98,11 +124,22 @@ __global__ void __launch_bounds__(THREADS, NormShape<T, NR, VPT, THREADS>::BLOCK
     for (int i = 0; i < VPT; ++i) {
       const int c = t + i * tpr;
       if (live && c < a.nchunks) {
+        float f[kChunk];
         Chunk<T> res;
-        if (residual) res.load(residual, c0 + c);
-        sum_all<T, NR>(in, a.nranks, c0 + c, h[i]);
+        if constexpr (S::AHEAD) {
+          part.v[i][0].get(h[i]);
+#pragma unroll
+          for (int r = 1; r < NR; ++r) {
+            part.v[i][r].get(f);
+#pragma unroll
+            for (int j = 0; j < kChunk; ++j) h[i][j] += f[j];
+          }
+          res = part.v[i][NR];
+        } else {
+          if (residual) res.load(residual, c0 + c);
+          sum_all<T, NR>(in, a.nranks, c0 + c, h[i]);
+        }
         if (residual) {
-          float f[kChunk];
           res.get(f);
 #pragma unroll
           for (int j = 0; j < kChunk; ++j) h[i][j] += f[j];
@@ -114,6 +151,10 @@ __global__ void __launch_bounds__(THREADS, NormShape<T, NR, VPT, THREADS>::BLOCK
         for (int j = 0; j < kChunk; ++j) h[i][j] = 0.0f;
       }
     }
+    if constexpr (S::AHEAD) {
+      const int64_t next = row + static_cast<int64_t>(gridDim.x) * rpb;
+      part.load(in, residual, next < a.rows, next * a.nchunks, t, tpr, a.nchunks);
+    }
     float mean = warp_sum(s) * inv_n, q = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
@@ -124,17 +165,15 @@ __global__ void __launch_bounds__(THREADS, NormShape<T, NR, VPT, THREADS>::BLOCK
     if (warps > 1) {
       if ((threadIdx.x & 31) == 0) red[turn][warp] = make_float2(mean, q);
       __syncthreads();
-      // (the joint mean as warp 0's and a correction, which leaves a mean far from zero its last bits)
+      // Lane i has warp i's pair, and the sums over the warps are shuffles (a loop over sixteen pairs was half of a row's
+      // instructions). The joint mean is warp 0's and a correction, which leaves a mean far from zero its last bits.
+      const bool has = lane < filled;
+      const float2 p = has ? red[turn][first + lane] : make_float2(0.0f, 0.0f);
+      const float n = has ? counts[lane] : 0.0f;
       const float m0 = red[turn][first].x;
-      float m = 0.0f;
-      for (int i = 1; i < filled; ++i) m = fmaf(red[turn][first + i].x - m0, counts[i], m);
-      mean = fmaf(m, inv_cols, m0);
-      q = 0.0f;
-      for (int i = 0; i < filled; ++i) {
-        const float2 p = red[turn][first + i];
-        const float d = p.x - mean;
-        q += fmaf(d * d, counts[i], p.y);
-      }
+      mean = fmaf(warp_sum(has ? (p.x - m0) * n : 0.0f), inv_cols, m0);
+      const float d = p.x - mean;
+      q = warp_sum(has ? fmaf(d * d, n, p.y) : 0.0f);
     }
     const float rstd = rsqrtf(fmaf(q, inv_cols, a.eps));
     if (live && t == 0) {
@@ -193,8 +232,12 @@ cudaError_t norm_go(LayerNormArgs& a, bool fp8, int ngroups, cudaStream_t s) {
   const int tpr = 1 << a.tpr_log2;
   const int threads = THREADS == 1024 ? 1024 : tpr < 256 ? 256 : tpr, rpb = threads / tpr;
   const int64_t blocks = (a.rows + rpb - 1) / rpb;
-  const dim3 grid(static_cast<unsigned>(blocks < (1 << 30) ? blocks : (1 << 30)), ngroups);
-  a.ahead = sm_count() * NormShape<T, NR, VPT, THREADS>::BLOCKS * rpb;
+  using S = NormShape<T, NR, VPT, THREADS>;
+  // (AHEAD: as many blocks as stay on the device; else one for each step)
+  int64_t most = S::AHEAD ? sm_count() * S::BLOCKS * (THREADS / threads) / ngroups : 1 << 30;
+  if (most < 1) most = 1;
+  const dim3 grid(static_cast<unsigned>(blocks < most ? blocks : most), ngroups);
+  a.ahead = sm_count() * S::BLOCKS * rpb;
   if (fp8) k_allreduce_layernorm<T, NR, VPT, THREADS, true><<<grid, threads, 0, s>>>(a);
   else k_allreduce_layernorm<T, NR, VPT, THREADS, false><<<grid, threads, 0, s>>>(a);
   count_launch();

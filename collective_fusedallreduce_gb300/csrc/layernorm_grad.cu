@@ -43,13 +43,10 @@ __device__ __forceinline__ float2 row_sum2(float2 v, int tpr, int slot, float2 (
   if ((threadIdx.x & 31) == 0) red[turn][warp] = v;
   if (blockDim.x == tpr || blockDim.x > 15 * tpr) __syncthreads();
   else asm volatile("bar.sync %0, %1;" ::"r"(1 + slot), "r"(tpr) : "memory");
-  const int first = warp & ~(warps - 1);
-  float2 s = red[turn][first];
-  for (int i = 1; i < warps; ++i) {
-    s.x += red[turn][first + i].x;
-    s.y += red[turn][first + i].y;
-  }
-  return s;
+  // (lane i has warp i's: shuffles again, in place of a loop over the warps)
+  const int lane = threadIdx.x & 31, first = warp & ~(warps - 1);
+  const float2 s = lane < warps ? red[turn][first + lane] : make_float2(0.0f, 0.0f);
+  return make_float2(warp_sum(s.x), warp_sum(s.y));
 }
 
 // THREADS and blocks an SM: 16-bit rows of up to 8192 columns have two blocks of 512 threads, wider ones 1024 threads a
