@@ -489,13 +489,23 @@ def coco_grouped_einsum(spec, lhs, lhs_scales, rhs, rhs_scales, offsets, out, st
 
 
 def _check_here(what, *tensors):
-    """_check_device, and refuses another device than the current one, on which the call runs."""
-    _check_device(what, *tensors)
-    here = torch.cuda.current_device()
+    """Refuses host memory and any device but the current one, on which the call runs; of lists the first tensor stands
+    for all, as in _check_device (this is one look at each)."""
+    here = None
     for t in tensors:
-        t = t.tensors[0] if type(t) is Dist else t[0] if type(t) is list and t else t
-        if t is not None and t.get_device() != here:
-            raise CocoError(7, f"{what}: a tensor of another device than the current one")
+        kind = type(t)
+        if kind is Dist:
+            t = t.tensors[0]
+        elif kind is list:
+            t = t[0] if t else None
+        if t is not None:
+            at = t.get_device()
+            if at < 0:
+                raise CocoError(7, f"{what}: a tensor that is not in device memory")
+            if at != here:
+                if here is not None or at != torch.cuda.current_device():
+                    raise CocoError(7, f"{what}: a tensor of another device than the current one")
+                here = at
 
 
 def _pointer(t, dtype, numel, what):

@@ -223,32 +223,45 @@ struct DispatchArgs {
   int64_t tokens, rows;
   int32_t choices, nranks;
   int32_t nvec, nscales;  // 16-byte vectors of a row, scales of a row
+  int32_t tpr_log2;
 };
 
-// Grid x: a token's vectors and then its scales, token after token; grid y: groups.
+// A token belongs to `tpr` threads (blockDim / tpr tokens a block) of each of the blocks of grid z, which hold kHeld of
+// its vectors each at a time and write them to one choice's row after another; grid y: groups.
+constexpr int kHeld = 2;
+
 __global__ void __launch_bounds__(kThreads) k_expert_dispatch(const __grid_constant__ DispatchArgs a) {
   const int g = blockIdx.y;
-  const char* x = static_cast<const char*>(a.t.in[g]);
+  const int tpr = 1 << a.tpr_log2;
+  const int tt = threadIdx.x & (tpr - 1), slot = threadIdx.x >> a.tpr_log2, rpb = kThreads >> a.tpr_log2;
   const float* scales = a.t.in_scales[g];
-  const int32_t* row_of = a.row_of + g * a.tokens * a.choices;
-  const int per = a.nvec + a.nscales, nout = a.t.nout[g], slot0 = g * a.nranks;
-  const int64_t total = a.tokens * per, step = static_cast<int64_t>(gridDim.x) * kThreads;
-  for (int64_t p = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; p < total; p += step) {
-    const int64_t t = total <= 0x7fffffff ? static_cast<uint32_t>(p) / static_cast<uint32_t>(per) : p / per;
-    const int c = static_cast<int>(p - t * per);
-    if (c < a.nvec) {
-      const uint4 v = ld_stream(x + (t * a.nvec + c) * 16);
+  const int nout = a.t.nout[g], slot0 = g * a.nranks;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * rpb + slot; t < a.tokens;
+       t += static_cast<int64_t>(gridDim.x) * rpb) {
+    const char* x = static_cast<const char*>(a.t.in[g]) + t * a.nvec * 16;
+    const int32_t* row_of = a.row_of + (g * a.tokens + t) * a.choices;
+    for (int c0 = blockIdx.z * kHeld * tpr + tt; c0 < a.nvec; c0 += gridDim.z * kHeld * tpr) {
+      uint4 v[kHeld];
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i)
+        if (c0 + i * tpr < a.nvec) v[i] = ld_stream(x + static_cast<int64_t>(c0 + i * tpr) * 16);
       for (int k = 0; k < a.choices; ++k) {
-        const int64_t row = row_of[t * a.choices + k];
-        if (row >= 0 && row < a.rows)
-          for (int q = 0; q < nout; ++q) __stcs(static_cast<uint4*>(a.t.out[slot0 + q]) + row * a.nvec + c, v);
+        const int64_t row = row_of[k];
+        if (row < 0 || row >= a.rows) continue;
+        for (int q = 0; q < nout; ++q) {
+          uint4* to = static_cast<uint4*>(a.t.out[slot0 + q]) + row * a.nvec + c0;
+#pragma unroll
+          for (int i = 0; i < kHeld; ++i)
+            if (c0 + i * tpr < a.nvec) __stcs(to + i * tpr, v[i]);
+        }
       }
-    } else {
-      const float v = scales[t * a.nscales + (c - a.nvec)];
+    }
+    for (int c = blockIdx.z * tpr + tt; c < a.nscales; c += gridDim.z * tpr) {
+      const float v = scales[t * a.nscales + c];
       for (int k = 0; k < a.choices; ++k) {
-        const int64_t row = row_of[t * a.choices + k];
+        const int64_t row = row_of[k];
         if (row >= 0 && row < a.rows)
-          for (int q = 0; q < nout; ++q) a.t.out_scales[slot0 + q][row * a.nscales + (c - a.nvec)] = v;
+          for (int q = 0; q < nout; ++q) a.t.out_scales[slot0 + q][row * a.nscales + c] = v;
       }
     }
   }
@@ -256,110 +269,114 @@ __global__ void __launch_bounds__(kThreads) k_expert_dispatch(const __grid_const
 
 // ----------------------------------------------------------------- combine
 
+// sum_all in pairs.
+template <typename T, int NR>
+__device__ __forceinline__ Vec8 sum_vec(const void* const* in, int nranks, int64_t c) {
+  Vec8 s;
+  if constexpr (NR > 0) {
+    Chunk<T> raw[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) raw[r].load(in[r], c);
+    s = values<T>(raw[0]);
+#pragma unroll
+    for (int r = 1; r < NR; ++r) s = s + values<T>(raw[r]);
+  } else {
+    s = splat8(-0.0f);  // (added to anything, it leaves that as it is)
+    for (int r0 = 0; r0 < nranks; r0 += 4) {
+      Chunk<T> raw[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (r0 + r < nranks) raw[r].load(in[r0 + r], c);
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (r0 + r < nranks) s = s + values<T>(raw[r]);
+    }
+  }
+  return s;
+}
+
 struct CombineArgs {
   ExpertTables t;
   const int32_t* row_of;  // [groups][tokens][choices]
   const float* gates;     // the same shape, or null (ones)
   int64_t tokens, rows;
   int32_t choices, nranks, nchunks;
+  int32_t tpr_log2;
 };
 
-// How many positions a thread takes and how many choices at a time, so that some loads are under way. MANY: more than two
+// How many chunks a thread takes and how many choices at a time, so that some loads are under way. MANY: more than two
 // choices.
 template <int NR, bool MANY>
 struct CombineShape {
   static constexpr int ITEMS = NR == 1 && !MANY ? 2 : 1;
   static constexpr int AHEAD = NR == 1 && MANY ? 4 : NR == 8 || NR == 0 ? 1 : 2;
-  static constexpr int BLOCKS = NR == 1 && MANY ? 5 : 4;
 };
 
-// SUMMED: grid y counts groups, whose ranks' rows are added up, with the residual, for every distinct output. Otherwise
-// it counts ranks, each with an output of its own (NR is 1). Grid x: chunks of 8 columns, token after token. A choice's
-// rows are added over the ranks first (in order), then weighted; product and sum are rounded one by one.
+// A token belongs to `tpr` threads (blockDim / tpr tokens a block) of each of the blocks of grid z. SUMMED: grid y counts groups, whose ranks' rows are
+// added up, with the residual, for every distinct output. Otherwise it counts ranks, each with an output of its own (NR is
+// 1). A choice's rows are added over the ranks first (in order), then weighted; product and sum are rounded one by one.
 template <typename T, int NR, bool SUMMED, bool MANY>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? CombineShape<NR, MANY>::BLOCKS : 2)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
     k_expert_combine(const __grid_constant__ CombineArgs a) {
   constexpr int ITEMS = CombineShape<NR, MANY>::ITEMS, AHEAD = CombineShape<NR, MANY>::AHEAD;
   const int g = SUMMED ? blockIdx.y : blockIdx.y / a.nranks;
   const int slot0 = SUMMED ? g * a.nranks : blockIdx.y;
+  const int tpr = 1 << a.tpr_log2;
+  const int tt = threadIdx.x & (tpr - 1), slot = threadIdx.x >> a.tpr_log2, rpb = kThreads >> a.tpr_log2;
   const void* const* in = a.t.in + slot0;
   const void* residual = SUMMED ? a.t.residual[g] : nullptr;
   const int nout = SUMMED ? a.t.nout[g] : 1;
-  const int32_t* row_of = a.row_of + g * a.tokens * a.choices;
-  const float* gates = a.gates ? a.gates + g * a.tokens * a.choices : nullptr;
-  const int64_t total = a.tokens * a.nchunks, step = static_cast<int64_t>(gridDim.x) * kThreads * ITEMS;
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * kThreads * ITEMS + threadIdx.x; base < total; base += step) {
-    int64_t first[ITEMS];  // a position's first choice, or -1
-    int32_t c[ITEMS];
-    Chunk<T> res[ITEMS];
-    float acc[ITEMS][kChunk];
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * rpb + slot; t < a.tokens;
+       t += static_cast<int64_t>(gridDim.x) * rpb) {
+    const int64_t at = (g * a.tokens + t) * a.choices;
+    for (int c0 = blockIdx.z * ITEMS * tpr + tt; c0 < a.nchunks; c0 += gridDim.z * ITEMS * tpr) {
+      Chunk<T> res[ITEMS];
+      Vec8 acc[ITEMS];
 #pragma unroll
-    for (int u = 0; u < ITEMS; ++u) {
-      const int64_t p = base + u * kThreads;
-      const int64_t t = total <= 0x7fffffff ? static_cast<uint32_t>(p) / static_cast<uint32_t>(a.nchunks) : p / a.nchunks;
-      c[u] = static_cast<int32_t>(p - t * a.nchunks);
-      first[u] = p < total ? t * a.choices : -1;
-      if (p < total && residual) res[u].load(residual, p);
-#pragma unroll
-      for (int j = 0; j < kChunk; ++j) acc[u][j] = 0.0f;
-    }
-    for (int k0 = 0; k0 < a.choices; k0 += AHEAD) {
-      int32_t row[ITEMS][AHEAD];
-      float w[ITEMS][AHEAD];
-#pragma unroll
-      for (int u = 0; u < ITEMS; ++u)
+      for (int u = 0; u < ITEMS; ++u) {
+        if (residual && c0 + u * tpr < a.nchunks) res[u].load(residual, t * a.nchunks + c0 + u * tpr);
+        acc[u] = splat8(0.0f);
+      }
+      for (int k0 = 0; k0 < a.choices; k0 += AHEAD) {
+        int32_t row[AHEAD];
+        float w[AHEAD];
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
-          const bool has = first[u] >= 0 && k0 + k < a.choices;
-          row[u][k] = has ? row_of[first[u] + k0 + k] : -1;
-          if (row[u][k] >= a.rows) row[u][k] = -1;
-          w[u][k] = has && gates ? gates[first[u] + k0 + k] : 1.0f;
+          row[k] = k0 + k < a.choices ? a.row_of[at + k0 + k] : -1;
+          if (row[k] >= a.rows) row[k] = -1;
+          w[k] = a.gates && k0 + k < a.choices ? a.gates[at + k0 + k] : 1.0f;
         }
-      if constexpr (NR > 0) {
-        Chunk<T> raw[ITEMS][AHEAD][NR];
-#pragma unroll
-        for (int u = 0; u < ITEMS; ++u)
+        if constexpr (NR > 0) {
+          Chunk<T> raw[ITEMS][AHEAD][NR];
 #pragma unroll
           for (int k = 0; k < AHEAD; ++k)
-            if (row[u][k] >= 0)
 #pragma unroll
-              for (int r = 0; r < NR; ++r) raw[u][k][r].load(in[r], static_cast<int64_t>(row[u][k]) * a.nchunks + c[u]);
+            for (int u = 0; u < ITEMS; ++u)
+              if (row[k] >= 0 && c0 + u * tpr < a.nchunks)
 #pragma unroll
-        for (int u = 0; u < ITEMS; ++u)
+                for (int r = 0; r < NR; ++r)
+                  raw[u][k][r].load(in[r], static_cast<int64_t>(row[k]) * a.nchunks + c0 + u * tpr);
 #pragma unroll
           for (int k = 0; k < AHEAD; ++k)
-            if (row[u][k] >= 0) {
-              float s[kChunk], f[kChunk];
-              raw[u][k][0].get(s);
 #pragma unroll
-              for (int r = 1; r < NR; ++r) {
-                raw[u][k][r].get(f);
+            for (int u = 0; u < ITEMS; ++u)
+              if (row[k] >= 0 && c0 + u * tpr < a.nchunks) {
+                Vec8 s = values<T>(raw[u][k][0]);
 #pragma unroll
-                for (int j = 0; j < kChunk; ++j) s[j] += f[j];
+                for (int r = 1; r < NR; ++r) s = s + values<T>(raw[u][k][r]);
+                acc[u] = acc[u] + s * splat8(w[k]);
               }
-#pragma unroll
-              for (int j = 0; j < kChunk; ++j) acc[u][j] = __fadd_rn(acc[u][j], __fmul_rn(s[j], w[u][k]));
-            }
-      } else if (row[0][0] >= 0) {
-        float s[kChunk];
-        sum_all<T, 0>(in, a.nranks, static_cast<int64_t>(row[0][0]) * a.nchunks + c[0], s);
-#pragma unroll
-        for (int j = 0; j < kChunk; ++j) acc[0][j] = __fadd_rn(acc[0][j], __fmul_rn(s[j], w[0][0]));
+        } else if (row[0] >= 0) {
+          acc[0] = acc[0] + sum_vec<T, 0>(in, a.nranks, static_cast<int64_t>(row[0]) * a.nchunks + c0) * splat8(w[0]);
+        }
       }
-    }
 #pragma unroll
-    for (int u = 0; u < ITEMS; ++u) {
-      const int64_t p = base + u * kThreads;
-      if (p >= total) break;
-      if (residual) {
-        float f[kChunk];
-        res[u].get(f);
-#pragma unroll
-        for (int j = 0; j < kChunk; ++j) acc[u][j] += f[j];
+      for (int u = 0; u < ITEMS; ++u) {
+        if (c0 + u * tpr >= a.nchunks) break;
+        if (residual) acc[u] = acc[u] + values<T>(res[u]);
+        const Chunk<T> o = rounded<T>(acc[u]);
+        for (int q = 0; q < nout; ++q) o.store(a.t.out[slot0 + q], t * a.nchunks + c0 + u * tpr);
       }
-      Chunk<T> o;
-      o.put(acc[u]);
-      for (int q = 0; q < nout; ++q) o.store(a.t.out[slot0 + q], p);
     }
   }
 }
@@ -435,11 +452,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 1024 ? 1 : VPT == 1 && NR 
         for (int i = 0; i < VPT; ++i) {
           const int c = tt + i * tpr;
           if (c < a.nchunks) {
-            float f[kChunk], o[kChunk];
-            sum_all<T, NR>(in, a.nranks, static_cast<int64_t>(row[k]) * a.nchunks + c, f);
-            d[i].get(o);
-#pragma unroll
-            for (int j = 0; j < kChunk; ++j) dot[k] = fmaf(f[j], o[j], dot[k]);
+            const Vec8 f = sum_vec<T, NR>(in, a.nranks, static_cast<int64_t>(row[k]) * a.nchunks + c);
+            dot[k] += sum8(f * values<T>(d[i]));
           }
         }
       }
@@ -451,12 +465,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 1024 ? 1 : VPT == 1 && NR 
         for (int i = 0; i < VPT; ++i) {
           const int c = tt + i * tpr;
           if (c < a.nchunks) {
-            float o[kChunk];
-            d[i].get(o);
-#pragma unroll
-            for (int j = 0; j < kChunk; ++j) o[j] *= w;
-            Chunk<T> ov;
-            ov.put(o);
+            const Chunk<T> ov = rounded<T>(values<T>(d[i]) * splat8(w));
             for (int q = 0; q < nout; ++q) ov.store(a.t.out[slot0 + q], static_cast<int64_t>(row[k]) * a.nchunks + c);
           }
         }
@@ -478,22 +487,37 @@ __global__ void __launch_bounds__(THREADS, THREADS == 1024 ? 1 : VPT == 1 && NR 
 
 // --------------------------------------------------------------- launchers
 
-int blocks_for(int64_t items) {
-  const int64_t want = (items + kThreads - 1) / kThreads, most = 1 << 30;
+// Threads of a token: a power of two for `items` steps, a warp to a block; and the blocks for all tokens.
+int token_threads_log2(int64_t items) {
+  int log2 = 5;
+  while ((1 << log2) < items && (1 << log2) < kThreads) ++log2;
+  return log2;
+}
+
+// Blocks that share a token: one for each step of its threads.
+int parts_for(int64_t columns, int step) {
+  const int64_t want = (columns + step - 1) / step;
+  return static_cast<int>(want < 1 ? 1 : want < 65535 ? want : 65535);
+}
+
+int blocks_for(int64_t tokens, int tpr_log2) {
+  const int64_t rpb = kThreads >> tpr_log2, want = (tokens + rpb - 1) / rpb, most = 1 << 30;
   return static_cast<int>(want < most ? want : most);
 }
 
 template <typename T, int NR, bool SUMMED, bool MANY = false>
-cudaError_t combine_go(const CombineArgs& a, int ngroups, cudaStream_t s) {
+cudaError_t combine_go(CombineArgs& a, int ngroups, cudaStream_t s) {
   constexpr int ITEMS = CombineShape<NR, MANY>::ITEMS;
-  const dim3 grid(blocks_for((a.tokens * a.nchunks + ITEMS - 1) / ITEMS), SUMMED ? ngroups : ngroups * a.nranks);
+  a.tpr_log2 = token_threads_log2((a.nchunks + ITEMS - 1) / ITEMS);
+  const dim3 grid(blocks_for(a.tokens, a.tpr_log2), SUMMED ? ngroups : ngroups * a.nranks,
+                  parts_for(a.nchunks, ITEMS << a.tpr_log2));
   k_expert_combine<T, NR, SUMMED, MANY><<<grid, kThreads, 0, s>>>(a);
   count_launch();
   return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t combine_ranks(const CombineArgs& a, bool summed, int ngroups, cudaStream_t s) {
+cudaError_t combine_ranks(CombineArgs& a, bool summed, int ngroups, cudaStream_t s) {
   const bool many = a.choices > 2;
   if (!summed) return many ? combine_go<T, 1, false, true>(a, ngroups, s) : combine_go<T, 1, false>(a, ngroups, s);
   if (a.nranks == 1 && many) return combine_go<T, 1, true, true>(a, ngroups, s);
@@ -587,7 +611,8 @@ cudaError_t launch_expert_dispatch(const ExpertRowsLaunch& L, cudaStream_t s) {
   a.nranks = L.nranks;
   a.nvec = static_cast<int32_t>(static_cast<int64_t>(L.cols) * dtype_size(L.dtype) / 16);
   a.nscales = L.dtype == COCO_F8E4M3 ? static_cast<int32_t>((static_cast<int64_t>(L.cols) + 127) / 128) : 0;
-  const dim3 grid(blocks_for(a.tokens * (static_cast<int64_t>(a.nvec) + a.nscales)), L.ngroups);
+  a.tpr_log2 = token_threads_log2((a.nvec + kHeld - 1) / kHeld);
+  const dim3 grid(blocks_for(a.tokens, a.tpr_log2), L.ngroups, parts_for(a.nvec, kHeld << a.tpr_log2));
   k_expert_dispatch<<<grid, kThreads, 0, s>>>(a);
   count_launch();
   return cudaGetLastError();
