@@ -337,14 +337,23 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
         if (residual && c0 + u * tpr < a.nchunks) res[u].load(residual, t * a.nchunks + c0 + u * tpr);
         acc[u] = splat8(0.0f);
       }
+      int32_t next_row[AHEAD];  // (the next choices' indexes and weights are under way with the data of these)
+      float next_w[AHEAD];
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        next_row[k] = k < a.choices ? a.row_of[at + k] : -1;
+        next_w[k] = a.gates && k < a.choices ? a.gates[at + k] : 1.0f;
+      }
       for (int k0 = 0; k0 < a.choices; k0 += AHEAD) {
         int32_t row[AHEAD];
         float w[AHEAD];
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
-          row[k] = k0 + k < a.choices ? a.row_of[at + k0 + k] : -1;
-          if (row[k] >= a.rows) row[k] = -1;
-          w[k] = a.gates && k0 + k < a.choices ? a.gates[at + k0 + k] : 1.0f;
+          row[k] = next_row[k] < a.rows ? next_row[k] : -1;
+          w[k] = next_w[k];
+          const bool more = k0 + AHEAD + k < a.choices;
+          next_row[k] = more ? a.row_of[at + k0 + AHEAD + k] : -1;
+          next_w[k] = a.gates && more ? a.gates[at + k0 + AHEAD + k] : 1.0f;
         }
         if constexpr (NR > 0) {
           Chunk<T> raw[ITEMS][AHEAD][NR];

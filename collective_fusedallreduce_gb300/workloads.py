@@ -18,11 +18,13 @@ libcoco; every arithmetic step runs in the library's kernels.
 
 and, past the pages, a mixture-of-experts layer of a tensor-parallel language
 model (N logical ranks, each with a slice of every expert's hidden dimension),
-whose products, norms and their gradients are the library's; rows are gathered,
-activated and combined by PyTorch between them:
+whose routing, products, norms and their gradients are the library's; the hidden
+units are activated by PyTorch between them:
 
 * ``moe_layer_fp8``: its forward in 8 bits, as it serves (one token or many);
-* ``moe_layer_train``: its forward and backward in 16 bits, as it trains.
+* ``moe_layer_train``: its forward and backward in 16 bits, as it trains;
+* ``moe_layer_step``: the same with a layer norm and weighted experts, its experts'
+  gradients clipped by their norm over all ranks.
 """
 
 import torch
@@ -175,6 +177,32 @@ def route(expert_of, experts):
     return order // expert_of.shape[1], row_of.view(expert_of.shape), offsets
 
 
+def sort_by_expert(expert_of, experts, ranks):
+    """``route`` by the library, for ``ranks`` ranks: (row_of_choice [tokens, choices] int32, offsets [ranks, experts + 1]
+    int32, a line per rank)."""
+    row_of = torch.empty_like(expert_of, dtype=torch.int32)
+    offsets = _empty((ranks, experts + 1), torch.int32, expert_of.device)
+    coco.coco_expert_sort(expert_of.contiguous(), experts, row_of, None, offsets)
+    return row_of, offsets
+
+
+def dispatch(x, row_of, ranks, scales=None):
+    """The rows of ``x`` [tokens, H] sorted by expert (and those of ``scales``, where x is in 8 bits), one copy for all
+    ranks. Rows that no choice names hold nothing; the products by expert do not read them."""
+    rows = _empty((row_of.numel(), x.shape[1]), x.dtype, x.device)
+    row_scales = None if scales is None else _empty((row_of.numel(), scales.shape[1]), torch.float32, x.device)
+    coco.coco_expert_dispatch(coco.replicated([x] * ranks), None if scales is None else [scales] * ranks, row_of,
+                              coco.replicated([rows] * ranks), None if scales is None else [row_scales] * ranks)
+    return rows, row_scales
+
+
+def combine(rows, row_of, gates, like):
+    """Every rank's own sum over a token's choices of gate * row (gates None: ones)."""
+    out = [torch.empty_like(like) for _ in rows]
+    coco.coco_expert_combine(coco.local(rows), row_of, gates, None, coco.local(out))
+    return out
+
+
 def _scales_like(q):
     return _empty((*q.shape[:-1], (q.shape[-1] + 127) // 128), torch.float32, q.device)
 
@@ -213,10 +241,8 @@ def moe_layer_fp8(partials, residual, weight, eps, expert_of, gates, up, up_scal
     scales)."""
     n, dev = len(partials), partials[0].device
     hidden, x, xs = norm_fp8(partials, residual, weight, eps)
-    token_of, row_of, offsets = route(expert_of, up[0].shape[0])
-    offsets = offsets.repeat(n, 1)
-    rows = x.view(torch.uint8)[token_of].view(x.dtype)
-    row_scales = xs[token_of]
+    row_of, offsets = sort_by_expert(expert_of, up[0].shape[0], n)
+    rows, row_scales = dispatch(x, row_of, n, xs)
     mid = [_empty((rows.shape[0], up[0].shape[2]), torch.bfloat16, dev) for _ in range(n)]
     coco.coco_grouped_einsum("tk,ekn->tn", coco.replicated([rows] * n), [row_scales] * n, coco.local(up), up_scales,
                              offsets, coco.local(mid))
@@ -227,8 +253,7 @@ def moe_layer_fp8(partials, residual, weight, eps, expert_of, gates, up, up_scal
     coco.coco_quantize_fp8(coco.local(mid), 1, coco.local(q), qs)
     out = [_empty((rows.shape[0], down[0].shape[2]), torch.bfloat16, dev) for _ in range(n)]
     coco.coco_grouped_einsum("tk,ekn->tn", coco.local(q), qs, coco.local(down), down_scales, offsets, coco.local(out))
-    y = [(o[row_of].float() * gates[..., None]).sum(1).to(hidden.dtype) for o in out]
-    return norm_fp8(y, hidden, next_weight, eps)
+    return norm_fp8(combine(out, row_of, gates.float().contiguous(), hidden), hidden, next_weight, eps)
 
 
 def moe_layer_train(partials, residual, weight, eps, expert_of, up, down, dout):
@@ -243,20 +268,19 @@ def moe_layer_train(partials, residual, weight, eps, expert_of, up, down, dout):
     rstd = _empty((tokens,), torch.float32, dev)
     coco.coco_allreduce_rmsnorm(coco.local(partials), coco.replicated([residual] * n), weight, eps,
                                 coco.replicated([hidden] * n), coco.replicated([x] * n), None, rstd)
-    token_of, row_of, offsets = route(expert_of, up[0].shape[0])
-    offsets = offsets.repeat(n, 1)
-    rows, f = token_of.numel(), up[0].shape[2]
-    xr = coco.replicated([x[token_of]] * n)
+    row_of, offsets = sort_by_expert(expert_of, up[0].shape[0], n)
+    rows, f = row_of.numel(), up[0].shape[2]
+    xr = coco.replicated([dispatch(x, row_of, n)[0]] * n)
     mid = [_empty((rows, f), dt, dev) for _ in range(n)]
     coco.coco_grouped_einsum("tk,ekn->tn", xr, None, coco.local(up), None, offsets, coco.local(mid))
     act = [m.relu() for m in mid]
     y = [_empty((rows, hid), dt, dev) for _ in range(n)]
     coco.coco_grouped_einsum("tk,ekn->tn", coco.local(act), None, coco.local(down), None, offsets, coco.local(y))
     out = torch.empty_like(hidden)
-    coco.coco_fused_allreduce(coco.local([o[row_of].float().sum(1).to(dt) for o in y]), None,
+    coco.coco_fused_allreduce(coco.local(combine(y, row_of, None, hidden)), None,
                               coco.replicated([hidden] * n), 0.0, 0, coco.replicated([out] * n))
     # backward: every rank's part of the sum has the gradient dout
-    drow = coco.replicated([dout[token_of]] * n)
+    drow = coco.replicated([dispatch(dout, row_of, n)[0]] * n)
     ddown, dact = [torch.empty_like(w) for w in down], [torch.empty_like(m) for m in mid]
     coco.coco_grouped_einsum("tk,tn->ekn", coco.local(act), None, drow, None, offsets, coco.local(ddown))
     coco.coco_grouped_einsum("tk,enk->tn", drow, None, coco.local(down), None, offsets, coco.local(dact))
@@ -264,11 +288,78 @@ def moe_layer_train(partials, residual, weight, eps, expert_of, up, down, dout):
     dup, dxr = [torch.empty_like(w) for w in up], [_empty((rows, hid), dt, dev) for _ in range(n)]
     coco.coco_grouped_einsum("tk,tn->ekn", xr, None, dmid, None, offsets, coco.local(dup))
     coco.coco_grouped_einsum("tk,enk->tn", dmid, None, coco.local(up), None, offsets, coco.local(dxr))
-    dnormed = [d[row_of].float().sum(1).to(dt) for d in dxr]
+    dnormed = combine(dxr, row_of, None, hidden)
     dx, dweight = torch.empty_like(hidden), _empty((hid,), torch.float32, dev)
     space = _empty((coco.coco_allreduce_rmsnorm_backward_bytes(tokens, hid),), torch.uint8, dev)
     coco.coco_allreduce_rmsnorm_backward(coco.local(dnormed), coco.replicated([dout] * n),
                                          coco.replicated([hidden] * n), weight, rstd, coco.replicated([dx] * n),
                                          dweight, space)
     return {"out": out, "dx": dx, "dweight": dweight, "dup": dup, "ddown": ddown, "mid": mid,
+            "row_of_choice": row_of.long()}
+
+
+def gradient_buffers(per_rank):
+    """What a training run keeps for clipping: ``per_rank[r][t]`` are rank r's gradients, whose table is built once.
+    Returns a dict for ``clip_gradients``."""
+    table = _empty((coco.coco_scattered_table_bytes([g.numel() for g in per_rank[0]], len(per_rank)),), torch.uint8,
+                   per_rank[0][0].device)
+    return {"plan": coco.coco_scattered_table_build(per_rank, table), "table": table, "grads": per_rank,
+            "norm": _empty((1,), torch.float32, table.device),
+            "space": _empty((coco.coco_scattered_clip_bytes(),), torch.uint8, table.device)}
+
+
+def clip_gradients(buffers, max_norm, layout=coco.LOCAL):
+    """Scales the gradients in place so that their norm over all ranks is at most ``max_norm``; returns the norm before
+    (one fp32, on the device)."""
+    coco.coco_scattered_clip(buffers["plan"], layout, max_norm, None, buffers["norm"], buffers["space"])
+    return buffers["norm"]
+
+
+def moe_layer_step(partials, residual, weight, bias, eps, expert_of, gates, up, down, dout, buffers, max_norm):
+    """A training step of the layer with a layer norm and weighted experts, in 16 bits:
+
+        h = AllReduce(partials) + residual,  x = layernorm(h)
+        out = h + AllReduce(y),  y_r = sum over a token's choices of gate * relu(x @ up_r[expert]) @ down_r[expert]
+
+    and, for the gradient ``dout`` of out, the gradients of each partial and of the residual (one tensor, dx), of the
+    gates, of the norm's parameters and of the experts. The last go to ``buffers`` (``gradient_buffers`` of [[dup_r, ddown_r]
+    for every rank r]) and are scaled so that their norm over all ranks is at most ``max_norm``. ``expert_of`` [tokens,
+    choices] int64 (a number outside [0, experts): that choice is dropped), ``gates`` the same shape, fp32. Returns a dict:
+    out, dx, dgates, dweight, dbias (fp32), norm (of the experts' gradients before clipping, one fp32), and what the
+    forward kept of the hidden units: mid (a row per choice, by expert) and row_of_choice (-1 for none)."""
+    n, dev = len(partials), partials[0].device
+    tokens, hid = partials[0].shape
+    dt = partials[0].dtype
+    rep = lambda t: coco.replicated([t] * n)  # noqa: E731
+    hidden, x = torch.empty_like(partials[0]), torch.empty_like(partials[0])
+    mean, rstd = _empty((tokens,), torch.float32, dev), _empty((tokens,), torch.float32, dev)
+    coco.coco_allreduce_layernorm(coco.local(partials), rep(residual), weight, bias, eps, rep(hidden), rep(x), None, mean,
+                                  rstd)
+    row_of, offsets = sort_by_expert(expert_of, up[0].shape[0], n)
+    rows, f = row_of.numel(), up[0].shape[2]
+    xr = rep(dispatch(x, row_of, n)[0])
+    mid = [_empty((rows, f), dt, dev) for _ in range(n)]
+    coco.coco_grouped_einsum("tk,ekn->tn", xr, None, coco.local(up), None, offsets, coco.local(mid))
+    act = [m.relu() for m in mid]
+    y = [_empty((rows, hid), dt, dev) for _ in range(n)]
+    coco.coco_grouped_einsum("tk,ekn->tn", coco.local(act), None, coco.local(down), None, offsets, coco.local(y))
+    out = torch.empty_like(hidden)
+    coco.coco_expert_combine(coco.local(y), row_of, gates, rep(hidden), rep(out))
+    # backward: of the experts' rows and the gates, through the products, back to the tokens, through the norm
+    dup, ddown = ([g[i] for g in buffers["grads"]] for i in range(2))
+    drow, dgates = _empty((rows, hid), dt, dev), torch.empty_like(gates)
+    coco.coco_expert_combine_backward(rep(dout), coco.local(y), row_of, gates, rep(drow), dgates)
+    dact = [torch.empty_like(m) for m in mid]
+    coco.coco_grouped_einsum("tk,tn->ekn", coco.local(act), None, rep(drow), None, offsets, coco.local(ddown))
+    coco.coco_grouped_einsum("tk,enk->tn", rep(drow), None, coco.local(down), None, offsets, coco.local(dact))
+    dmid = coco.local([torch.where(m > 0, d, torch.zeros_like(d)) for m, d in zip(mid, dact)])
+    dxr = [_empty((rows, hid), dt, dev) for _ in range(n)]
+    coco.coco_grouped_einsum("tk,tn->ekn", xr, None, dmid, None, offsets, coco.local(dup))
+    coco.coco_grouped_einsum("tk,enk->tn", dmid, None, coco.local(up), None, offsets, coco.local(dxr))
+    dx, dweight, dbias = torch.empty_like(hidden), _empty((hid,), torch.float32, dev), _empty((hid,), torch.float32, dev)
+    space = _empty((coco.coco_allreduce_layernorm_backward_bytes(tokens, hid),), torch.uint8, dev)
+    coco.coco_allreduce_layernorm_backward(coco.local(combine(dxr, row_of, None, hidden)), rep(dout), rep(hidden), weight,
+                                           mean, rstd, rep(dx), dweight, dbias, space)
+    norm = clip_gradients(buffers, max_norm)
+    return {"out": out, "dx": dx, "dgates": dgates, "dweight": dweight, "dbias": dbias, "norm": norm, "mid": mid,
             "row_of_choice": row_of}
