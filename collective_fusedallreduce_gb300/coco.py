@@ -496,7 +496,7 @@ def _check_here(what, *tensors):
         kind = type(t)
         if kind is Dist:
             t = t.tensors[0]
-        elif kind is list:
+        elif kind is list or kind is tuple:
             t = t[0] if t else None
         if t is not None:
             at = t.get_device()
@@ -629,7 +629,7 @@ def _clip(name, plan, second, max_norm, out, norm, workspace, stream):
     if not workspace.is_contiguous():
         raise CocoError(2, name)
     _check_here(name, norm, workspace)
-    _check(getattr(_lib, name)(ctypes.byref(plan), second, max_norm, None if out is None else ctypes.byref(out), n,
+    _check(getattr(_lib, name)(ctypes.byref(plan), second, float(max_norm), None if out is None else ctypes.byref(out), n,
                                workspace.data_ptr(), workspace.nbytes, _stream(stream)), name)
 
 

@@ -267,7 +267,7 @@ __device__ __forceinline__ double squares_end(const ClipArgs& a, int64_t b, uint
 // the ranks' tensors are added in rank order, scaled by alpha, rounded to U and stored to out's rank 0, and it is those
 // values' norm. Where the two tables' tensors do not have a bucket in common, nothing is written and the norm is NaN.
 template <typename T, typename U, int MODE, int NR>
-__global__ void __launch_bounds__(kThreads, MODE == CLIP_SUM ? (NR == 8 ? 3 : 4) : sizeof(T) == 2 ? 6 : 4)
+__global__ void __launch_bounds__(kThreads, MODE == CLIP_SUM ? 2 : 4)
     k_clip_squares(const __grid_constant__ ClipArgs a) {
   __shared__ double red[kWarps];
   const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
@@ -292,6 +292,7 @@ __global__ void __launch_bounds__(kThreads, MODE == CLIP_SUM ? (NR == 8 ? 3 : 4)
     else if ((code & 1023u) == 1023u) sum += squares_full<T, U, MODE, NR>(a, it, w, ow);
     else sum += squares_end<T, U, MODE>(a, it, w, ow);
   }
+  free_launches();
   sum = block_sum(sum, red);
   if (threadIdx.x == 0) a.parts[blockIdx.x] = sum;
 }
@@ -347,6 +348,7 @@ template <typename T, typename U, int MODE>
 __global__ void __launch_bounds__(kThreads, 4) k_clip_scale(const __grid_constant__ ClipArgs a, bool in_place) {
   __shared__ double red[kWarps];
   __shared__ float shared_factor;
+  await_launches();
   double total = 0.0;
   for (int i = threadIdx.x; i < a.nparts; i += kThreads) total += a.parts[i];
   total = block_sum(total, red);
@@ -399,7 +401,7 @@ cudaError_t clip_go(const ClipLaunch& L, cudaStream_t s) {
   a.parts = L.parts;
   const int64_t items = MODE == CLIP_LOCAL ? L.nbuckets * L.nranks : L.nbuckets;
   const int64_t want = items ? (items + kWarps - 1) / kWarps : 1;
-  int64_t most = static_cast<int64_t>(sm_count()) * (MODE == CLIP_SUM ? 4 : 6);
+  int64_t most = static_cast<int64_t>(sm_count()) * 4;
   most = most < kClipMaxParts ? most : kClipMaxParts;
   a.nparts = static_cast<int32_t>(want < most ? want : most);
   if constexpr (MODE == CLIP_SUM) {
@@ -414,9 +416,10 @@ cudaError_t clip_go(const ClipLaunch& L, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   count_launch();
-  k_clip_scale<T, U, MODE><<<a.nparts, kThreads, 0, s>>>(a, L.table == L.out_table);
+  const cudaError_t e = launch_early(k_clip_scale<T, U, MODE>, dim3(a.nparts), dim3(kThreads), s, a,
+                                     L.table == L.out_table);
   count_launch();
-  return cudaGetLastError();
+  return e;
 }
 
 template <typename T, typename U>

@@ -86,6 +86,7 @@ template <typename I>
 __global__ void __launch_bounds__(kSortThreads) k_expert_sort(const __grid_constant__ SortArgs a) {
   extern __shared__ int32_t sort_smem[];
   __shared__ int32_t scan[2][kSortWarps];
+  free_launches();  // (a few CTAs: the dispatch behind it may take its places)
   int32_t* hist = sort_smem;                // [warps][tile]
   int32_t* sums = hist + a.warps * a.tile;  // [tile]: this CTA's choices of every expert
   int32_t* start = sums + a.tile;           // [tile]: the first row of this CTA's
@@ -231,6 +232,7 @@ struct DispatchArgs {
 constexpr int kHeld = 2;
 
 __global__ void __launch_bounds__(kThreads) k_expert_dispatch(const __grid_constant__ DispatchArgs a) {
+  await_launches();
   const int g = blockIdx.y;
   const int tpr = 1 << a.tpr_log2;
   const int tt = threadIdx.x & (tpr - 1), slot = threadIdx.x >> a.tpr_log2, rpb = kThreads >> a.tpr_log2;
@@ -337,24 +339,32 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
         if (residual && c0 + u * tpr < a.nchunks) res[u].load(residual, t * a.nchunks + c0 + u * tpr);
         acc[u] = splat8(0.0f);
       }
-      int32_t next_row[AHEAD];  // (the next choices' indexes and weights are under way with the data of these)
-      float next_w[AHEAD];
-#pragma unroll
-      for (int k = 0; k < AHEAD; ++k) {
-        next_row[k] = k < a.choices ? a.row_of[at + k] : -1;
-        next_w[k] = a.gates && k < a.choices ? a.gates[at + k] : 1.0f;
+      int32_t next_row = -1;  // (one choice at a time: the next one's index and weight are under way with this one's data)
+      float next_w = 1.0f;
+      if (AHEAD == 1 && a.choices > 0) {
+        next_row = a.row_of[at];
+        if (a.gates) next_w = a.gates[at];
       }
       for (int k0 = 0; k0 < a.choices; k0 += AHEAD) {
         int32_t row[AHEAD];
         float w[AHEAD];
+        if constexpr (AHEAD == 1) {
+          row[0] = next_row;
+          w[0] = next_w;
+          if (k0 + 1 < a.choices) {
+            next_row = a.row_of[at + k0 + 1];
+            if (a.gates) next_w = a.gates[at + k0 + 1];
+          }
+        } else {
 #pragma unroll
-        for (int k = 0; k < AHEAD; ++k) {
-          row[k] = next_row[k] < a.rows ? next_row[k] : -1;
-          w[k] = next_w[k];
-          const bool more = k0 + AHEAD + k < a.choices;
-          next_row[k] = more ? a.row_of[at + k0 + AHEAD + k] : -1;
-          next_w[k] = a.gates && more ? a.gates[at + k0 + AHEAD + k] : 1.0f;
+          for (int k = 0; k < AHEAD; ++k) {
+            row[k] = k0 + k < a.choices ? a.row_of[at + k0 + k] : -1;
+            w[k] = a.gates && k0 + k < a.choices ? a.gates[at + k0 + k] : 1.0f;
+          }
         }
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+          if (row[k] >= a.rows) row[k] = -1;
         if constexpr (NR > 0) {
           Chunk<T> raw[ITEMS][AHEAD][NR];
 #pragma unroll
@@ -549,7 +559,7 @@ cudaError_t combine_bwd_shape(CombineBwdArgs& a, int ngroups, cudaStream_t s) {
   a.tpr_log2 = 5;
   while (a.tpr_log2 < 9 && (1 << a.tpr_log2) < a.nchunks) ++a.tpr_log2;
   if (a.nchunks <= 512)
-    return with_ranks<1, 2, 4, 8>(a.nranks, [&](auto n) { return combine_bwd_go<T, n.value, 1, 512>(a, ngroups, s); });
+    return with_ranks<1, 2, 3, 4, 8>(a.nranks, [&](auto n) { return combine_bwd_go<T, n.value, 1, 512>(a, ngroups, s); });
   if (a.nchunks <= 1024)
     return with_ranks<1, 2, 8>(a.nranks, [&](auto n) { return combine_bwd_go<T, n.value, 2, 512>(a, ngroups, s); });
   a.tpr_log2 = 10;
@@ -559,6 +569,39 @@ cudaError_t combine_bwd_shape(CombineBwdArgs& a, int ngroups, cudaStream_t s) {
 }
 
 }  // namespace
+
+// What a kernel needs once per device: leave for the most dynamic shared memory that comes here, and for clusters of more
+// than eight CTAs; and whether the device has room for one of sixteen. (Leaves are the process's, so no call can take
+// another's.)
+static cudaError_t sort_setup(const void* fn, bool index64, bool* wide) {
+  static std::atomic<int> known[2][64];  // 0 not yet, 1 clusters of eight, 2 of sixteen
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool kept = dev >= 0 && dev < 64;
+  int k = kept ? known[index64][dev].load(std::memory_order_acquire) : 0;
+  if (k == 0) {
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(16);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = kSortSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 16;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int fit = 0;
+    k = cudaOccupancyMaxActiveClusters(&fit, fn, &cfg) == cudaSuccess && fit > 0 ? 2 : 1;
+    (void)cudaGetLastError();  // (a device that has none says so as an error)
+    if (kept) known[index64][dev].store(k, std::memory_order_release);
+  }
+  *wide = k == 2;
+  return cudaSuccess;
+}
 
 cudaError_t launch_expert_sort(const ExpertSortLaunch& L, cudaStream_t s) {
   SortArgs a;
@@ -570,8 +613,14 @@ cudaError_t launch_expert_sort(const ExpertSortLaunch& L, cudaStream_t s) {
   a.experts = L.experts;
   a.nranks = L.nranks;
   a.tile = L.experts < kSortTile ? (L.experts > 0 ? L.experts : 1) : kSortTile;
-  // One CTA, of as many threads as there are choices or experts, or eight.
-  const int ctas = L.n <= kSortThreads ? 1 : L.n <= 32 * kSortThreads ? 8 : 16;
+  const void* fn = L.index64 ? reinterpret_cast<const void*>(&k_expert_sort<int64_t>)
+                             : reinterpret_cast<const void*>(&k_expert_sort<int32_t>);
+  bool wide_clusters = false;
+  cudaError_t e = sort_setup(fn, L.index64, &wide_clusters);
+  if (e != cudaSuccess) return e;
+  // One CTA, of as many threads as there are choices or experts, or eight, or sixteen. 4096 choices of 32 experts took 8.4
+  // us on one and 5.8 on eight; 131072 of 1024 24.7 on eight and 16.6 on sixteen (1024 choices: 5.0 and 5.6).
+  const int ctas = L.n <= kSortThreads ? 1 : L.n <= 32 * kSortThreads || !wide_clusters ? 8 : 16;
   const int64_t wide = L.n > L.experts ? L.n : L.experts;
   const int threads = ctas > 1 || wide >= kSortThreads ? kSortThreads : wide <= 128 ? 128 : static_cast<int>((wide + 31) / 32 * 32);
   const int most = kSortSmem / (4 * a.tile) - 2, filled = static_cast<int>(L.n < kSortThreads ? (L.n + 31) / 32 : kSortWarps);
@@ -579,21 +628,6 @@ cudaError_t launch_expert_sort(const ExpertSortLaunch& L, cudaStream_t s) {
   if (a.warps > filled && ctas == 1) a.warps = filled > 0 ? filled : 1;
   a.seg = (L.n + ctas * a.warps - 1) / (ctas * a.warps);
   a.seg = (a.seg + 31) / 32 * 32;
-  const void* fn = L.index64 ? reinterpret_cast<const void*>(&k_expert_sort<int64_t>)
-                             : reinterpret_cast<const void*>(&k_expert_sort<int32_t>);
-  // (the leave for dynamic shared memory is the process's: once per device and kernel, for the most that comes here)
-  static std::atomic<bool> leave[2][64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const bool kept = dev >= 0 && dev < 64;
-  if (!kept || !leave[L.index64][dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    if (kept) leave[L.index64][dev].store(true, std::memory_order_release);
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas, L.ngroups);
   cfg.blockDim = dim3(threads);
@@ -622,9 +656,9 @@ cudaError_t launch_expert_dispatch(const ExpertRowsLaunch& L, cudaStream_t s) {
   a.nscales = L.dtype == COCO_F8E4M3 ? static_cast<int32_t>((static_cast<int64_t>(L.cols) + 127) / 128) : 0;
   a.tpr_log2 = token_threads_log2((a.nvec + kHeld - 1) / kHeld);
   const dim3 grid(blocks_for(a.tokens, a.tpr_log2), L.ngroups, parts_for(a.nvec, kHeld << a.tpr_log2));
-  k_expert_dispatch<<<grid, kThreads, 0, s>>>(a);
+  const cudaError_t e = launch_early(k_expert_dispatch, grid, dim3(kThreads), s, a);
   count_launch();
-  return cudaGetLastError();
+  return e;
 }
 
 cudaError_t launch_expert_combine(const ExpertRowsLaunch& L, cudaStream_t s) {

@@ -249,9 +249,9 @@ cudaError_t norm_shape(LayerNormArgs& a, bool fp8, int ngroups, cudaStream_t s) 
   a.tpr_log2 = 5;
   while (a.tpr_log2 < 9 && (1 << a.tpr_log2) < a.nchunks) ++a.tpr_log2;
   if (a.nchunks <= 512)
-    return with_ranks<1, 2, 4, 8>(a.nranks, [&](auto n) { return norm_go<T, n.value, 1, 512>(a, fp8, ngroups, s); });
+    return with_ranks<1, 2, 3, 4, 8>(a.nranks, [&](auto n) { return norm_go<T, n.value, 1, 512>(a, fp8, ngroups, s); });
   if (a.nchunks <= 1024)
-    return with_ranks<1, 8>(a.nranks, [&](auto n) { return norm_go<T, n.value, 2, 512>(a, fp8, ngroups, s); });
+    return with_ranks<1, 2, 8>(a.nranks, [&](auto n) { return norm_go<T, n.value, 2, 512>(a, fp8, ngroups, s); });
   a.tpr_log2 = 10;
   if (a.nchunks <= 2048)
     return with_ranks<1>(a.nranks, [&](auto n) { return norm_go<T, n.value, 2, 1024>(a, fp8, ngroups, s); });

@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(THREADS, BwdShape<T, VPT, THREADS>::BLOCKS)
       }
     }
   }
+  free_launches();
   __syncthreads();
   if (slot == 0) {
 #pragma unroll
@@ -185,9 +186,10 @@ __global__ void __launch_bounds__(THREADS, BwdShape<T, VPT, THREADS>::BLOCKS)
 }
 
 // dweight[c] and dbias[c]: the sums over the workspace's rows, 32 rows at a time in parallel, then in order. Grid y: which.
-__global__ void __launch_bounds__(1024) k_layernorm_dweight(const float* __restrict__ partial, int nparts, int cols,
-                                                            float* __restrict__ dweight, float* __restrict__ dbias) {
+__global__ void __launch_bounds__(1024) k_layernorm_dweight(const float* partial, int nparts, int cols, float* dweight,
+                                                            float* dbias) {
   __shared__ float part[32][33];
+  await_launches();
   const int c = blockIdx.x * 32 + threadIdx.x;
   float* out = blockIdx.y ? dbias : dweight;
   float s = 0.0f;
@@ -238,7 +240,7 @@ cudaError_t bwd_shape(LayerNormBwdArgs& a, int groups, int* parts, cudaStream_t 
   a.tpr_log2 = r.tpr_log2;
   if constexpr (sizeof(T) == 2) {
     if (r.vpt == 1)
-      return with_ranks<1, 2, 4, 8>(a.nranks, [&](auto n) { return bwd_go<T, n.value, 1, 512>(a, groups, parts, s); });
+      return with_ranks<1, 2, 3, 4, 8>(a.nranks, [&](auto n) { return bwd_go<T, n.value, 1, 512>(a, groups, parts, s); });
     if (r.vpt == 2)
       return with_ranks<1, 2, 8>(a.nranks, [&](auto n) { return bwd_go<T, n.value, 2, 512>(a, groups, parts, s); });
     a.tpr_log2 = 10;
@@ -287,10 +289,10 @@ cudaError_t launch_layernorm_backward(const LayerNormBwdLaunch& B, cudaStream_t 
     default: e = bwd_shape<__nv_bfloat16>(a, L.ngroups, &parts, s); break;
   }
   if (e != cudaSuccess) return e;
-  k_layernorm_dweight<<<dim3((L.cols + 31) / 32, B.dbias ? 2 : 1), dim3(32, 32), 0, s>>>(L.partial, parts, L.cols,
-                                                                                      L.dweight, B.dbias);
+  e = launch_early(k_layernorm_dweight, dim3((L.cols + 31) / 32, B.dbias ? 2 : 1), dim3(32, 32), s, L.partial, parts, L.cols,
+                   L.dweight, B.dbias);
   count_launch();
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace coco

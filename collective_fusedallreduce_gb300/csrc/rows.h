@@ -281,6 +281,26 @@ __device__ __forceinline__ Chunk<T> rounded(const Vec8& a) {
   return c;
 }
 
+// Launches a kernel that may be placed on the device before the one ahead of it in the stream has ended. Its first
+// statement is await_launches(): it reads and writes nothing before that kernel's end, so the order of their effects is the
+// stream's, and what is saved is the launch. A kernel whose successor is known calls free_launches() when its last work is under way.
+__device__ __forceinline__ void await_launches() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void free_launches() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // Calls f with the first of the numbers of ranks NS that nranks is, or with 0 (any number).
 template <int... NS, typename F>
 cudaError_t with_ranks(int nranks, F&& f) {

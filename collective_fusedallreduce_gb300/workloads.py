@@ -180,7 +180,9 @@ def route(expert_of, experts):
 def sort_by_expert(expert_of, experts, ranks):
     """``route`` by the library, for ``ranks`` ranks: (row_of_choice [tokens, choices] int32, offsets [ranks, experts + 1]
     int32, a line per rank)."""
-    row_of = torch.empty_like(expert_of, dtype=torch.int32)
+    if expert_of.dtype not in (torch.int64, torch.int32):
+        expert_of = expert_of.long()
+    row_of = _empty(expert_of.shape, torch.int32, expert_of.device)
     offsets = _empty((ranks, experts + 1), torch.int32, expert_of.device)
     coco.coco_expert_sort(expert_of.contiguous(), experts, row_of, None, offsets)
     return row_of, offsets
