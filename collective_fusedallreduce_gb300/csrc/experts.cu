@@ -433,9 +433,20 @@ __device__ __forceinline__ void token_sums(float (&v)[kDots], int tpr, int slot,
   }
 }
 
+// Blocks an SM: a token's waits, for its indexes, its rows and its barrier, follow one another, and other blocks fill them.
+// 8192 tokens of two experts, 4096 columns of bf16, one rank: 101 us with two blocks, 80 with three, 78 with four; three
+// ranks 121 and 102 with two and three; eight ranks 186 and 191. (Blocks that stay, with the next token's indexes and
+// gradient under way, took 80, 103 and 203.)
+template <typename T, int NR, int VPT, int THREADS>
+constexpr int bwd_blocks() {
+  if (THREADS == 1024) return 1;
+  if (sizeof(T) == 4 || VPT > 1 || NR == 0 || NR > 4) return 2;
+  return NR == 1 ? 4 : 3;
+}
+
 // A token belongs to `tpr` threads, which keep its gradient in registers; grid y: groups.
 template <typename T, int NR, int VPT, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS == 1024 ? 1 : VPT == 1 && NR > 0 && NR <= 2 && sizeof(T) == 2 ? 3 : 2)
+__global__ void __launch_bounds__(THREADS, bwd_blocks<T, NR, VPT, THREADS>())
     k_expert_combine_backward(const __grid_constant__ CombineBwdArgs a) {
   __shared__ float red[2][kDots][32];
   const int g = blockIdx.y;
@@ -618,9 +629,10 @@ cudaError_t launch_expert_sort(const ExpertSortLaunch& L, cudaStream_t s) {
   bool wide_clusters = false;
   cudaError_t e = sort_setup(fn, L.index64, &wide_clusters);
   if (e != cudaSuccess) return e;
-  // One CTA, of as many threads as there are choices or experts, or eight, or sixteen. 4096 choices of 32 experts took 8.4
-  // us on one and 5.8 on eight; 131072 of 1024 24.7 on eight and 16.6 on sixteen (1024 choices: 5.0 and 5.6).
-  const int ctas = L.n <= kSortThreads ? 1 : L.n <= 32 * kSortThreads || !wide_clusters ? 8 : 16;
+  // One CTA, of as many threads as there are choices or experts, or eight, or sixteen. Measured on 1, 8 and 16, us: 512
+  // choices of 32 experts 4.1, 4.9, 5.1; 1024 5.4, 5.5, 5.7; 4096 7.3, 5.8, 5.9; 16384 16.3, 6.2, 5.9; 131072 of 64 105,
+  // 18.1, 10.6.
+  const int ctas = L.n <= kSortThreads ? 1 : L.n <= 8 * kSortThreads || !wide_clusters ? 8 : 16;
   const int64_t wide = L.n > L.experts ? L.n : L.experts;
   const int threads = ctas > 1 || wide >= kSortThreads ? kSortThreads : wide <= 128 ? 128 : static_cast<int>((wide + 31) / 32 * 32);
   const int most = kSortSmem / (4 * a.tile) - 2, filled = static_cast<int>(L.n < kSortThreads ? (L.n + 31) / 32 : kSortWarps);
