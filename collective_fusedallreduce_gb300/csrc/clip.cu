@@ -10,6 +10,11 @@
 // With CLIP_SUM the first also sums the ranks' tensors and stores the sums, so the
 // AllReduce's one pass gives the norm as well. Bound by HBM: the second pass walks
 // backwards, and finds in L2 what the first touched last.
+//
+// Measured, from a graph: BERT-large's 335 million fp16 gradients of 8 ranks, averaged
+// and clipped into one copy, 1090 us (the two passes' 7.4 GB at 6.8 TB/s); 12.6 million
+// bf16 ones to fp32 22.7 us, where the two launches and what each waits for at its
+// ends are half; 153 million fp32 ones 293 us.
 
 #include <float.h>
 
@@ -263,7 +268,8 @@ __device__ __forceinline__ double squares_end(const ClipArgs& a, int64_t b, uint
   else return squares<T, N>(k, s);
 }
 
-// Warps take buckets round-robin (those of every rank with CLIP_LOCAL), the next one's entries under way. With CLIP_SUM
+// Warps take buckets round-robin (those of every rank with CLIP_LOCAL), the next one's entries under way. Two blocks an SM
+// with CLIP_SUM, whose 128 registers hold a bucket's loads of eight ranks (three blocks took BERT-large's from 1086 to 1188 us). With CLIP_SUM
 // the ranks' tensors are added in rank order, scaled by alpha, rounded to U and stored to out's rank 0, and it is those
 // values' norm. Where the two tables' tensors do not have a bucket in common, nothing is written and the norm is NaN.
 template <typename T, typename U, int MODE, int NR>

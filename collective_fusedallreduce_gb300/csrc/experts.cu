@@ -81,7 +81,8 @@ __device__ __forceinline__ void load_experts(const I* e, int64_t i0, int64_t las
 // experts in shared memory; a column's counts become the warps' starts in order, the CTAs' sums are exchanged through
 // distributed shared memory, and a scan over the experts gives the offsets. Each warp then walks its run again, 32
 // choices at a time: a choice's row is its expert's start, plus what the warp has placed there, plus the earlier lanes
-// with the same expert.
+// with the same expert. Latency bounds it (16 x 2 choices of 64 experts 3.1 us, an empty launch some 2.3; 8192 x 2 of 32
+// 6.0): the choices are loaded eight at a time and, where they fit, once, the peers' sums all at once.
 template <typename I>
 __global__ void __launch_bounds__(kSortThreads) k_expert_sort(const __grid_constant__ SortArgs a) {
   extern __shared__ int32_t sort_smem[];
@@ -228,7 +229,9 @@ struct DispatchArgs {
 };
 
 // A token belongs to `tpr` threads (blockDim / tpr tokens a block) of each of the blocks of grid z, which hold kHeld of
-// its vectors each at a time and write them to one choice's row after another; grid y: groups.
+// its vectors each at a time and write them to one choice's row after another; grid y: groups. HBM bounds it: 8192 tokens of
+// two experts, 4096 columns of bf16, 36.3 us with the sort ahead of it, of which 29.4 are their bytes. (A thread a vector,
+// which divides for its token and reads the indexes itself, took twice the instructions and 39.0.)
 constexpr int kHeld = 2;
 
 __global__ void __launch_bounds__(kThreads) k_expert_dispatch(const __grid_constant__ DispatchArgs a) {
@@ -307,7 +310,8 @@ struct CombineArgs {
 };
 
 // How many chunks a thread takes and how many choices at a time, so that some loads are under way. MANY: more than two
-// choices.
+// choices (8 of 2048 columns, one rank: 114 us, 5.9 TB/s; 132 with a choice at a time, 130 with two of two chunks). Eight
+// ranks' rows of two experts, 8192 x 4096: 175 us, at the copy rate; their own sums 262 (91 %).
 template <int NR, bool MANY>
 struct CombineShape {
   static constexpr int ITEMS = NR == 1 && !MANY ? 2 : 1;
@@ -631,8 +635,10 @@ cudaError_t launch_expert_sort(const ExpertSortLaunch& L, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   // One CTA, of as many threads as there are choices or experts, or eight, or sixteen. Measured on 1, 8 and 16, us: 512
   // choices of 32 experts 4.1, 4.9, 5.1; 1024 5.4, 5.5, 5.7; 4096 7.3, 5.8, 5.9; 16384 16.3, 6.2, 5.9; 131072 of 64 105,
-  // 18.1, 10.6.
-  const int ctas = L.n <= kSortThreads ? 1 : L.n <= 8 * kSortThreads || !wide_clusters ? 8 : 16;
+  // 18.1, 10.6, of 1024 136, 24.4, 16.8. Where counting more experts than that is most of the work, more CTAs only repeat
+  // it (16384 of 8192: 25 on eight, 31 on sixteen).
+  const bool sixteen = wide_clusters && L.n > 8 * kSortThreads && L.experts <= 2048;
+  const int ctas = L.n <= kSortThreads ? 1 : sixteen ? 16 : 8;
   const int64_t wide = L.n > L.experts ? L.n : L.experts;
   const int threads = ctas > 1 || wide >= kSortThreads ? kSortThreads : wide <= 128 ? 128 : static_cast<int>((wide + 31) / 32 * 32);
   const int most = kSortSmem / (4 * a.tile) - 2, filled = static_cast<int>(L.n < kSortThreads ? (L.n + 31) / 32 : kSortWarps);
