@@ -268,10 +268,11 @@ __device__ __forceinline__ double squares_end(const ClipArgs& a, int64_t b, uint
   else return squares<T, N>(k, s);
 }
 
-// Warps take buckets round-robin (those of every rank with CLIP_LOCAL), the next one's entries under way. Two blocks an SM
-// with CLIP_SUM, whose 128 registers hold a bucket's loads of eight ranks (three blocks took BERT-large's from 1086 to 1188 us). With CLIP_SUM
-// the ranks' tensors are added in rank order, scaled by alpha, rounded to U and stored to out's rank 0, and it is those
-// values' norm. Where the two tables' tensors do not have a bucket in common, nothing is written and the norm is NaN.
+// Two blocks an SM with CLIP_SUM, whose 128 registers hold a bucket's loads of eight ranks (three blocks: BERT-large's 1086
+// -> 1188 us). Warps take buckets round-robin (those of every rank with CLIP_LOCAL), the next one's entries under way.
+// With CLIP_SUM the ranks' tensors are added in rank order, scaled by alpha, rounded to U and stored to out's rank 0, and
+// it is those values' norm. Where the two tables' tensors do not have a bucket in common, nothing is written and the norm
+// is NaN.
 template <typename T, typename U, int MODE, int NR>
 __global__ void __launch_bounds__(kThreads, MODE == CLIP_SUM ? 2 : 4)
     k_clip_squares(const __grid_constant__ ClipArgs a) {

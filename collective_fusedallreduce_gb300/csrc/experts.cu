@@ -318,9 +318,10 @@ struct CombineShape {
   static constexpr int AHEAD = NR == 1 && MANY ? 4 : NR == 8 || NR == 0 ? 1 : 2;
 };
 
-// A token belongs to `tpr` threads (blockDim / tpr tokens a block) of each of the blocks of grid z. SUMMED: grid y counts groups, whose ranks' rows are
-// added up, with the residual, for every distinct output. Otherwise it counts ranks, each with an output of its own (NR is
-// 1). A choice's rows are added over the ranks first (in order), then weighted; product and sum are rounded one by one.
+// A token belongs to `tpr` threads (blockDim / tpr tokens a block) of each of the blocks of grid z. SUMMED: grid y counts
+// groups, whose ranks' rows are added up, with the residual, for every distinct output. Otherwise it counts ranks, each with
+// an output of its own (NR is 1). A choice's rows are added over the ranks first (in order), then weighted; product and sum
+// are rounded one by one.
 template <typename T, int NR, bool SUMMED, bool MANY>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
     k_expert_combine(const __grid_constant__ CombineArgs a) {
@@ -640,8 +641,11 @@ cudaError_t launch_expert_sort(const ExpertSortLaunch& L, cudaStream_t s) {
   const bool sixteen = wide_clusters && L.n > 8 * kSortThreads && L.experts <= 2048;
   const int ctas = L.n <= kSortThreads ? 1 : sixteen ? 16 : 8;
   const int64_t wide = L.n > L.experts ? L.n : L.experts;
-  const int threads = ctas > 1 || wide >= kSortThreads ? kSortThreads : wide <= 128 ? 128 : static_cast<int>((wide + 31) / 32 * 32);
-  const int most = kSortSmem / (4 * a.tile) - 2, filled = static_cast<int>(L.n < kSortThreads ? (L.n + 31) / 32 : kSortWarps);
+  const int threads = ctas > 1 || wide >= kSortThreads ? kSortThreads
+                      : wide <= 128                    ? 128
+                                                       : static_cast<int>((wide + 31) / 32 * 32);
+  const int most = kSortSmem / (4 * a.tile) - 2;
+  const int filled = static_cast<int>(L.n < kSortThreads ? (L.n + 31) / 32 : kSortWarps);
   a.warps = most < threads / 32 ? most : threads / 32;
   if (a.warps > filled && ctas == 1) a.warps = filled > 0 ? filled : 1;
   a.seg = (L.n + ctas * a.warps - 1) / (ctas * a.warps);

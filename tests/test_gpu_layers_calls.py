@@ -167,6 +167,76 @@ def test_a_call_behind_its_own_copy():
     assert same(c.taken(), want)
 
 
+def test_calls_behind_copies_events_and_other_kernels_in_a_graph():
+    """The dispatch, the clip's second launch and the norm gradient's last sum may be placed early; what is ahead of them
+    here are a copy, a memset, an event of another stream, and PyTorch's kernels."""
+    tokens, cols = 4096, 1024
+    x, new = torch.zeros(tokens, cols, device=DEV), torch.randn(tokens, cols, device=DEV)
+    row = torch.randperm(tokens, device=DEV, dtype=torch.int32)[:, None].contiguous()
+    out = [torch.zeros(tokens, cols, device=DEV) for _ in range(4)]
+    side = torch.cuda.Stream()
+
+    def send(to):
+        coco.coco_expert_dispatch(coco.replicated([x]), None, row, coco.replicated([to]), None)
+
+    def run():
+        x.copy_(new)              # a copy
+        send(out[0])
+        x.mul_(2.0)               # a kernel
+        send(out[1])
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            x.zero_()             # another stream's work, joined by an event
+            x.add_(new)
+        main.wait_stream(side)
+        send(out[2])
+        out[3].zero_()            # a memset of what is written
+        send(out[3])
+
+    def check():
+        want = torch.empty_like(x)
+        want[row[:, 0].long()] = new
+        assert torch.equal(out[0], want) and torch.equal(out[1], 2 * want)
+        assert torch.equal(out[2], want) and torch.equal(out[3], want)
+
+    run()
+    torch.cuda.synchronize()
+    check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(3):
+        new.normal_()
+        for t in out + [x]:
+            t.fill_(7.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        check()
+
+
+def test_sorting_many_groups_on_wide_clusters():
+    groups, tokens, choices, experts = 9, 9000, 2, 50
+    e = torch.randint(-1, experts + 1, (groups, tokens, choices), device=DEV)
+    row = torch.empty(groups, tokens, choices, dtype=torch.int32, device=DEV)
+    of = torch.empty(groups, tokens * choices, dtype=torch.int32, device=DEV)
+    off = torch.empty(groups * 2, experts + 1, dtype=torch.int32, device=DEV)
+    coco.coco_expert_sort(e, experts, row, of, off)
+    coco.coco_device_status()
+    for g in range(groups):
+        flat = e[g].reshape(-1)
+        key = torch.where((flat >= 0) & (flat < experts), flat, experts)
+        order = torch.argsort(key, stable=True)
+        live = int((key < experts).sum())
+        assert torch.equal(of[g, :live].long(), order[:live]) and bool((of[g, live:] == -1).all())
+        want = torch.full_like(flat, -1)
+        want[order[:live]] = torch.arange(live, device=DEV)
+        assert torch.equal(row[g].reshape(-1).long(), want)
+        assert torch.equal(off[2 * g].long(), torch.searchsorted(key[order], torch.arange(experts + 1, device=DEV)))
+        assert torch.equal(off[2 * g], off[2 * g + 1])
+
+
 @pytest.fixture
 def room():
     if torch.cuda.get_device_properties(0).total_memory < 100 << 30:
