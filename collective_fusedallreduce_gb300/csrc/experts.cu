@@ -300,6 +300,16 @@ __device__ __forceinline__ Vec8 sum_vec(const void* const* in, int nranks, int64
   return s;
 }
 
+// acc + s * w, product and sum each rounded. The products are single ones: the compiler contracts a pair's product and the
+// sum after it, in spite of their .rn, which leaves out the product's rounding.
+__device__ __forceinline__ Vec8 add_weighted(const Vec8& acc, const Vec8& s, float w) {
+  float f[kChunk];
+  unpack8(s, f);
+#pragma unroll
+  for (int j = 0; j < kChunk; ++j) f[j] = __fmul_rn(f[j], w);
+  return acc + Vec8{{pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])}};
+}
+
 struct CombineArgs {
   ExpertTables t;
   const int32_t* row_of;  // [groups][tokens][choices]
@@ -388,10 +398,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
                 Vec8 s = values<T>(raw[u][k][0]);
 #pragma unroll
                 for (int r = 1; r < NR; ++r) s = s + values<T>(raw[u][k][r]);
-                acc[u] = acc[u] + s * splat8(w[k]);
+                acc[u] = add_weighted(acc[u], s, w[k]);
               }
         } else if (row[0] >= 0) {
-          acc[0] = acc[0] + sum_vec<T, 0>(in, a.nranks, static_cast<int64_t>(row[0]) * a.nchunks + c0) * splat8(w[0]);
+          const Vec8 s = sum_vec<T, 0>(in, a.nranks, static_cast<int64_t>(row[0]) * a.nchunks + c0);
+          acc[0] = add_weighted(acc[0], s, w[0]);
         }
       }
 #pragma unroll

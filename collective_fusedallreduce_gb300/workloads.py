@@ -199,10 +199,15 @@ def dispatch(x, row_of, ranks, scales=None):
 
 
 def combine(rows, row_of, gates, like):
-    """Every rank's own sum over a token's choices of gate * row (gates None: ones)."""
-    out = [torch.empty_like(like) for _ in rows]
+    """Every rank's own sum over a token's choices of gate * row (gates: what broadcasts to the choices; None: ones), in
+    the shape and type of ``like``. Rows of another type are summed in fp32, and rounded to it once."""
+    if gates is not None:
+        gates = gates.float().expand(row_of.shape).contiguous()
+    if rows[0].dtype != like.dtype:
+        rows = [r.float() for r in rows]
+    out = [torch.empty_like(like, dtype=r.dtype) for r in rows]
     coco.coco_expert_combine(coco.local(rows), row_of, gates, None, coco.local(out))
-    return out
+    return [o.to(like.dtype) for o in out]
 
 
 def _scales_like(q):
@@ -255,7 +260,7 @@ def moe_layer_fp8(partials, residual, weight, eps, expert_of, gates, up, up_scal
     coco.coco_quantize_fp8(coco.local(mid), 1, coco.local(q), qs)
     out = [_empty((rows.shape[0], down[0].shape[2]), torch.bfloat16, dev) for _ in range(n)]
     coco.coco_grouped_einsum("tk,ekn->tn", coco.local(q), qs, coco.local(down), down_scales, offsets, coco.local(out))
-    return norm_fp8(combine(out, row_of, gates.float().contiguous(), hidden), hidden, next_weight, eps)
+    return norm_fp8(combine(out, row_of, gates, hidden), hidden, next_weight, eps)
 
 
 def moe_layer_train(partials, residual, weight, eps, expert_of, up, down, dout):

@@ -174,3 +174,29 @@ def test_the_librarys_routing_is_pytorchs():
     for g in (gates, None):
         want = (rows[row_of].float() * (gates[..., None] if g is not None else 1.0)).sum(1).bfloat16()
         assert torch.equal(workloads.combine([rows], got, g, x)[0], want)  # as the layers did it before
+
+
+@pytest.mark.parametrize("choices", [1, 2, 3, 4, 8])
+@pytest.mark.parametrize("ranks", [1, 2, 3, 4, 8, 5])
+def test_combined_products_and_sums_are_rounded_one_by_one(choices, ranks):
+    """In fp32, where nothing hides it: the ranks in order, the weight, then the choices in order."""
+    tokens, cols = 301, 256
+    rows = [torch.randn(tokens * choices, cols, device=DEV) for _ in range(ranks)]
+    row_of = torch.randperm(tokens * choices, device=DEV, dtype=torch.int32).view(tokens, choices)
+    gates, at = torch.rand(tokens, choices, device=DEV), row_of.long()
+
+    def summed(values):
+        total = torch.zeros(tokens, cols, device=DEV)
+        for k in range(choices):
+            total = total + values[at[:, k]] * gates[:, k, None]
+        return total
+
+    for r, got in zip(rows, workloads.combine(rows, row_of, gates, rows[0][:tokens])):
+        assert torch.equal(got, summed(r))
+    over = rows[0]
+    for r in rows[1:]:
+        over = over + r
+    out, res = torch.empty(tokens, cols, device=DEV), torch.randn(tokens, cols, device=DEV)
+    coco.coco_expert_combine(coco.local(rows), row_of, gates, coco.replicated([res] * ranks), coco.replicated([out] * ranks))
+    coco.coco_device_status()
+    assert torch.equal(out, summed(over) + res)
