@@ -176,6 +176,18 @@ def test_the_librarys_routing_is_pytorchs():
         assert torch.equal(workloads.combine([rows], got, g, x)[0], want)  # as the layers did it before
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shape", [(37, 2), (37, 1), (1, 2), (2,), ()])
+def test_combining_for_any_residual_stream_with_gates_that_broadcast(dtype, shape):
+    """The experts' products are bf16 whatever the stream's type is, and one gate may stand for many choices."""
+    x, y = torch.randn(37, 64, device=DEV).to(dtype), torch.randn(74, 64, device=DEV).bfloat16()
+    row_of = torch.randperm(74, device=DEV, dtype=torch.int32).view(37, 2)
+    for gates in (torch.rand(shape, device=DEV), torch.rand(shape, device=DEV).bfloat16()):
+        want = (y[row_of.long()].float() * gates[..., None]).sum(1).to(dtype)
+        got = workloads.combine([y], row_of, gates, x)[0]
+        assert got.dtype == dtype and torch.equal(got, want)
+
+
 @pytest.mark.parametrize("choices", [1, 2, 3, 4, 8])
 @pytest.mark.parametrize("ranks", [1, 2, 3, 4, 8, 5])
 def test_combined_products_and_sums_are_rounded_one_by_one(choices, ranks):
@@ -200,3 +212,20 @@ def test_combined_products_and_sums_are_rounded_one_by_one(choices, ranks):
     coco.coco_expert_combine(coco.local(rows), row_of, gates, coco.replicated([res] * ranks), coco.replicated([out] * ranks))
     coco.coco_device_status()
     assert torch.equal(out, summed(over) + res)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_serving_layer_with_other_residual_streams(dtype):
+    """As test_gpu_llm_layer's, whose stream is bf16; its tolerances (the stream's own rounding is no coarser here)."""
+    parts, res, w, _, up, down, expert_of, gates, _ = inputs(37, 400, 144, 5, 3, 2, 901)
+    parts, res, w = [p.to(dtype) for p in parts], res.to(dtype), w.to(dtype)
+    expert_of = expert_of.clamp(min=0)
+    up8, down8 = workloads.quantize_weights(dev(up)), workloads.quantize_weights(dev(down))
+    h2, q, s = workloads.moe_layer_fp8(dev(parts), res.to(DEV), w.to(DEV), 1e-5, expert_of.to(DEV), gates.to(DEV), *up8,
+                                       *down8, torch.ones(400, dtype=dtype, device=DEV))
+    coco.coco_device_status()
+    h, _, y = oracle.moe_layer([f64(p) for p in parts], f64(res), f64(w), 1e-5, expert_of.numpy(), f64(gates),
+                               [f64(u) for u in up], [f64(d) for d in down])
+    assert h2.dtype == dtype and far(f64(h2) - h, y) <= 0.08
+    x2 = oracle.allreduce_rmsnorm([h + y], None, np.ones(400), 1e-5)[1]
+    assert far(oracle.dequantize(f64(q), f64(s), 1), x2) <= 0.09
