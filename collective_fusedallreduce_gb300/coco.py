@@ -208,14 +208,18 @@ class Dist:
         """The coco_tensor as bytes: one struct.pack instead of a field at a time, which is most of what a call
         on small tensors costs. The library sees addresses only: that every tensor is dense, and as large as the
         others, is checked here (which costs as much again as taking an address, so once for one that is repeated)."""
-        ts, times = self.tensors, 1
-        if self.layout == REPLICATED:
-            first = ts[0]
+        ts, shape = self.tensors, self.shape
+        first = ts[0]
+        if self.layout == REPLICATED and first is not None:
             for t in ts:
                 if t is not first:
                     break
-            else:
-                ts, times = [first], len(ts)
+            else:  # (its address, packed once)
+                if not first.is_contiguous():
+                    raise CocoError(2, what)
+                n = len(ts)
+                return _tensor_head.pack(self.dtype, REPLICATED, len(shape), self.slice_dim, *(shape + (0, 0, 0))[:3],
+                                         self.nranks, self.ngroups) + _one_pointer(first.data_ptr()) * n + _no_pointers(n)
         try:
             addresses = list(map(torch.Tensor.data_ptr, ts))
         except TypeError:  # a None stands for a null pointer
@@ -224,11 +228,18 @@ class Dist:
         if not all(map(torch.Tensor.is_contiguous, ts)) or (len(ts) > 1 and len(set(map(_nbytes, ts))) > 1):
             raise CocoError(2, what)
         return _tensor_struct(len(self.tensors)).pack(
-            self.dtype, self.layout, len(self.shape), self.slice_dim, *(self.shape + (0, 0, 0))[:3], self.nranks,
-            self.ngroups, *addresses * times)
+            self.dtype, self.layout, len(shape), self.slice_dim, *(shape + (0, 0, 0))[:3], self.nranks, self.ngroups,
+            *addresses)
 
 
 _nbytes = operator.attrgetter("nbytes")
+_tensor_head = struct.Struct("=4i3q2i")
+_one_pointer = struct.Struct("=Q").pack
+
+
+@functools.lru_cache(maxsize=None)
+def _no_pointers(n):
+    return bytes(8 * max(0, MAX_PTRS - n))
 
 
 @functools.lru_cache(maxsize=None)
@@ -503,7 +514,7 @@ def _check_here(what, *tensors):
             if at < 0:
                 raise CocoError(7, f"{what}: a tensor that is not in device memory")
             if at != here:
-                if here is not None or at != torch.cuda.current_device():
+                if here is not None or at != torch._C._cuda_getDevice():
                     raise CocoError(7, f"{what}: a tensor of another device than the current one")
                 here = at
 
