@@ -10,10 +10,10 @@
 // which k_layernorm_dweight adds in block order: no atomics, so repeated calls
 // give the same bits.
 //
-// Measured, from a graph: 8192 x 4096 fp16 on 8 ranks 121.5 us (6.1 TB/s; some 6 of
-// them the second kernel, which is placed early), 777 x 8192 bf16 on 2 26.2 (two or three
-// rows a block, whose waits follow one another), 8192 x 4096 bf16 on 3 75.8, 4096 x 16384
-// on one 117, 2048 x 32768 265 (db through L2). dw and db in registers instead of shared
+// Measured, from a graph: 8192 x 4096 fp16 on 8 ranks 119.5 us (6.2 TB/s; some 6 of
+// them the second kernel, which is placed early), 777 x 8192 bf16 on 2 26.0 (two or three
+// rows a block, whose waits follow one another), 8192 x 4096 bf16 on 3 67.4, 4096 x 16384
+// on one 119, 2048 x 32768 266 (db through L2). dw and db in registers instead of shared
 // memory do not fit two blocks an SM (204 us for the first with one).
 
 #include <atomic>
@@ -55,25 +55,39 @@ __device__ __forceinline__ float2 row_sum2(float2 v, int tpr, int slot, float2 (
   return make_float2(warp_sum(s.x), warp_sum(s.y));
 }
 
+// A thread's own 16 bytes of shared memory, filled from global memory while it does other things.
+__device__ __forceinline__ void copy_16(float4* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(to))), "l"(from)
+               : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // THREADS and blocks an SM: 16-bit rows of up to 8192 columns have two blocks of 512 threads, wider ones 1024 threads a
 // row of two or four chunks; fp32 rows 512 threads, two blocks of one chunk.
-template <typename T, int VPT, int THREADS>
+template <typename T, int NR, int VPT, int THREADS>
 struct BwdShape {
   // A thread's sums: two vectors of dw and two of db a chunk, in shared memory. Rows of 32768 columns would need 256 KB of
   // it: their db lies in the workspace from the start, where L2 holds it.
   static constexpr bool FAR = VPT * THREADS > 2048;
   static constexpr int PER = FAR ? 2 : 4;
-  static constexpr int SMEM = PER * VPT * THREADS * 16;
+  // Operands (the ranks', hidden, dhidden) whose next row is copied to shared memory while this one is summed and stored:
+  // all, where a thread has one 16-bit chunk of each and their number is known (8192 x 4096 on two ranks 70.7 -> 63.3 us, on
+  // three 76 -> 67.4, on four 81 -> 75.7, on eight 121.4 -> 119.5). Two chunks a thread lost by it (8192 x 8192 on one rank
+  // 114 -> 118), fp32 more (one rank 101 -> 140).
+  static constexpr int STAGED = sizeof(T) == 2 && VPT == 1 && NR > 0 ? NR + 2 : 0;
+  static constexpr int SMEM = (PER * VPT + STAGED) * THREADS * 16;
   static constexpr int BLOCKS = THREADS == 512 && VPT <= (sizeof(T) == 2 ? 2 : 1) ? 2 : 1;
 };
 
 template <typename T, int NR, int VPT, int THREADS>
-__global__ void __launch_bounds__(THREADS, BwdShape<T, VPT, THREADS>::BLOCKS)
+__global__ void __launch_bounds__(THREADS, BwdShape<T, NR, VPT, THREADS>::BLOCKS)
     k_layernorm_backward(const __grid_constant__ LayerNormBwdArgs a) {
-  constexpr bool FAR = BwdShape<T, VPT, THREADS>::FAR;
-  constexpr int PER = BwdShape<T, VPT, THREADS>::PER;
+  using S = BwdShape<T, NR, VPT, THREADS>;
+  constexpr bool FAR = S::FAR;
+  constexpr int PER = S::PER, STAGED = S::STAGED;
   __shared__ float2 red[2][32];
   extern __shared__ float4 sums[];  // [PER * VPT][threads]
+  float4* staged = sums + PER * VPT * THREADS + threadIdx.x;  // [STAGED][threads]
   const int g = blockIdx.y;
   const int tpr = 1 << a.tpr_log2;
   const int t = threadIdx.x & (tpr - 1), slot = threadIdx.x >> a.tpr_log2, rpb = THREADS >> a.tpr_log2;
@@ -87,15 +101,34 @@ __global__ void __launch_bounds__(THREADS, BwdShape<T, VPT, THREADS>::BLOCKS)
   for (int i = 0; i < PER * VPT; ++i) sums[i * THREADS + threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
   if constexpr (FAR)
     for (int c = t; c < a.nchunks; c += tpr) far_db[2 * c] = far_db[2 * c + 1] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float next_mean = 0.0f, next_rstd = 0.0f;
+  auto stage = [&](int64_t row) {  // (a thread reads what it copied itself: no barrier)
+    if (row >= a.rows) return;
+    next_mean = a.mean[g * a.rows + row];
+    next_rstd = a.rstd[g * a.rows + row];
+    if (t >= a.nchunks) return;
+#pragma unroll
+    for (int r = 0; r < STAGED; ++r) {
+      const void* p = r < NR ? in[r] : r == NR ? hidden : dhidden;
+      if (p) copy_16(staged + r * THREADS, static_cast<const uint4*>(p) + row * a.nchunks + t);
+    }
+  };
+  auto fetch = [&](int r) {
+    Chunk<T> c;
+    c.load_cached(staged + r * THREADS, 0);
+    return c;
+  };
+  if constexpr (STAGED > 0) stage(static_cast<int64_t>(blockIdx.x) * rpb + slot);
   int turn = 0;
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * rpb; base < a.rows;
        base += static_cast<int64_t>(gridDim.x) * rpb, turn ^= 1) {
     const int64_t row = base + slot;
     const bool live = row < a.rows;
     const int64_t c0 = row * a.nchunks;
-    // The block's next row is brought to L2 meanwhile: a row's loads, its barrier and its stores do not overlap.
+    // The block's next row is brought to L2 meanwhile, if not to shared memory: a row's loads, its barrier and its stores do
+    // not overlap.
     const int64_t ahead = row + static_cast<int64_t>(gridDim.x) * rpb;
-    if (ahead < a.rows && (VPT > 1 || a.nranks < 8))
+    if (STAGED == 0 && ahead < a.rows && (VPT > 1 || a.nranks < 8))
       for (int i = t; i < a.nranks + 2; i += tpr) {
         const void* p = i < a.nranks ? in[i] : i == a.nranks ? hidden : dhidden;
         const int bytes = a.cols * static_cast<int>(sizeof(T));
@@ -104,7 +137,15 @@ __global__ void __launch_bounds__(THREADS, BwdShape<T, VPT, THREADS>::BLOCKS)
                        "r"(bytes)
                        : "memory");
       }
-    const float mean = live ? a.mean[g * a.rows + row] : 0.0f, rstd = live ? a.rstd[g * a.rows + row] : 0.0f;
+    float mean = 0.0f, rstd = 0.0f;
+    if constexpr (STAGED > 0) {
+      copies_done();
+      mean = next_mean;
+      rstd = next_rstd;
+    } else if (live) {
+      mean = a.mean[g * a.rows + row];
+      rstd = a.rstd[g * a.rows + row];
+    }
     float gr[VPT][kChunk];
     Chunk<T> hv[VPT], dh[1];
     float2 along = make_float2(0.0f, 0.0f);
@@ -113,11 +154,24 @@ __global__ void __launch_bounds__(THREADS, BwdShape<T, VPT, THREADS>::BLOCKS)
       const int c = t + i * tpr;
       if (live && c < a.nchunks) {
         Chunk<T> wv;
-        hv[i].load(hidden, c0 + c);
-        if constexpr (VPT == 1)
-          if (dhidden) dh[0].load(dhidden, c0 + c);
         wv.load_cached(a.weight, c);
-        sum_all<T, NR>(in, a.nranks, c0 + c, gr[i]);
+        if constexpr (STAGED > 0) {
+          fetch(0).get(gr[0]);
+#pragma unroll
+          for (int r = 1; r < NR; ++r) {
+            float f[kChunk];
+            fetch(r).get(f);
+#pragma unroll
+            for (int j = 0; j < kChunk; ++j) gr[0][j] += f[j];
+          }
+          hv[0] = fetch(NR);
+          dh[0] = fetch(NR + 1);
+        } else {
+          hv[i].load(hidden, c0 + c);
+          if constexpr (VPT == 1)
+            if (dhidden) dh[0].load(dhidden, c0 + c);
+          sum_all<T, NR>(in, a.nranks, c0 + c, gr[i]);
+        }
         float w[kChunk], xh[kChunk], d[kChunk];
         hv[i].get(xh);
         wv.get(w);
@@ -147,6 +201,7 @@ __global__ void __launch_bounds__(THREADS, BwdShape<T, VPT, THREADS>::BLOCKS)
         }
       }
     }
+    if constexpr (STAGED > 0) stage(ahead);  // (its operands are in registers)
     along = row_sum2(along, tpr, slot, red, turn);
     along.x *= inv_cols;
     along.y *= inv_cols;
@@ -215,7 +270,7 @@ __global__ void __launch_bounds__(1024) k_layernorm_dweight(const float* partial
 
 template <typename T, int NR, int VPT, int THREADS>
 cudaError_t bwd_go(const LayerNormBwdArgs& a, int groups, int* parts, cudaStream_t s) {
-  using S = BwdShape<T, VPT, THREADS>;
+  using S = BwdShape<T, NR, VPT, THREADS>;
   // (as many blocks as stay on the device, each with at most its share of the rows)
   const int rpb = THREADS >> a.tpr_log2;
   int64_t most = sm_count() * S::BLOCKS < kNormMaxParts ? sm_count() * S::BLOCKS : kNormMaxParts;
