@@ -20,7 +20,7 @@
 // Measured, from a graph: 8192 x 4096 fp16 on 8 ranks, 8 copies, 246 us (6.8 TB/s, the
 // copy rate); fp32 on 8 ranks, one copy, 213. Few ranks' rows are bound by
 // instructions (3.2 a cycle of 4 are issued): bf16 on 2 ranks 57 us (5.8 TB/s), to 8
-// bits 66; on one 52; 4096 x 16384 on one 111 (4.8 TB/s).
+// bits 66; on one 52; 2048 x 16384 on one 56 (4.8 TB/s), 3111 x 10784 59.
 
 #include "internal.h"
 #include "rows.h"
@@ -34,7 +34,7 @@ struct LayerNormArgs {
   int32_t nranks;
   int32_t cols, nchunks, nblocks;  // nblocks: scales per row
   int32_t tpr_log2;
-  int32_t ahead;  // rows on the device at a time
+  int32_t ahead;  // how many rows ahead one is brought to L2
   float eps;
   const void* weight;
   const void* bias;
@@ -52,11 +52,11 @@ __device__ __forceinline__ int warp_columns(int w, int tpr, int nchunks, int vpt
   return n * kChunk;
 }
 
-// Rows of up to 4096 columns have one chunk a thread, up to 8192 two; wider ones have 1024 threads and two or four.
+// Rows of up to 4096 columns have one chunk a thread, wider ones two to four (norm_shape has the rule).
 // AHEAD: few ranks' rows are loaded a row ahead, by blocks that stay and walk the rows.
 template <typename T, int NR, int VPT, int THREADS>
 struct NormShape {
-  static constexpr bool AHEAD = NR > 0 && VPT * (NR + 1) * sizeof(T) <= (VPT == 1 ? 8 : 12);
+  static constexpr bool AHEAD = NR > 0 && VPT < 3 && VPT * (NR + 1) * sizeof(T) <= (VPT == 1 ? 8 : 12);
   static constexpr int BLOCKS = THREADS == 1024 ? 1 : VPT == 1 && NR > 0 && sizeof(T) == 2 ? 3 : 2;
 };
 
@@ -242,6 +242,7 @@ cudaError_t norm_go(LayerNormArgs& a, bool fp8, int ngroups, cudaStream_t s) {
   int64_t most = S::AHEAD ? sm_count() * S::BLOCKS * (THREADS / threads) / ngroups : 1 << 30;
   if (most < 1) most = 1;
   const dim3 grid(static_cast<unsigned>(blocks < most ? blocks : most), ngroups);
+  // (blocks of 256 threads are twice as many; twice as far ahead, 4161 x 4608 fp32 on four ranks took 119 us, not 108)
   a.ahead = sm_count() * S::BLOCKS * rpb;
   if (fp8) k_allreduce_layernorm<T, NR, VPT, THREADS, true><<<grid, threads, 0, s>>>(a);
   else k_allreduce_layernorm<T, NR, VPT, THREADS, false><<<grid, threads, 0, s>>>(a);
@@ -258,10 +259,36 @@ cudaError_t norm_shape(LayerNormArgs& a, bool fp8, int ngroups, cudaStream_t s) 
   const int threads = pairs ? (a.nchunks + 1) / 2 : a.nchunks;
   a.tpr_log2 = 5;
   while (a.tpr_log2 < 9 && (1 << a.tpr_log2) < threads) ++a.tpr_log2;
-  if (a.nchunks <= 512 && !pairs)
+  if (pairs) return with_ranks<1, 2>(a.nranks, [&](auto n) { return norm_go<T, n.value, 2, 512>(a, fp8, ngroups, s); });
+  if (a.nchunks <= 512)
     return with_ranks<1, 2, 3, 4, 8>(a.nranks, [&](auto n) { return norm_go<T, n.value, 1, 512>(a, fp8, ngroups, s); });
+  // Wide rows: three chunks a thread where two would leave a quarter of the threads idle (tpr a power of two), four in place
+  // of 1024 threads, so that two to four rows are on an SM instead of one or two. One and three ranks, bf16, some 268 MB:
+  // 4608 columns 73.9 -> 57.2 and 74.7 -> 52.8 us, 10784 77.3 -> 59.2 and 76.0 -> 58.6, 16384 60.5 -> 56.1 and 62.2 -> 61.1;
+  // fp32, two ranks, 9216 186 -> 105. Not taken where it costs: eight ranks' 4608 columns (54.6 -> 57.5), 8192 columns with
+  // four chunks (two ranks 50.2 -> 57.8); other numbers of ranks, whose loop over them takes too many registers (fp32, 3669 x
+  // 6096: 140 -> 154), and 6096 columns of fp32 of two (102 -> 106); few rows, which wait longer: a row an SM (40 x 13152 to
+  // 8 bits, three ranks 6.8 -> 7.4; but fp32, three ranks 12.1 -> 9.5), of one rank, which are loaded ahead, eight (700 x
+  // 13152 to 8 bits 23.5 -> 25.5).
+  const bool few = a.nranks == 1 ? a.rows <= 8 * sm_count() : sizeof(T) == 2 && a.rows <= sm_count();
+  if ((a.nranks <= 4 || a.nranks == 8) && !few) {
+    if ((a.nchunks <= 768 && a.nranks < 8 && (sizeof(T) == 2 || a.nranks != 2)) || (a.nchunks > 1024 && a.nchunks <= 2048)) {
+      a.tpr_log2 = a.nchunks <= 768 ? 8 : 9;
+      auto go = [&](auto n) {
+        return a.nchunks <= 1536 ? norm_go<T, n.value, 3, 512>(a, fp8, ngroups, s)
+                                 : norm_go<T, n.value, 4, 512>(a, fp8, ngroups, s);
+      };
+      switch (a.nranks) {
+        case 1: return go(std::integral_constant<int, 1>());
+        case 2: return go(std::integral_constant<int, 2>());
+        case 3: return go(std::integral_constant<int, 3>());
+        case 4: return go(std::integral_constant<int, 4>());
+        default: return go(std::integral_constant<int, 8>());
+      }
+    }
+  }
   if (a.nchunks <= 1024)
-    return with_ranks<1, 2, 8>(a.nranks, [&](auto n) { return norm_go<T, n.value, 2, 512>(a, fp8, ngroups, s); });
+    return with_ranks<1, 2, 3, 4, 8>(a.nranks, [&](auto n) { return norm_go<T, n.value, 2, 512>(a, fp8, ngroups, s); });
   a.tpr_log2 = 10;
   if (a.nchunks <= 2048)
     return with_ranks<1>(a.nranks, [&](auto n) { return norm_go<T, n.value, 2, 1024>(a, fp8, ngroups, s); });

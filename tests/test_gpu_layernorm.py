@@ -70,6 +70,14 @@ def test_norm_matches_the_oracle(dtype, n, rows, cols, fp8):
             within(f64(nrm[c]), y, np.abs(y) * U[dtype] * 1.01 + yb + TINY[dtype], "normed")
 
 
+@pytest.mark.parametrize("dtype,fp8", [(torch.bfloat16, False), (torch.float16, True), (torch.float32, False)])
+@pytest.mark.parametrize("n,rows,cols", [(1, 1230, 4112), (1, 1230, 8208), (1, 1230, 12304), (2, 170, 6096), (2, 170, 12304),
+                                         (3, 170, 6144), (3, 170, 16384), (4, 170, 10784), (8, 170, 9216), (8, 170, 16384)])
+def test_many_wide_rows_match_the_oracle(dtype, fp8, n, rows, cols):
+    """More rows than the device has multiprocessors (eight times as many, on one rank): three and four chunks a thread."""
+    test_norm_matches_the_oracle(dtype, n, rows, cols, fp8)
+
+
 @pytest.mark.parametrize("cols", [256, 4096, 5008])
 def test_a_mean_far_from_zero(cols):
     """Rows whose mean is some 3000 times their deviation. h is exact here (multiples of 2^-11 near 4) and so are the sums of
@@ -201,6 +209,13 @@ def test_backward_matches_the_oracle(dtype, n, rows, cols):
     coco.coco_allreduce_layernorm_backward(*args, None, ws)
     torch.cuda.synchronize()
     assert torch.equal(dw, first[1]) and bool((db == 5.0).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,rows,cols", [(1, 3100, 1024), (2, 640, 4000), (3, 1000, 2064), (4, 5000, 272), (8, 650, 4096)])
+def test_backward_of_several_rows_a_block_matches_the_oracle(dtype, n, rows, cols):
+    """More rows than the device holds at a time, the last ones for some blocks only."""
+    test_backward_matches_the_oracle(dtype, n, rows, cols)
 
 
 def test_backward_of_groups_joins_their_rows():
