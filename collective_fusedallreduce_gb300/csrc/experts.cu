@@ -320,8 +320,8 @@ struct CombineArgs {
 };
 
 // How many chunks a thread takes and how many choices at a time, so that some loads are under way. MANY: more than two
-// choices (8 of 2048 columns, one rank: 114 us, 5.9 TB/s; 132 with a choice at a time, 130 with two of two chunks). Eight
-// ranks' rows of two experts, 8192 x 4096: 175 us, at the copy rate; their own sums 262 (91 %).
+// choices (8 of 2048 columns, one rank: 116 us, 5.8 TB/s; 132 with a choice at a time, 130 with two of two chunks). Eight
+// ranks' rows of two experts, 8192 x 4096: 175 us, at the copy rate; their own sums 264 (90 %).
 template <int NR, bool MANY>
 struct CombineShape {
   static constexpr int ITEMS = NR == 1 && !MANY ? 2 : 1;

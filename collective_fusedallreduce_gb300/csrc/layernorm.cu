@@ -20,7 +20,7 @@
 // Measured, from a graph: 8192 x 4096 fp16 on 8 ranks, 8 copies, 246 us (6.8 TB/s, the
 // copy rate); fp32 on 8 ranks, one copy, 213. Few ranks' rows are bound by
 // instructions (3.2 a cycle of 4 are issued): bf16 on 2 ranks 57 us (5.8 TB/s), to 8
-// bits 66; on one 52; 2048 x 16384 on one 56 (4.8 TB/s), 3111 x 10784 59.
+// bits 66; on one 52; 4096 x 16384 on one 98 (5.5 TB/s), 3111 x 10784 bf16 59.
 
 #include "internal.h"
 #include "rows.h"

@@ -10,10 +10,10 @@
 // which k_layernorm_dweight adds in block order: no atomics, so repeated calls
 // give the same bits.
 //
-// Measured, from a graph: 8192 x 4096 fp16 on 8 ranks 119.5 us (6.2 TB/s; some 6 of
-// them the second kernel, which is placed early), 777 x 8192 bf16 on 2 26.0 (two or three
+// Measured, from a graph: 8192 x 4096 fp16 on 8 ranks 118 us (6.3 TB/s; some 6 of
+// them the second kernel, which is placed early), 777 x 8192 bf16 on 2 26.3 (two or three
 // rows a block, whose waits follow one another), 8192 x 4096 bf16 on 3 67.4, 4096 x 16384
-// on one 119, 2048 x 32768 266 (db through L2). dw and db in registers instead of shared
+// on one 117, 2048 x 32768 265 (db through L2). dw and db in registers instead of shared
 // memory do not fit two blocks an SM (204 us for the first with one).
 
 #include <atomic>
@@ -72,7 +72,7 @@ struct BwdShape {
   static constexpr int PER = FAR ? 2 : 4;
   // Operands (the ranks', hidden, dhidden) whose next row is copied to shared memory while this one is summed and stored:
   // all, where a thread has one 16-bit chunk of each and their number is known (8192 x 4096 on two ranks 70.7 -> 63.3 us, on
-  // three 76 -> 67.4, on four 81 -> 75.7, on eight 121.4 -> 119.5). Two chunks a thread lost by it (8192 x 8192 on one rank
+  // three 76 -> 67.4, on four 81 -> 75.7, on eight 121.4 -> 118). Two chunks a thread lost by it (8192 x 8192 on one rank
   // 114 -> 118), fp32 more (one rank 101 -> 140).
   static constexpr int STAGED = sizeof(T) == 2 && VPT == 1 && NR > 0 ? NR + 2 : 0;
   static constexpr int SMEM = (PER * VPT + STAGED) * THREADS * 16;

@@ -237,8 +237,8 @@ __device__ __forceinline__ void sum_all(const void* const* in, int nranks, int64
 }
 
 // A chunk's eight values as four pairs, for instructions that take two values, each rounded as by itself. Half as many
-// instructions, for twice as many registers in pairs: what they cost was won back where a thread keeps little else (two
-// ranks' rows of two experts combined 74 -> 65 us), and not in the norms (two ranks 69 -> 83 us).
+// instructions, for twice as many registers in pairs: for the experts' rows, where a thread keeps little else, and not for
+// the norms (two ranks to 8 bits 69 -> 83 us). A pair's product and the sum after it are contracted by the compiler.
 struct Vec8 {
   uint64_t p[4];
 };
