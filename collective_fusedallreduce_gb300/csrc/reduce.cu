@@ -84,9 +84,10 @@ struct V16<__nv_bfloat16> {
   }
 };
 
+// (Not the non-coherent path, which is for memory that nothing writes while the kernel runs: outputs may take inputs' places.)
 __device__ __forceinline__ uint4 ld_stream(const void* p) {
   uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
   return r;
 }

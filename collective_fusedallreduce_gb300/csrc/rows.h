@@ -21,9 +21,11 @@ constexpr float kAmaxFloor = 0x1p-100f;  // smallest block maximum a scale is ma
 
 // ------------------------------------------------------------------ chunks
 
+// (Not the non-coherent path, which is for memory that nothing writes while the kernel runs: outputs take inputs' places here,
+// and a kernel placed early is on the device while the one ahead still stores what it will read. The times are the same.)
 __device__ __forceinline__ uint4 ld_stream(const void* p) {
   uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
   return r;
 }
