@@ -242,18 +242,15 @@ __device__ __forceinline__ double squares_full(const ClipArgs& a, int64_t b, uin
         for (int j = 0; j < N; ++j) f[j] = -0.0f;  // (added to anything, it leaves that as it is)
 #pragma unroll 1
         for (int r0 = 0; r0 < a.nranks; r0 += 4) {
-          Part<T, N> now[4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) now[r] = next[r];
-          const bool same = r0 + 4 < a.nranks;
-          if (same || i + 1 < UNITS) fetch(same ? i : i + 1, same ? r0 + 4 : 0);
 #pragma unroll
           for (int r = 0; r < 4; ++r)
             if (r0 + r < a.nranks) {
-              now[r].get(g);
+              next[r].get(g);
 #pragma unroll
               for (int j = 0; j < N; ++j) f[j] += g[j];
             }
+          const bool same = r0 + 4 < a.nranks;
+          if (same || i + 1 < UNITS) fetch(same ? i : i + 1, same ? r0 + 4 : 0);
         }
         finish(f, i);
       }
@@ -294,7 +291,7 @@ __device__ __forceinline__ double squares_end(const ClipArgs& a, int64_t b, uint
 }
 
 // Two blocks an SM with CLIP_SUM, whose 128 registers hold a bucket's loads of eight ranks (three blocks: BERT-large's 1086
-// -> 1188 us), and four with any number of ranks (19 million values of five, fp32 131 -> 88 us, fp16 108 -> 65). Warps take buckets round-robin (those of every rank with CLIP_LOCAL), the next one's entries under way.
+// -> 1188 us), and four with any number of ranks (19 million values of five, fp16 78 us with three and 50 with four, fp32 127 and 85). Warps take buckets round-robin (those of every rank with CLIP_LOCAL), the next one's entries under way.
 // With CLIP_SUM the ranks' tensors are added in rank order, scaled by alpha, rounded to U and stored to out's rank 0, and
 // it is those values' norm. Where the two tables' tensors do not have a bucket in common, nothing is written and the norm
 // is NaN.
