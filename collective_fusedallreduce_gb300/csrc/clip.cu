@@ -77,6 +77,7 @@ struct Part {  // 8 values of 16 bits
   __device__ __forceinline__ void load(const void* base, int i) { c.load(base, i); }
   __device__ __forceinline__ void get(float (&f)[8]) const { c.get(f); }
   __device__ __forceinline__ void put(const float (&f)[8]) { c.put(f); }
+  __device__ __forceinline__ uint32_t bits() const { return (c.v.x | c.v.y | c.v.z | c.v.w) & 0x7fff7fffu; }  // 0: all zeros
   __device__ __forceinline__ void store(void* base, int i) const { static_cast<uint4*>(base)[i] = c.v; }
   __device__ __forceinline__ void store_stream(void* base, int i) const { c.store(base, i); }
 };
@@ -90,6 +91,7 @@ struct Part<float, 4> {
   __device__ __forceinline__ void put(const float (&f)[4]) {
     v = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
   }
+  __device__ __forceinline__ uint32_t bits() const { return (v.x | v.y | v.z | v.w) & 0x7fffffffu; }
   __device__ __forceinline__ void store(void* base, int i) const { static_cast<uint4*>(base)[i] = v; }
   __device__ __forceinline__ void store_stream(void* base, int i) const { __stcs(static_cast<uint4*>(base) + i, v); }
 };
@@ -111,6 +113,7 @@ struct Part<T, 4> {  // 4 values of 16 bits
     const float g[8] = {f[0], f[1], f[2], f[3], 0.0f, 0.0f, 0.0f, 0.0f};
     c.put(g);
   }
+  __device__ __forceinline__ uint32_t bits() const { return (c.v.x | c.v.y) & 0x7fff7fffu; }
   __device__ __forceinline__ void store(void* base, int i) const { static_cast<uint2*>(base)[i] = make_uint2(c.v.x, c.v.y); }
   __device__ __forceinline__ void store_stream(void* base, int i) const {
     __stcs(static_cast<uint2*>(base) + i, make_uint2(c.v.x, c.v.y));
@@ -141,10 +144,12 @@ __device__ __forceinline__ float add_squares(const float (&f)[N], float s) {
 }
 
 // The squares' sum of a lane's part of a bucket, s in fp32; taken again in fp64 where that has left fp32's range (past
-// its largest number, or so low that squares were lost).
+// its largest number, or so low that squares were lost). `bits` is 0 where the values are all zeros, whose sum is right:
+// gradients have them (words that a batch has not, experts without tokens), and walking them again took three to five times
+// as long as the pass itself.
 template <typename T, int N>
-__device__ __forceinline__ double squares(const Bucket& b, float s) {
-  if (s >= 0x1p-80f && s <= FLT_MAX) return s;
+__device__ __forceinline__ double squares(const Bucket& b, float s, uint32_t bits) {
+  if ((s >= 0x1p-80f && s <= FLT_MAX) || bits == 0) return s;
   double d = 0.0;
 #pragma unroll 1
   for (int i = threadIdx.x & 31; i * N < b.len; i += 32) {
@@ -174,6 +179,7 @@ __device__ __forceinline__ double squares_full(const ClipArgs& a, int64_t b, uin
   constexpr int N = unit_of<T, U>(), UNITS = 1024 / N / 32;
   const int lane = threadIdx.x & 31;
   float s = 0.0f;
+  uint32_t bits = 0;
   if constexpr (MODE != CLIP_SUM) {
     const Bucket k = bucket_of<T>(words, 0);
     Part<T, N> v[UNITS];
@@ -184,8 +190,9 @@ __device__ __forceinline__ double squares_full(const ClipArgs& a, int64_t b, uin
       float f[N];
       v[i].get(f);
       s = add_squares(f, s);
+      bits |= v[i].bits();
     }
-    return squares<T, N>(k, s);
+    return squares<T, N>(k, s, bits);
   } else {
     const Bucket to = bucket_of<U>(out_words, 0);
     auto finish = [&](float (&f)[N], int i) {
@@ -195,6 +202,7 @@ __device__ __forceinline__ double squares_full(const ClipArgs& a, int64_t b, uin
       o.put(f);
       o.store(to.base, lane + 32 * i);  // (not a streaming store: it is read again)
       s = add_squares(f, s);
+      bits |= o.bits();
     };
     // Loads do not pass a store, so those of the next units are issued ahead of it: 32 a thread where the ranks are known
     // (BERT-large's 1095 us with 16, 1079 with 32; 75.6 million bf16 of three ranks to fp32 131 and 122), else the next four
@@ -255,7 +263,7 @@ __device__ __forceinline__ double squares_full(const ClipArgs& a, int64_t b, uin
         finish(f, i);
       }
     }
-    return squares<U, N>(to, s);
+    return squares<U, N>(to, s, bits);
   }
 }
 
@@ -266,6 +274,7 @@ __device__ __forceinline__ double squares_end(const ClipArgs& a, int64_t b, uint
   const Bucket k = bucket_of<T>(words, 0), to = bucket_of<U>(out_words, 0);
   const int rounds = (k.len + 32 * N - 1) / (32 * N);
   float s = 0.0f;
+  uint32_t bits = 0;
 #pragma unroll 1
   for (int r0 = 0; r0 < rounds; ++r0) {
     const int i = (threadIdx.x & 31) + 32 * r0;
@@ -285,9 +294,11 @@ __device__ __forceinline__ double squares_end(const ClipArgs& a, int64_t b, uint
       store_end<U>(to, i, f);
     }
     s = add_squares(f, s);
+#pragma unroll
+    for (int j = 0; j < N; ++j) bits |= __float_as_uint(f[j]) << 1;
   }
-  if constexpr (MODE == CLIP_SUM) return squares<U, N>(to, s);
-  else return squares<T, N>(k, s);
+  if constexpr (MODE == CLIP_SUM) return squares<U, N>(to, s, bits);
+  else return squares<T, N>(k, s, bits);
 }
 
 // Two blocks an SM with CLIP_SUM, whose 128 registers hold a bucket's loads of eight ranks (three blocks: BERT-large's 1086

@@ -1,0 +1,74 @@
+"""Clipping of gradients whose values are out of the ordinary, through the C-ABI: exact zeros, which are many in a real
+model's gradients and may not cost more than other numbers."""
+
+import pytest
+import torch
+
+from collective_fusedallreduce_gb300 import coco
+from test_gpu_clip import INF, Guarded, like, space
+from test_gpu_llm_norm import DEV
+
+pytestmark = pytest.mark.gpu
+TYPES = [torch.bfloat16, torch.float16, torch.float32]
+
+
+def graph_time(call):
+    """The shortest of some replays, in ms."""
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(4):
+            call()
+    times = []
+    for _ in range(8):
+        start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        start.record()
+        graph.replay()
+        end.record()
+        torch.cuda.synchronize()
+        times.append(start.elapsed_time(end))
+    return min(times)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("summed", [False, True])
+def test_zeros_take_no_longer_than_other_numbers(dtype, summed):
+    """The norm alone of 32 million values a rank, in and out of place: the same bytes whatever they are. (A walk over them
+    that only lost squares need takes three to five times as long: half as long again is far from either.)"""
+    ranks = 2 if summed else 1
+    g = Guarded([[torch.randn(32 << 20, device=DEV).to(dtype), torch.randn(1021, device=DEV).to(dtype)] for _ in range(ranks)])
+    out = like(g.tensors, 1, torch.float32) if summed else None
+    ws, norm = space()
+    if summed:
+        call = lambda: coco.coco_scattered_allreduce_clip(g.plan, 0.5, INF, out.plan, norm, ws)  # noqa: E731
+    else:
+        call = lambda: coco.coco_scattered_clip(g.plan, coco.LOCAL, INF, None, norm, ws)  # noqa: E731
+    dense = graph_time(call)
+    assert float(norm) > 1000
+    for row in g.tensors:
+        for t in row:
+            t.zero_()
+            t[::3] *= -1.0  # (zeros of either sign)
+    zeros = graph_time(call)
+    assert float(norm) == 0.0
+    assert zeros <= 1.5 * dense, (zeros, dense)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_one_small_value_among_zeros_is_seen(dtype):
+    """A value whose square fp32 loses, in a bucket of zeros and in a tensor's last one: the sum is taken in fp64."""
+    x = 2.0 ** -90
+    for at in (0, 517, 1023, 2047, 2050):
+        for sign in (1.0, -1.0):
+            g = Guarded([[torch.zeros(2051, dtype=dtype)]])
+            g.tensors[0][0][at] = sign * x
+            ws, norm = space()
+            coco.coco_scattered_clip(g.plan, coco.LOCAL, INF, None, norm, ws)
+            torch.cuda.synchronize()
+            assert float(norm) == x, (at, sign)
+            h = Guarded([[torch.zeros(2051, dtype=dtype)] for _ in range(3)])
+            h.tensors[1][0][at] = sign * x
+            coco.coco_scattered_allreduce_clip(h.plan, 1.0, INF, None, norm, ws)
+            torch.cuda.synchronize()
+            assert float(norm) == x and float(h.tensors[2][0][at]) == sign * x
