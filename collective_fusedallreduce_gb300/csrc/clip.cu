@@ -17,6 +17,7 @@
 // ends are half; 153 million fp32 ones 293 us.
 
 #include <float.h>
+#include <math.h>
 
 #include <type_traits>
 
@@ -302,10 +303,10 @@ __device__ __forceinline__ double squares_end(const ClipArgs& a, int64_t b, uint
 }
 
 // Two blocks an SM with CLIP_SUM, whose 128 registers hold a bucket's loads of eight ranks (three blocks: BERT-large's 1086
-// -> 1188 us), and four with any number of ranks (19 million values of five, fp16 78 us with three and 50 with four, fp32 127 and 85). Warps take buckets round-robin (those of every rank with CLIP_LOCAL), the next one's entries under way.
-// With CLIP_SUM the ranks' tensors are added in rank order, scaled by alpha, rounded to U and stored to out's rank 0, and
-// it is those values' norm. Where the two tables' tensors do not have a bucket in common, nothing is written and the norm
-// is NaN.
+// -> 1188 us), and four with any number of ranks (19 million values of five, fp16 78 us with three and 50 with four, fp32 127
+// and 85). Warps take buckets round-robin (those of every rank with CLIP_LOCAL), the next one's entries under way. With
+// CLIP_SUM the ranks' tensors are added in rank order, scaled by alpha, rounded to U and stored to out's rank 0, and it is
+// those values' norm. Where the two tables' tensors do not have a bucket in common, nothing is written and the norm is NaN.
 template <typename T, typename U, int MODE, int NR>
 __global__ void __launch_bounds__(kThreads, MODE == CLIP_SUM && NR > 0 ? 2 : 4)
     k_clip_squares(const __grid_constant__ ClipArgs a) {
@@ -395,7 +396,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_clip_scale(const __grid_constan
   if (threadIdx.x == 0) {
     const double norm = sqrt(total);
     if (blockIdx.x == 0) *a.norm = static_cast<float>(norm);
-    shared_factor = norm <= static_cast<double>(a.max_norm) ? 1.0f : static_cast<float>(a.max_norm / norm);
+    const bool stay = a.max_norm == INFINITY || norm <= static_cast<double>(a.max_norm);  // (no limit: a NaN's too)
+    shared_factor = stay ? 1.0f : static_cast<float>(a.max_norm / norm);
   }
   __syncthreads();
   const float factor = shared_factor;

@@ -656,7 +656,8 @@ size_t coco_allreduce_layernorm_backward_bytes(int64_t rows, int64_t cols);
  *   plan      the tensors' plan. layout COCO_LOCAL: the ranks' tensors are parts of one gradient (a tensor-parallel
  *             model's slices), all of them enter the norm and each is scaled; COCO_REPLICATED: they are copies of one, of
  *             which rank 0's is read. Other layouts: COCO_ERR_LAYOUT.
- *   max_norm  >= 0, else COCO_ERR_VALUE; INFINITY only takes the norm (in place, nothing is written).
+ *   max_norm  >= 0, else COCO_ERR_VALUE; INFINITY only takes the norm: values stay what they are whatever it is, and in
+ *             place nothing is written.
  *   out       the plan of the tensors that receive the result, of the same sizes in the same order, in any type (fp32
  *             gradients for the optimizer from 16-bit ones), or NULL: in place. COCO_LOCAL: as many ranks as `plan`;
  *             COCO_REPLICATED: each of its ranks receives a copy. `out` may be `plan` itself; its tensors may otherwise
@@ -667,8 +668,9 @@ size_t coco_allreduce_layernorm_backward_bytes(int64_t rows, int64_t cols);
  *             before and after do not matter. Calls that may run at the same time need one each.
  * Squares are summed in fp32 per lane and bucket (fp64 where they leave its range), beyond that in fp64, in a fixed order:
  * repeated calls on one device give the same bits. The product is rounded once to out's type. In place with a factor of
- * 1, nothing is written. A norm that is NaN makes every value NaN; an infinite one makes finite values zero and
- * infinities NaN.
+ * 1, nothing is written. With a finite max_norm, a norm that is NaN makes every value NaN, and an infinite one (of an
+ * infinite value) makes finite values zero and infinities NaN. Where only the norm's fp32 form overflows, INFINITY is
+ * reported and values are scaled by the norm as it is.
  */
 coco_status coco_scattered_clip(const coco_scattered_plan* plan, int32_t layout, float max_norm,
                                 const coco_scattered_plan* out, float* norm, void* workspace, size_t workspace_bytes,

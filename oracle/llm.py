@@ -202,7 +202,7 @@ def allreduce_layernorm_backward(dnormed, dhidden, h, mean, rstd, weight):
 
 
 def clip(tensors, max_norm):
-    """(the tensors scaled so that their norm is at most max_norm, the norm before)."""
+    """(the tensors scaled so that their norm is at most max_norm, the norm before); an infinite max_norm scales nothing."""
     norm = np.sqrt(sum(np.sum(np.square(t)) for t in tensors))
-    factor = 1.0 if norm <= max_norm else max_norm / norm
+    factor = 1.0 if norm <= max_norm or np.isinf(max_norm) else max_norm / norm
     return [t * factor for t in tensors], norm

@@ -1,5 +1,5 @@
 """Clipping of gradients whose values are out of the ordinary, through the C-ABI: exact zeros, which are many in a real
-model's gradients and may not cost more than other numbers."""
+model's gradients and may not cost more than other numbers, and values that are no numbers where only the norm is asked for."""
 
 import pytest
 import torch
@@ -72,3 +72,40 @@ def test_one_small_value_among_zeros_is_seen(dtype):
             coco.coco_scattered_allreduce_clip(h.plan, 1.0, INF, None, norm, ws)
             torch.cuda.synchronize()
             assert float(norm) == x and float(h.tensors[2][0][at]) == sign * x
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("bad", [float("nan"), INF, -INF])
+def test_without_a_limit_values_stay_what_they_are(dtype, bad):
+    """INFINITY asks for the norm alone (to skip a step whose gradients are no numbers, say): nothing is scaled."""
+    def filled(n):
+        rows = [[torch.randn(5003, device=DEV).to(dtype), torch.randn(9, device=DEV).to(dtype)] for _ in range(n)]
+        rows[0][0][2050] = bad
+        return rows
+
+    def same(x, y):
+        return torch.equal(x.isnan(), y.isnan()) and torch.equal(x[~x.isnan()], y[~y.isnan()])
+
+    def seen(norm):
+        return bool(torch.isnan(norm)) if bad != bad else float(norm) == INF
+
+    rows, (ws, norm) = filled(2), space()
+    for layout, ranks in ((coco.LOCAL, 2), (coco.REPLICATED, 1)):
+        g, out = Guarded(rows[:ranks]), like(rows, ranks, torch.float32)
+        before = [[t.clone() for t in row] for row in g.tensors]
+        coco.coco_scattered_clip(g.plan, layout, INF, None, norm.zero_(), ws)
+        torch.cuda.synchronize()
+        assert seen(norm)
+        coco.coco_scattered_clip(g.plan, layout, INF, out.plan, norm.zero_(), ws)
+        torch.cuda.synchronize()
+        assert seen(norm)
+        g.check(), out.check()
+        for b, t, o in zip(before, g.tensors, out.tensors):
+            assert all(same(x, y) and same(x.float(), z) for x, y, z in zip(b, t, o))
+    a, b = Guarded(rows), Guarded(rows)
+    coco.coco_scattered_allreduce(a.plan, 0.5)
+    coco.coco_scattered_allreduce_clip(b.plan, 0.5, INF, None, norm.zero_(), ws)
+    torch.cuda.synchronize()
+    assert seen(norm)
+    for x, y in zip(a.tensors, b.tensors):
+        assert all(same(s, t) for s, t in zip(x, y))
