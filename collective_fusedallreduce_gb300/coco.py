@@ -524,6 +524,22 @@ def _pointer(t, dtype, numel, what):
     return None if t is None else _vector(t, dtype, numel, what)
 
 
+def _per_choice(t, dtype, tokens, rows, groups, what):
+    """The address of a tensor with a value for every token's choices, or None: [groups, tokens, choices] in this order, of
+    which neighbours may be one dimension. The number of its elements does not tell it from another order."""
+    if t is None:
+        return None
+    p = _vector(t, dtype, rows * groups, what)
+    shape = t.shape
+    if len(shape) != 2 or shape[1] * tokens != rows:
+        n, runs = 1, (1, rows // tokens if tokens else 0, rows, rows * groups)
+        for d in reversed(shape):
+            n *= d
+            if n not in runs and t.numel():
+                raise CocoError(2, what)
+    return p
+
+
 def coco_expert_sort(expert_of, experts, row_of_choice, choice_of_row, offsets, stream=None):
     """The rows of a mixture of experts, sorted by expert. ``expert_of`` [tokens, choices] or [groups, tokens, choices]
     (int32 or int64; a number outside [0, experts) has no row) gives ``row_of_choice`` (int32, the same shape, -1 for
@@ -540,7 +556,7 @@ def coco_expert_sort(expert_of, experts, row_of_choice, choice_of_row, offsets, 
     if groups < 1 or lines % groups:
         raise CocoError(2, what)
     n = expert_of.numel()
-    row = _vector(row_of_choice, torch.int32, n, what)
+    row = _per_choice(row_of_choice, torch.int32, shape[-2], n // groups, groups, what)
     choice = _pointer(choice_of_row, torch.int32, n, what)
     off = _vector(offsets, torch.int32, lines * (experts + 1), what)
     _check_here(what, expert_of, row_of_choice, choice_of_row, offsets)
@@ -561,7 +577,7 @@ def coco_expert_dispatch(x, x_scales, row_of_choice, rows, row_scales, stream=No
     as they were."""
     what = "coco_expert_dispatch"
     sx, sr = _row_scales(x_scales, x, what), _row_scales(row_scales, rows, what)
-    row = _vector(row_of_choice, torch.int32, rows.shape[0] * rows.ngroups, what)
+    row = _per_choice(row_of_choice, torch.int32, x.shape[0], rows.shape[0], rows.ngroups, what)
     xp, rp = x.packed(what), rows.packed(what)
     _check_here(what, x, rows, row_of_choice, x_scales, row_scales)
     _check(_lib.coco_expert_dispatch(xp, sx, row, rp, sr, _stream(stream)), what)
@@ -572,8 +588,9 @@ def coco_expert_combine(rows, row_of_choice, gates, residual, out, stream=None):
     None), or their AllReduce with the residual (``out`` REPLICATED). ``gates``: fp32, the shape of ``row_of_choice``, or
     None for ones, which is the dispatch's gradient."""
     what = "coco_expert_combine"
-    n = rows.shape[0] * rows.ngroups
-    row, w = _vector(row_of_choice, torch.int32, n, what), _pointer(gates, torch.float32, n, what)
+    tokens, n, groups = out.shape[0], rows.shape[0], rows.ngroups
+    row = _per_choice(row_of_choice, torch.int32, tokens, n, groups, what)
+    w = _per_choice(gates, torch.float32, tokens, n, groups, what)
     rp, res, o = rows.packed(what), _packed(residual, what), out.packed(what)
     _check_here(what, rows, residual, out, row_of_choice, gates)
     _check(_lib.coco_expert_combine(rp, row, w, res, o, _stream(stream)), what)
@@ -583,9 +600,10 @@ def coco_expert_combine_backward(dout, rows, row_of_choice, gates, drows, dgates
     """The gradient of coco_expert_combine: ``drows`` (REPLICATED: every rank's is the same) and ``dgates`` (fp32, the
     shape of ``row_of_choice``; None with ``rows`` None) for ``dout``, the gradient of the summed output."""
     what = "coco_expert_combine_backward"
-    n = drows.shape[0] * drows.ngroups
-    row, w = _vector(row_of_choice, torch.int32, n, what), _pointer(gates, torch.float32, n, what)
-    dw = _pointer(dgates, torch.float32, n, what)
+    tokens, n, groups = dout.shape[0], drows.shape[0], drows.ngroups
+    row = _per_choice(row_of_choice, torch.int32, tokens, n, groups, what)
+    w = _per_choice(gates, torch.float32, tokens, n, groups, what)
+    dw = _per_choice(dgates, torch.float32, tokens, n, groups, what)
     d, rp, o = dout.packed(what), _packed(rows, what), drows.packed(what)
     _check_here(what, dout, rows, drows, row_of_choice, gates, dgates)
     _check(_lib.coco_expert_combine_backward(d, rp, row, w, o, dw, _stream(stream)), what)
