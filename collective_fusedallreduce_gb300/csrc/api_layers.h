@@ -1,5 +1,5 @@
 // Checks shared by the entry points of the operators of a language model's layers
-// (api_llm.cu, api_experts.cu).
+// (api_llm.cu, api_layers.cu).
 #pragma once
 
 #include "api_common.h"

@@ -17,10 +17,12 @@
 //
 // so nothing is lost where a row's mean is large against its spread.
 //
-// Measured, from a graph: 8192 x 4096 fp16 on 8 ranks, 8 copies, 246 us (6.8 TB/s, the
-// copy rate); fp32 on 8 ranks, one copy, 213. Few ranks' rows are bound by
-// instructions (3.2 a cycle of 4 are issued): bf16 on 2 ranks 57 us (5.8 TB/s), to 8
-// bits 66; on one 52; 4096 x 16384 on one 98 (5.5 TB/s), 3111 x 10784 bf16 59.
+// Measured, from a graph: 8192 x 4096 fp16 on 8 ranks, 8 copies, 248 us (6.8 TB/s, the
+// copy rate); fp32 on 8 ranks, one copy, 212. Few ranks' rows are bound by
+// instructions (3.2 a cycle of 4 are issued): bf16 on 2 ranks 58 us (5.8 TB/s), to 8
+// bits 66; on one 52; 4096 x 16384 on one 98 (5.5 TB/s), 3106 x 10784 bf16 59. Far from
+// the bytes' time: 2048 x 32768 bf16 on one rank 152 us (3.5 TB/s), 1024 x 32768 fp32 224
+// (registers spill), 8192 x 4096 bf16 on 5 ranks 136 (3.9 TB/s).
 
 #include "internal.h"
 #include "rows.h"
@@ -52,7 +54,8 @@ __device__ __forceinline__ int warp_columns(int w, int tpr, int nchunks, int vpt
   return n * kChunk;
 }
 
-// Rows of up to 4096 columns have one chunk a thread, wider ones two to four (norm_shape has the rule).
+// Rows of up to 4096 columns have one chunk a thread, many narrow ones of one or two ranks two, wider ones two to four
+// (norm_shape has the rules).
 // AHEAD: few ranks' rows are loaded a row ahead, by blocks that stay and walk the rows.
 template <typename T, int NR, int VPT, int THREADS>
 struct NormShape {

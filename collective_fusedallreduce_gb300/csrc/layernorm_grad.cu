@@ -11,9 +11,10 @@
 // give the same bits.
 //
 // Measured, from a graph: 8192 x 4096 fp16 on 8 ranks 118 us (6.3 TB/s; some 6 of
-// them the second kernel, which is placed early), 777 x 8192 bf16 on 2 26.3 (two or three
+// them the second kernel, which is placed early), 777 x 8192 bf16 on 2 26.1 (two or three
 // rows a block, whose waits follow one another), 8192 x 4096 bf16 on 3 67.4, 4096 x 16384
-// on one 117, 2048 x 32768 265 (db through L2). dw and db in registers instead of shared
+// on one 117, 2048 x 32768 267 (db through L2); fp32, 8192 x 4096, on one 101 (5.3 TB/s),
+// on 4 199 (4.7), on 8 233 (6.3). dw and db in registers instead of shared
 // memory do not fit two blocks an SM (204 us for the first with one).
 
 #include <atomic>

@@ -211,8 +211,9 @@ __device__ __forceinline__ void sum_ranks(const void* const* in, int nranks, int
   }
 }
 
-// The same; any number of ranks (NR 0) goes four at a time, whose loads are all under way before the first addition.
-// (sum_ranks loads one rank alone first: 8192 x 4096 bf16 normed on two ranks took 195 us with it.)
+// The same; any number of ranks (NR 0) goes four at a time, whose loads are all under way before the first addition, where
+// sum_ranks loads one rank alone first. Which is better depends on what the last four hold: 8192 x 4096 bf16 normed on six
+// ranks takes 132 us, and 137 with sum_ranks; on five 134 and 115.
 template <typename T, int NR>
 __device__ __forceinline__ void sum_all(const void* const* in, int nranks, int64_t c, float (&acc)[kChunk]) {
   if constexpr (NR > 0) {
